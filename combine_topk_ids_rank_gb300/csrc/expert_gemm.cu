@@ -33,14 +33,13 @@
 #include "kernels.h"
 #include "ptx.cuh"
 #include "tcgen05.cuh"
+#include "tensor_map.h"
 
 #include "moe_a2a.h"
 
-#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include <cstring>
-#include <mutex>
 
 namespace moe {
 namespace {
@@ -383,45 +382,6 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreads, 1)
     __syncthreads();
     if (tid == 0 && s_failed) atomicOr(p.flags, MOE_DEVICE_FLAG_WAIT_TIMEOUT);
     if (warp == kMmaWarp) tc::tmem_dealloc(taddr, 2 * BN);
-}
-
-// ---- host: tensor maps -------------------------------------------------------
-
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                 const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                 const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encoder() {
-    static EncodeTiled fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
-                                             cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiled>(ptr);
-    });
-    return fn;
-}
-
-// bf16 matrix of `rows` x `cols` (row-major, cols contiguous), boxes of
-// box_rows x 64 with the 128-byte swizzle; rows past the end read as zero.
-bool make_map(CUtensorMap *m, const void *base, long long rows, int cols, int box_rows,
-              bool fp8) {
-    EncodeTiled enc = encoder();
-    if (enc == nullptr) return false;
-    const int esize = fp8 ? 1 : 2;
-    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)cols * esize};
-    const cuuint32_t box[2] = {(cuuint32_t)(kRowBytes / esize), (cuuint32_t)box_rows};
-    const cuuint32_t estr[2] = {1, 1};
-    return enc(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-               const_cast<void *>(base), dims, strides,
-               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int BN, int STAGES, bool FP8, bool GATHER>

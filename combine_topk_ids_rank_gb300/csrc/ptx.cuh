@@ -132,6 +132,17 @@ __device__ __forceinline__ void cp_async_mbar_arrive_noinc(uint64_t *bar) {
                  : "memory");
 }
 
+// Close the group of the cp.async that this thread issued since the last one.
+__device__ __forceinline__ void cp_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// Wait until at most N of this thread's latest groups are still in flight.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Wait until every cp.async this thread issued has completed.
 __device__ __forceinline__ void cp_async_wait_all() {
     asm volatile("cp.async.wait_all;" ::: "memory");

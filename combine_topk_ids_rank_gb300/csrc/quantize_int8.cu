@@ -1,0 +1,144 @@
+// quantize_int8.cu -- activation rows to 8-bit integer codes with one scale
+// per row, the token operand of the 8-bit integer product.
+//
+// Operation, per row x[0..H) (bf16 or fp32):
+//   amax = max_h |x_h|,  scale = max(RN32(amax / 127), 2^-126), 1 if amax = 0,
+//   q_h  = the integer nearest to RN32(x_h / scale), ties to even: |q_h| <= 127.
+// A row that holds a NaN or an infinity has scale NaN and zero codes, so
+// whatever is computed from it is NaN.  With counts, rows j >= counts[g] of
+// plane g are neither read nor written.
+//
+// The quotients are the correctly rounded x / scale through one reciprocal
+// per row and remainder steps (fp8.cuh explains them); the rounding to an
+// integer adds and keeps 1.5 * 2^23, whose neighbours are one apart.
+//
+// Memory bound: each element is read once and its code written once.  One
+// CTA a row, the row in registers, 16 bytes a thread and load.
+#include "fp8.cuh"
+#include "layer.h"
+
+namespace moe {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kMaxWarps = 8;
+
+__device__ __forceinline__ fp8::RowScale int8_scale(float amax) {
+    fp8::RowScale r;
+    r.s = amax > 0.0f ? fmaxf(__fdiv_rn(amax, 127.0f), 0x1p-126f) : 1.0f;
+    r.m = r.s < 0x1p-100f ? 0x1p100f : (r.s > 0x1p100f ? 0x1p-100f : 1.0f);
+    r.sd = __fmul_rn(r.s, r.m);
+    r.y = __frcp_rn(r.sd);
+    return r;
+}
+
+__device__ __forceinline__ uint32_t code(float q) {  // low byte: the nearest integer
+    return __float_as_uint(__fadd_rn(q, 12582912.0f));
+}
+
+template <bool SCALED>
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], const fp8::RowScale &r) {
+    uint32_t c[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a, b;
+        fp8::quotient2<SCALED>(v[2 * i], v[2 * i + 1], r, a, b);
+        c[2 * i] = code(a);
+        c[2 * i + 1] = code(b);
+    }
+    uint2 o;
+    o.x = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+    o.y = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
+    return o;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void load8(const void *row, int v, float (&f)[8]) {
+    if (BF16) {
+        const uint4 u = __ldg(static_cast<const uint4 *>(row) + v);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    } else {
+        const float4 a = __ldg(static_cast<const float4 *>(row) + 2 * v);
+        const float4 b = __ldg(static_cast<const float4 *>(row) + 2 * v + 1);
+        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+        f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    }
+}
+
+// One CTA a row; thread i takes the 8-element vectors i, i + threads, ...
+template <int VPT, bool BF16>
+__global__ void __launch_bounds__(kMaxWarps * 32) quantize_int8_kernel(const QuantInt8Params p) {
+    __shared__ uint32_t red[2][kMaxWarps];
+    const int tid = threadIdx.x, nt = blockDim.x, H8 = p.H / 8;
+    const long long total = (long long)p.groups * p.rows;
+    int turn = 0;
+    for (long long r = blockIdx.x; r < total; r += gridDim.x) {
+        if (p.counts != nullptr) {
+            const long long g = r / p.rows;
+            if (r - g * p.rows >= __ldg(p.counts + g)) continue;  // (the whole CTA alike)
+        }
+        const char *row = static_cast<const char *>(p.x) + r * p.row_stride * (BF16 ? 2 : 4);
+        float f[VPT][8];
+        uint32_t m = 0;  // bits of |x|: NaN above infinity above every number
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int v = tid + j * nt;
+            if (v < H8) {
+                load8<BF16>(row, v, f[j]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[j][i]) & 0x7fffffffu);
+            }
+        }
+        m = __reduce_max_sync(kFull, m);
+        if ((tid & 31) == 0) red[turn][tid >> 5] = m;
+        __syncthreads();
+        for (int w = 0; w < nt / 32; ++w) m = max(m, red[turn][w]);
+        turn ^= 1;
+        const bool finite = m < 0x7f800000u;
+        const fp8::RowScale s = int8_scale(finite ? __uint_as_float(m) : 0.0f);
+        uint2 *q = reinterpret_cast<uint2 *>(p.q + r * p.H);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int v = tid + j * nt;
+            if (v < H8) {
+                uint2 o = make_uint2(0, 0);
+                if (finite) o = s.m == 1.0f ? codes8<false>(f[j], s) : codes8<true>(f[j], s);
+                q[v] = o;
+            }
+        }
+        if (tid == 0) p.scale[r] = finite ? s.s : __uint_as_float(0x7fc00000u);
+    }
+}
+
+template <int VPT>
+cudaError_t launch_t(const QuantInt8Params &p, int threads, int num_sms, cudaStream_t st) {
+    const long long total = (long long)p.groups * p.rows;
+    const long long most = (long long)num_sms * 16;
+    const unsigned grid = (unsigned)(total < most ? total : most);
+    if (p.bf16)
+        quantize_int8_kernel<VPT, true><<<grid, threads, 0, st>>>(p);
+    else
+        quantize_int8_kernel<VPT, false><<<grid, threads, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_rows_int8(const QuantInt8Params &p, int num_sms, cudaStream_t st) {
+    if (p.H % 8 != 0 || p.H < 8 || p.H > 16384) return cudaErrorInvalidValue;
+    const int H8 = p.H / 8;
+    int threads = (H8 + 31) / 32 * 32;
+    if (threads > kMaxWarps * 32) threads = kMaxWarps * 32;
+    const int vpt = (H8 + threads - 1) / threads;
+    if (vpt <= 1) return launch_t<1>(p, threads, num_sms, st);
+    if (vpt <= 2) return launch_t<2>(p, threads, num_sms, st);
+    if (vpt <= 4) return launch_t<4>(p, threads, num_sms, st);
+    return launch_t<8>(p, threads, num_sms, st);
+}
+
+}  // namespace moe

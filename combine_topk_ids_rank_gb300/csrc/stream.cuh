@@ -1,0 +1,171 @@
+// stream.cuh -- what the two persistent products that stream weights through
+// the tensor cores share (layer_small.cu, gemm_int8.cu): the even split of
+// the k-blocks of all output tiles over the CTAs, the widening of 8-bit
+// weight rows into tensor memory, and waits on counters in global memory.
+//
+// Orientation.  The weights are the A operand: 128 output channels a tile
+// are the 128 tensor-memory lanes, and the tokens are the columns (N), as
+// few as the group has (a multiple of 16).  So a tile costs what its weight
+// bytes cost, whatever the number of tokens.
+//
+// Split.  Tiles x k-blocks ("units") form one line that is cut into equal
+// ranges, one per CTA, wherever the cuts fall.  A tile cut between CTAs is
+// summed by the CTA that finishes its part last, over the parts in ascending
+// k: the order of the additions does not depend on timing.
+#pragma once
+
+#include <cstdint>
+
+#include "layer.h"
+#include "ptx.cuh"
+#include "tcgen05.cuh"
+
+namespace moe {
+namespace stream {
+
+constexpr int kTileRows = 128;   // output channels of a tile
+constexpr int kBlockK = 128;     // k extent of a unit
+constexpr int kAtom = 128;       // bytes of a shared-memory row (128-byte swizzle)
+constexpr uint64_t kWaitNs = 500ull * 1000 * 1000;  // 0.5 s of wall time per wait
+
+// The units [0, total) cut into `parts` ranges; parts <= total (or both 0).
+struct Cut {
+    long long total;
+    int parts;
+    __device__ long long first(int c) const { return (long long)c * total / parts; }
+    // the part that holds unit u
+    __device__ int of(long long u) const {
+        return (int)(((u + 1) * parts - 1) / total);
+    }
+};
+
+__device__ __forceinline__ Cut cut(long long total, int ctas) {
+    return Cut{total, total < ctas ? (int)total : ctas};
+}
+
+// A run of units of one tile: k-blocks [k0, k1) of tile `tile`.
+struct Segment {
+    int tile, k0, k1;
+};
+
+// The segments of CTA c in ascending order; `blocks` k-blocks a tile.
+struct Segments {
+    long long u, end;
+    int blocks;
+    __device__ Segments(const Cut &ct, int c, int blocks_) : u(0), end(0), blocks(blocks_) {
+        if (c < ct.parts) {
+            u = ct.first(c);
+            end = ct.first(c + 1);
+        }
+    }
+    __device__ bool next(Segment &s) {
+        if (u >= end) return false;
+        s.tile = (int)(u / blocks);
+        s.k0 = (int)(u - (long long)s.tile * blocks);
+        const long long left = end - u;
+        s.k1 = s.k0 + left < blocks ? (int)(s.k0 + left) : blocks;
+        u += s.k1 - s.k0;
+        return true;
+    }
+};
+
+// Parts of tile t: CTAs [c0, c1]; the part of CTA c is kept in slot 0 if it
+// begins that CTA's range, else in slot 1.
+struct Parts {
+    int c0, c1, slot0;
+    __device__ Parts(const Cut &ct, int tile, int blocks) {
+        const long long a = (long long)tile * blocks;
+        c0 = ct.of(a);
+        c1 = ct.of(a + blocks - 1);
+        slot0 = ct.first(c0) == a ? 0 : 1;
+    }
+    __device__ int slot(int c) const { return c == c0 ? slot0 : 0; }
+    __device__ int count() const { return c1 - c0 + 1; }
+};
+
+__device__ __forceinline__ int ld_acquire(const int *p) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
+// Wait until *p reaches `want` (it only grows meanwhile); false on timeout or
+// when another role of this CTA has failed.
+__device__ __forceinline__ bool wait_count(const int *p, int want, volatile int *failed) {
+    if (ld_acquire(p) >= want) return true;
+    const uint64_t t0 = ptx::globaltimer_ns();
+    for (;;) {
+        for (int i = 0; i < 64; ++i)
+            if (ld_acquire(p) >= want) return true;
+        if (*failed || ptx::globaltimer_ns() - t0 > kWaitNs) return false;
+    }
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(
+                     ptx::smem_u32(bar))
+                 : "memory");
+}
+
+// Barrier 1 of the 128 epilogue threads; true where any of them says so.
+__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool epi_any(bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(v ? 1u : 0u)
+        : "memory");
+    return r != 0;
+}
+
+// A flag in shared memory, read alike by all lanes of a warp.
+__device__ __forceinline__ bool warp_flag(const volatile int *f) {
+    return __any_sync(0xffffffffu, *f != 0);
+}
+
+// ---- four 8-bit codes -> four 16-bit values (two words, ascending) -----------
+
+// int8 -> bf16, exact: the low 7 bits ride on 128 (0x4300, one unit apart),
+// the sign bit turns the subtracted 128 into 256 (0x4380).
+__device__ __forceinline__ void int8_to_bf16(uint32_t v, uint32_t &a, uint32_t &b) {
+    const uint32_t lo = v & 0x7f7f7f7fu, hi = v & 0x80808080u;
+    const uint32_t la = __byte_perm(lo, 0x43434343u, 0x5140), lb = __byte_perm(lo, 0x43434343u, 0x7362);
+    const uint32_t ha = __byte_perm(hi, 0x43434343u, 0x5140), hb = __byte_perm(hi, 0x43434343u, 0x7362);
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(la), "r"(ha));
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(lb), "r"(hb));
+}
+
+// int8 -> f16, exact: code + 128 rides on 1024 (0x6400, one unit apart).
+__device__ __forceinline__ void int8_to_f16(uint32_t v, uint32_t &a, uint32_t &b) {
+    const uint32_t u = v ^ 0x80808080u;
+    const uint32_t ua = __byte_perm(u, 0x64646464u, 0x5140), ub = __byte_perm(u, 0x64646464u, 0x7362);
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(a) : "r"(ua), "r"(0x64806480u));  // 1152
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(b) : "r"(ub), "r"(0x64806480u));
+}
+
+// e4m3 -> bf16, exact: the code's exponent and mantissa moved into bf16's
+// fields are 2^-120 times the value, also for e4m3's subnormals; the codes
+// 0x7f and 0xff are NaN.
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t w) {  // codes in the high bytes
+    const uint32_t m = ((w & 0x7f007f00u) >> 4) | (w & 0x80008000u);
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(0x7b807b80u));  // 2^120
+    return r;
+}
+__device__ __forceinline__ void e4m3_to_bf16(uint32_t v, uint32_t &a, uint32_t &b) {
+    a = e4m3_pair(__byte_perm(v, 0, 0x1404));
+    b = e4m3_pair(__byte_perm(v, 0, 0x3424));
+    if (((v & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) {  // a NaN among the four
+        if ((v & 0x7fu) == 0x7fu) a = (a & 0xffff0000u) | 0x7fffu;
+        if ((v & 0x7f00u) == 0x7f00u) a = (a & 0xffffu) | 0x7fff0000u;
+        if ((v & 0x7f0000u) == 0x7f0000u) b = (b & 0xffff0000u) | 0x7fffu;
+        if ((v & 0x7f000000u) == 0x7f000000u) b = (b & 0xffffu) | 0x7fff0000u;
+    }
+}
+
+}  // namespace stream
+}  // namespace moe

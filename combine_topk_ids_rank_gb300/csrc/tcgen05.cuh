@@ -1,6 +1,7 @@
 // tcgen05.cuh -- inline-PTX wrappers for the sm_100-family tensor cores
-// (tcgen05: MMA from shared-memory descriptors into tensor memory) and the
-// tiled TMA load, as used by expert_gemm.cu.
+// (tcgen05: MMA from shared-memory descriptors or tensor memory into tensor
+// memory) and the tiled TMA load, as used by expert_gemm.cu, layer_small.cu
+// and gemm_int8.cu.
 //
 // Encodings (PTX ISA, "Tensor Memory" and "tcgen05.mma" sections):
 //  * shared-memory matrix descriptor (64 bits): start address >> 4 in
@@ -9,7 +10,7 @@
 //    in [49,52), swizzle mode in [61,64) (2 = 128-byte swizzle);
 //  * instruction descriptor of .kind::f16 / .kind::f8f6f4 (32 bits): D
 //    format in [4,6) (1 = f32), A format in [7,10) and B format in [10,13)
-//    (f16 kind: 1 = bf16; f8f6f4 kind: 0 = E4M3),
+//    (f16 kind: 0 = f16, 1 = bf16; f8f6f4 kind: 0 = E4M3),
 //    A / B major in bits 15 / 16 (0 = K-major), N >> 3 in [17,23),
 //    M >> 4 in [24,29);
 //  * tensor-memory address: lane in bits [16,32), column in [0,16).
@@ -39,6 +40,11 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t smem_addr) {
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) |
            ((uint32_t)(M >> 4) << 24);
+}
+
+// f16 x f16 -> f32, both operands K-major, M x N tile.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 // e4m3 x e4m3 -> f32 (.kind::f8f6f4, format code 0 = E4M3), both K-major.
@@ -92,6 +98,18 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_
         : "memory");
 }
 
+// D[tmem] (+)= A[tmem] * B[smem]^T on 16-bit operands: lane r of A holds row r
+// of the operand, two K-adjacent values a column (8 columns per K step).
+__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                           uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+
 // The mbarrier receives one arrival when every tcgen05 operation issued so
 // far by this thread has completed.
 __device__ __forceinline__ void commit(uint64_t *bar) {
@@ -117,6 +135,38 @@ __device__ __forceinline__ void ld_32x32(uint32_t taddr, uint32_t (&r)[32]) {
           "=r"(r[31])
         : "r"(taddr)
         : "memory");
+}
+
+// 32 lanes x 16 columns.
+__device__ __forceinline__ void ld_32x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// Registers -> 32 lanes x 32 columns: thread i of the warp writes lane
+// (base lane + i), columns [col, col + 32).
+__device__ __forceinline__ void st_32x32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void wait_st() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void wait_ld() {

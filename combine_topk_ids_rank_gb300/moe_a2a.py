@@ -34,12 +34,19 @@ EXPORTS = ("moe_a2a_workspace_bytes", "moe_a2a_create", "moe_dispatch",
            "moe_a2a_set_recv_format", "moe_combine_fp8", "moe_quantize_rows_fp8",
            "moe_a2a_workspace_bytes_layout", "moe_a2a_create_layout",
            "moe_expert_gemm", "moe_expert_gemm_fp8", "moe_expert_gemm_rank_scratch_bytes",
-           "moe_expert_gemm_rank", "moe_expert_gemm_rank_fp8")
+           "moe_expert_gemm_rank", "moe_expert_gemm_rank_fp8", "moe_topk_gate",
+           "moe_quantize_rows_int8", "moe_gemm_int8_scratch_bytes", "moe_gemm_int8",
+           "moe_layer_small_scratch_bytes", "moe_layer_small", "moe_scratch_init",
+           "moe_scratch_get_error")
 MOE_REDUCE_FP32_RANK_ORDER = 0
 MOE_REDUCE_BF16_TOPK_TREE = 1
 MOE_STATIC_SCRATCH_BYTES = 4 << 20
 MOE_FORMAT_BF16 = 0
 MOE_FORMAT_FP8_E4M3 = 1
+MOE_FORMAT_INT8 = 2
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
+MOE_LAYER_MAX_TOKENS = 64
 MOE_LAYOUT_RANK = 0
 MOE_LAYOUT_EXPERT = 1
 
@@ -121,6 +128,23 @@ def _load(path: str = LIBRARY):
     lib.moe_a2a_set_recv_format.restype = ctypes.c_int
     lib.moe_a2a_set_reduction.argtypes = [p, i32]
     lib.moe_a2a_set_reduction.restype = ctypes.c_int
+    i64, f32 = ctypes.c_int64, ctypes.c_float
+    lib.moe_topk_gate.argtypes = [p, i32, i64, i64, i32, i32, i32, i32, f32, p, p, p]
+    lib.moe_topk_gate.restype = ctypes.c_int
+    lib.moe_quantize_rows_int8.argtypes = [p, i32, i32, i32, i32, i64, p, p, p, p]
+    lib.moe_quantize_rows_int8.restype = ctypes.c_int
+    lib.moe_gemm_int8_scratch_bytes.argtypes = [i32]
+    lib.moe_gemm_int8_scratch_bytes.restype = sz
+    lib.moe_gemm_int8.argtypes = [p, p, p, p, p, i32, i32, i32, i32, p, p, sz, p]
+    lib.moe_gemm_int8.restype = ctypes.c_int
+    lib.moe_layer_small_scratch_bytes.argtypes = [i32, i32, i32, i32]
+    lib.moe_layer_small_scratch_bytes.restype = sz
+    lib.moe_layer_small.argtypes = [p] * 8 + [i32] * 6 + [p, p, sz, p]
+    lib.moe_layer_small.restype = ctypes.c_int
+    lib.moe_scratch_init.argtypes = [p, sz, p]
+    lib.moe_scratch_init.restype = ctypes.c_int
+    lib.moe_scratch_get_error.argtypes = [p, p, ctypes.POINTER(ctypes.c_uint32)]
+    lib.moe_scratch_get_error.restype = ctypes.c_int
     lib.moe_a2a_status_string.argtypes = [ctypes.c_int]
     lib.moe_a2a_status_string.restype = ctypes.c_char_p
     return lib
@@ -314,6 +338,268 @@ def moe_route_static_scratch(ep_size: int, num_experts: int, top_k: int, tokens_
              v(d_topk_ids), v(d_topk_w), v(d_send_slot), v(d_dest_weight), v(d_src_token),
              v(d_recv_counts), v(d_local_expert_counts), v(d_recv_topk_ids), v(d_recv_topk_w),
              v(d_flags), v(stream))
+
+
+def moe_topk_gate(d_logits: int, bf16: bool, tokens: int, row_stride: int, num_experts: int,
+                  top_k: int, scoring: int, renormalize: bool, scale: float, d_topk_ids: int,
+                  d_topk_w: int, stream: int = 0) -> int:
+    return _lib.moe_topk_gate(d_logits, int(bf16), tokens, row_stride, num_experts, top_k,
+                              scoring, int(renormalize), scale, d_topk_ids, d_topk_w, stream)
+
+
+def moe_quantize_rows_int8(d_x: int, bf16: bool, groups: int, rows: int, hidden: int,
+                           row_stride: int, d_counts: int, d_q: int, d_scale: int,
+                           stream: int = 0) -> int:
+    return _lib.moe_quantize_rows_int8(d_x, int(bf16), groups, rows, hidden, row_stride,
+                                       d_counts, d_q, d_scale, stream)
+
+
+def moe_gemm_int8_scratch_bytes(rows: int) -> int:
+    return int(_lib.moe_gemm_int8_scratch_bytes(rows))
+
+
+def moe_gemm_int8(d_xq: int, d_x_scale: int, d_wq: int, d_w_scale: int, d_counts: int,
+                  groups: int, rows: int, N: int, hidden: int, d_out: int, d_scratch: int,
+                  scratch_bytes: int, stream: int = 0) -> int:
+    return _lib.moe_gemm_int8(d_xq, d_x_scale, d_wq, d_w_scale, d_counts, groups, rows, N,
+                              hidden, d_out, d_scratch, scratch_bytes, stream)
+
+
+def moe_layer_small_scratch_bytes(tokens: int, top_k: int, hidden: int, inter: int) -> int:
+    return int(_lib.moe_layer_small_scratch_bytes(tokens, top_k, hidden, inter))
+
+
+def moe_layer_small(d_x: int, d_topk_ids: int, d_topk_w: int, d_w13: int, d_w13_scale: int,
+                    d_w2: int, d_w2_scale: int, d_residual: int, tokens: int, top_k: int,
+                    num_experts: int, hidden: int, inter: int, fmt: int, d_out: int,
+                    d_scratch: int, scratch_bytes: int, stream: int = 0) -> int:
+    return _lib.moe_layer_small(d_x, d_topk_ids, d_topk_w, d_w13, d_w13_scale, d_w2, d_w2_scale,
+                                d_residual, tokens, top_k, num_experts, hidden, inter, fmt,
+                                d_out, d_scratch, scratch_bytes, stream)
+
+
+def moe_scratch_init(d_scratch: int, scratch_bytes: int, stream: int = 0) -> int:
+    return _lib.moe_scratch_init(d_scratch, scratch_bytes, stream)
+
+
+def moe_scratch_get_error(d_scratch: int, stream: int = 0):
+    """Returns (status, device flag bits)."""
+    flags = ctypes.c_uint32(0)
+    st = _lib.moe_scratch_get_error(d_scratch, stream, ctypes.byref(flags))
+    return st, int(flags.value)
+
+
+# ---- torch forms of the operators around dispatch and combine ------------------
+
+def _raw_stream(stream, device) -> int:
+    if stream is None:
+        import torch
+        return torch.cuda.current_stream(device).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor that belongs to the stream it is going to be used on."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _expect(t, dtype, shape, device, name):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError("%s: expected %s %s, got %s %s" % (name, dtype, tuple(shape), t.dtype,
+                                                            tuple(t.shape)))
+    if t.device != device or not t.is_contiguous():
+        raise ValueError("%s must be contiguous on %s" % (name, device))
+
+
+def topk_gate(logits, top_k: int, scoring: int = MOE_SCORE_SOFTMAX, renormalize: bool = True,
+              scale: float = 1.0, out_ids=None, out_w=None, stream=None):
+    """Router logits, fp32 or bf16 [..., E] with dense rows (2-D logits may
+    have any row stride) -> (ids int32 [..., K], weights float32 [..., K])."""
+    import torch
+    if not logits.is_cuda or logits.dtype not in (torch.float32, torch.bfloat16) or \
+            logits.dim() < 1:
+        raise ValueError("logits must be a float32 or bfloat16 CUDA tensor [..., E]")
+    E, lead = logits.shape[-1], logits.shape[:-1]
+    row_stride = E
+    if not logits.is_contiguous():
+        if logits.dim() != 2 or logits.stride(1) != 1 or logits.stride(0) < E:
+            raise ValueError("logits must be contiguous, or 2-D with dense rows")
+        row_stride = logits.stride(0)
+    shape = (*lead, top_k)
+    if out_ids is None:
+        out_ids = _empty(shape, torch.int32, logits.device, stream)
+    else:
+        _expect(out_ids, torch.int32, shape, logits.device, "out_ids")
+    if out_w is None:
+        out_w = _empty(shape, torch.float32, logits.device, stream)
+    else:
+        _expect(out_w, torch.float32, shape, logits.device, "out_w")
+    st = _lib.moe_topk_gate(logits.data_ptr(), logits.dtype == torch.bfloat16,
+                            logits.numel() // E if E else 0, row_stride, E, top_k, scoring,
+                            bool(renormalize), scale, out_ids.data_ptr(), out_w.data_ptr(),
+                            _raw_stream(stream, logits.device))
+    if st != MOE_OK:
+        raise MoeA2AError(st, "moe_topk_gate")
+    return out_ids, out_w
+
+
+def quantize_rows_int8(x, counts=None, out=None, scale=None, stream=None):
+    """fp32 or bf16 [..., H] CUDA tensor -> (int8 [..., H], float32 [...]).
+    With counts (int32 [G] on the device) x is [G, rows, H] and rows past a
+    plane's count are left alone.  2-D x may have any row stride that is a
+    multiple of 16 bytes."""
+    import torch
+    if not x.is_cuda or x.dtype not in (torch.float32, torch.bfloat16) or x.dim() < 1:
+        raise ValueError("x must be a float32 or bfloat16 CUDA tensor [..., H]")
+    H, lead = x.shape[-1], x.shape[:-1]
+    row_stride = H
+    if not x.is_contiguous():
+        if x.dim() != 2 or x.stride(1) != 1 or x.stride(0) < H:
+            raise ValueError("x must be contiguous, or 2-D with dense rows")
+        row_stride = x.stride(0)
+    groups, rows = 1, x.numel() // H if H else 0
+    if counts is not None:
+        if x.dim() != 3:
+            raise ValueError("with counts x must be [groups, rows, hidden]")
+        groups, rows = lead
+        _expect(counts, torch.int32, (groups,), x.device, "counts")
+    if out is None:
+        out = _empty(x.shape, torch.int8, x.device, stream)
+    else:
+        _expect(out, torch.int8, x.shape, x.device, "out")
+    if scale is None:
+        scale = _empty(lead, torch.float32, x.device, stream)
+    else:
+        _expect(scale, torch.float32, lead, x.device, "scale")
+    st = _lib.moe_quantize_rows_int8(x.data_ptr(), x.dtype == torch.bfloat16, groups, rows, H,
+                                     row_stride, _ptr(counts), out.data_ptr(),
+                                     scale.data_ptr(), _raw_stream(stream, x.device))
+    if st != MOE_OK:
+        raise MoeA2AError(st, "moe_quantize_rows_int8")
+    return out, scale
+
+
+class _Scratch:
+    """Device memory that one operator keeps between its calls."""
+
+    def __init__(self, nbytes: int, device, where: str):
+        import torch
+        if nbytes == 0:
+            raise MoeA2AError(MOE_ERR_INVALID_ARG, where)
+        self.device = torch.device(device if device is not None else "cuda")
+        self.scratch = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        self.device = self.scratch.device
+        stream = torch.cuda.current_stream(self.device)
+        st = moe_scratch_init(self.scratch.data_ptr(), nbytes, stream.cuda_stream)
+        if st != MOE_OK:
+            raise MoeA2AError(st, "moe_scratch_init")
+        stream.synchronize()  # calls may come on any stream
+
+    def get_error(self, stream=None):
+        """Synchronise, read and clear the device flag word: (status, bits)."""
+        return moe_scratch_get_error(self.scratch.data_ptr(), _raw_stream(stream, self.device))
+
+
+class MoeGemmInt8(_Scratch):
+    """The 8-bit integer product over `groups` weight matrices, with the
+    scratch memory it needs.  One call at a time: calls in stream order."""
+
+    def __init__(self, groups: int, max_rows: int, N: int, hidden: int, device=None):
+        self.groups, self.max_rows, self.N, self.hidden = groups, max_rows, N, hidden
+        super().__init__(moe_gemm_int8_scratch_bytes(max_rows), device,
+                         "moe_gemm_int8_scratch_bytes")
+
+    def gemm(self, xq, x_scale, wq, w_scale, counts=None, out=None, stream=None):
+        """xq int8 [G, rows, H], x_scale float32 [G, rows], wq int8 [G, N, H],
+        w_scale float32 [G, N], counts int32 [G] on the device or None (all
+        rows) -> out bf16 [G, rows, N], rows past a count untouched (undefined
+        in a new tensor).  With one group the leading extent may be left out."""
+        import torch
+        G, N, H, dev = self.groups, self.N, self.hidden, self.device
+        lead = (G,) if xq.dim() == 3 or G != 1 else ()
+        rows = xq.shape[-2] if xq.dim() >= 2 else 0
+        _expect(xq, torch.int8, (*lead, rows, H), dev, "xq")
+        _expect(x_scale, torch.float32, (*lead, rows), dev, "x_scale")
+        _expect(wq, torch.int8, (*lead, N, H), dev, "wq")
+        _expect(w_scale, torch.float32, (*lead, N), dev, "w_scale")
+        if counts is not None:
+            _expect(counts, torch.int32, (G,), dev, "counts")
+        if rows > self.max_rows:
+            raise MoeA2AError(MOE_ERR_CAPACITY, "moe_gemm_int8")
+        if out is None:
+            out = _empty((*lead, rows, N), torch.bfloat16, dev, stream)
+        else:
+            _expect(out, torch.bfloat16, (*lead, rows, N), dev, "out")
+        st = _lib.moe_gemm_int8(xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(),
+                                w_scale.data_ptr(), _ptr(counts), G, rows, N, H, out.data_ptr(),
+                                self.scratch.data_ptr(), self.scratch.numel(),
+                                _raw_stream(stream, dev))
+        if st != MOE_OK:
+            raise MoeA2AError(st, "moe_gemm_int8")
+        return out
+
+
+class MoeLayerSmall(_Scratch):
+    """A whole mixture-of-experts layer for at most `max_tokens` tokens (64 at
+    most), with the scratch memory it needs.  One call at a time: calls in
+    stream order."""
+
+    def __init__(self, num_experts: int, hidden: int, inter: int, top_k: int,
+                 max_tokens: int = MOE_LAYER_MAX_TOKENS, fmt: int = MOE_FORMAT_BF16,
+                 device=None):
+        import torch
+        self.num_experts, self.hidden, self.inter, self.top_k = num_experts, hidden, inter, top_k
+        self.max_tokens, self.fmt = max_tokens, fmt
+        self._wtypes = {MOE_FORMAT_BF16: (torch.bfloat16,), MOE_FORMAT_INT8: (torch.int8,),
+                        MOE_FORMAT_FP8_E4M3: (torch.float8_e4m3fn, torch.uint8)}.get(fmt)
+        if self._wtypes is None:
+            raise MoeA2AError(MOE_ERR_INVALID_ARG, "moe_layer_small")
+        super().__init__(moe_layer_small_scratch_bytes(max_tokens, top_k, hidden, inter), device,
+                         "moe_layer_small_scratch_bytes")
+
+    def forward(self, x, topk_ids, topk_w, w13, w2, w13_scale=None, w2_scale=None,
+                residual=None, out=None, stream=None):
+        """x bf16 [T, H], topk_ids int32 [T, K], topk_w float32 [T, K],
+        w13 [E, 2I, H] (gate rows, then up rows), w2 [E, H, I] in the
+        handle's format, with channel scales float32 [E, 2I], [E, H] for the
+        8-bit formats -> out bf16 [T, H] (+ residual)."""
+        import torch
+        E, H, I, K, dev = self.num_experts, self.hidden, self.inter, self.top_k, self.device
+        T = x.shape[0]
+        _expect(x, torch.bfloat16, (T, H), dev, "x")
+        _expect(topk_ids, torch.int32, (T, K), dev, "topk_ids")
+        _expect(topk_w, torch.float32, (T, K), dev, "topk_w")
+        if T > self.max_tokens:
+            raise MoeA2AError(MOE_ERR_CAPACITY, "moe_layer_small")
+        if w13.dtype not in self._wtypes or w2.dtype not in self._wtypes:
+            raise ValueError("w13, w2: expected %s" % (self._wtypes[0],))
+        _expect(w13, w13.dtype, (E, 2 * I, H), dev, "w13")
+        _expect(w2, w2.dtype, (E, H, I), dev, "w2")
+        if self.fmt != MOE_FORMAT_BF16:
+            if w13_scale is None or w2_scale is None:
+                raise ValueError("w13_scale and w2_scale are needed for 8-bit weights")
+            _expect(w13_scale, torch.float32, (E, 2 * I), dev, "w13_scale")
+            _expect(w2_scale, torch.float32, (E, H), dev, "w2_scale")
+        if residual is not None:
+            _expect(residual, torch.bfloat16, (T, H), dev, "residual")
+        if out is None:
+            out = _empty((T, H), torch.bfloat16, dev, stream)
+        else:
+            _expect(out, torch.bfloat16, (T, H), dev, "out")
+        st = _lib.moe_layer_small(x.data_ptr(), topk_ids.data_ptr(), topk_w.data_ptr(),
+                                  w13.data_ptr(), _ptr(w13_scale), w2.data_ptr(),
+                                  _ptr(w2_scale), _ptr(residual), T, K, E, H, I, self.fmt,
+                                  out.data_ptr(), self.scratch.data_ptr(), self.scratch.numel(),
+                                  _raw_stream(stream, dev))
+        if st != MOE_OK:
+            raise MoeA2AError(st, "moe_layer_small")
+        return out
 
 
 # ---- torch convenience wrapper ------------------------------------------------

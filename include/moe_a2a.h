@@ -436,7 +436,11 @@ int moe_a2a_set_reduction(moe_a2a_t *h, int32_t reduction);
  *     recv_scale fp32 [R][R][m]; the metadata rows, counts and send tables
  *     are unchanged.  Needs H a multiple of 16 (MOE_ERR_INVALID_ARG).
  *   The expert outputs that combine reads stay bf16 in either format. */
-enum moe_format { MOE_FORMAT_BF16 = 0, MOE_FORMAT_FP8_E4M3 = 1 };
+enum moe_format {
+    MOE_FORMAT_BF16 = 0,
+    MOE_FORMAT_FP8_E4M3 = 1,
+    MOE_FORMAT_INT8 = 2        /* weights only: moe_layer_small */
+};
 
 int moe_a2a_set_recv_format(moe_a2a_t *h, int32_t format);
 
@@ -465,6 +469,117 @@ int moe_combine_fp8(moe_a2a_t *h, const void *d_expert_out, int32_t weighted,
  * scaled by 2^100 or 2^-100, which leaves the quotient unchanged). */
 int moe_quantize_rows_fp8(const float *d_x, int64_t rows, int32_t hidden, void *d_q,
                           float *d_scale, void *stream);
+
+/* ---- Router gate ------------------------------------------------------------
+ * The router's logits to the top-k expert ids and weights that moe_dispatch
+ * and moe_layer_small take.  Per token with logits l_e, an expert whose logit
+ * is -inf or NaN is closed to it; S are the others:
+ *   d_topk_ids[t][0..K) = the K experts of S with the largest logits, in
+ *     descending order, equal logits by ascending id; -1 past |S|;
+ *   score s_e = exp(l_e - max) / sum over S (MOE_SCORE_SOFTMAX; a row with
+ *     +inf shares the weight among its infinities), or 1 / (1 + exp(-l_e))
+ *     (MOE_SCORE_SIGMOID);
+ *   d_topk_w[t][k] = scale * s, divided by the sum of the K selected scores
+ *     if renormalize; 0 where the id is -1.
+ * fp32 arithmetic whatever the logits' type.
+ *   d_logits  fp32 (bf16 = 0) or bf16 (bf16 = 1) [tokens][row_stride],
+ *             naturally aligned; row_stride >= num_experts
+ *   num_experts 1..1024, top_k 1..32 and <= num_experts
+ *   d_topk_ids int32, d_topk_w fp32 [tokens][top_k]
+ * Queues one kernel on `stream`; no handle. */
+enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+
+int moe_topk_gate(const void *d_logits, int32_t bf16, int64_t tokens, int64_t row_stride,
+                  int32_t num_experts, int32_t top_k, int32_t scoring, int32_t renormalize,
+                  float scale, int32_t *d_topk_ids, float *d_topk_w, void *stream);
+
+/* ---- 8-bit integer product --------------------------------------------------
+ * Rows to 8-bit integer codes with one scale per row:
+ *   scale = max(amax_h |x_h| / 127, 2^-126) in binary32 (1 for an all-zero row),
+ *   q_h   = x_h / scale (binary32 quotient) to the nearest integer, ties to
+ *           even: -127..127.  A row with a NaN or an infinity gets scale NaN
+ *           and zero codes.
+ *   d_x     fp32 or bf16, `groups` planes of `rows` rows, row r of plane g at
+ *           (g * rows + r) * row_stride; 16-byte aligned, row_stride a
+ *           multiple of 16 bytes
+ *   hidden  a multiple of 8, 8..16384
+ *   d_counts int32 [groups] or NULL: rows j >= d_counts[g] of plane g are
+ *           neither read nor written (the counts of an expert-layout dispatch)
+ *   d_q     int8 [groups][rows][hidden], 16-byte aligned; d_scale fp32
+ *           [groups][rows]
+ * Queues one kernel on `stream`; no handle. */
+int moe_quantize_rows_int8(const void *d_x, int32_t bf16, int32_t groups, int32_t rows,
+                           int32_t hidden, int64_t row_stride, const int32_t *d_counts,
+                           int8_t *d_q, float *d_scale, void *stream);
+
+/* Product of 8-bit integer codes with scales, dense (groups = 1) or grouped:
+ *   out[g][m][n] = bf16_rn( (sum_h xq[g][m][h] * wq[g][n][h]) * sx[g][m] * sw[g][n] ),
+ * the sum exact while it and its partial sums stay within 2^24 in magnitude
+ * (fp32 accumulation past that), then two fp32 multiplies.
+ *   d_xq int8 [groups][rows][hidden], d_x_scale fp32 [groups][rows]
+ *   d_wq int8 [groups][N][hidden] (row n = the weights of output n),
+ *   d_w_scale fp32 [groups][N]
+ *   d_counts int32 [groups] or NULL (all rows): rows m >= d_counts[g] are not
+ *           written (counts are clamped to 0..rows)
+ *   hidden  a multiple of 16; N and rows any; groups <= 1024;
+ *           groups * rows, groups * N < 2^31
+ *   d_out   bf16 [groups][rows][N]
+ *   d_scratch at least moe_gemm_int8_scratch_bytes(rows) bytes, 256-byte
+ *           aligned, prepared once by moe_scratch_init and then used by one
+ *           call at a time (calls in stream order)
+ * d_xq and d_wq 16-byte aligned.  Queues one kernel on `stream`. */
+size_t moe_gemm_int8_scratch_bytes(int32_t rows);
+
+int moe_gemm_int8(const int8_t *d_xq, const float *d_x_scale, const int8_t *d_wq,
+                  const float *d_w_scale, const int32_t *d_counts, int32_t groups, int32_t rows,
+                  int32_t N, int32_t hidden, void *d_out, void *d_scratch, size_t scratch_bytes,
+                  void *stream);
+
+/* ---- Whole layer for a few tokens -------------------------------------------
+ * A mixture-of-experts layer of gated two-layer experts in one kernel, for
+ * batches too small for receive planes (at most MOE_LAYER_MAX_TOKENS tokens):
+ *   h   = W13[e] x_t * s13[e]      rows 0..I-1 the gate, I..2I-1 the up part,
+ *   a   = bf16_rn( silu(h_gate) * h_up ),  silu(z) = z / (1 + exp(-z)),
+ *   y_k = (W2[e] a) * s2[e],       e = topk_ids[t][k],
+ *   out[t] = bf16_rn( sum over k ascending of topk_w[t][k] * y_k (+ residual[t]) ),
+ * fp32 accumulation and sum.  Id -1 is no expert; an id outside [-1, E) is
+ * skipped and raises the flag; a token that names an expert twice gets it
+ * once with the sum of the gates; a token without an expert gets 0 (or its
+ * residual).
+ *   d_x      bf16 [tokens][hidden], 16-byte aligned
+ *   d_w13    [E][2 * inter][hidden], d_w2 [E][hidden][inter], 16-byte aligned:
+ *            bf16 (MOE_FORMAT_BF16, scales NULL), e4m3 codes
+ *            (MOE_FORMAT_FP8_E4M3) or int8 codes (MOE_FORMAT_INT8) with fp32
+ *            channel scales d_w13_scale [E][2 * inter], d_w2_scale [E][hidden]
+ *   d_residual bf16 [tokens][hidden] or NULL (8-byte aligned; may be d_out)
+ *   hidden, inter multiples of 16, up to 16384; num_experts <= 1024; top_k <= 32
+ *   d_out    bf16 [tokens][hidden], 8-byte aligned; must not overlap d_x
+ *   d_scratch at least moe_layer_small_scratch_bytes bytes, as for
+ *            moe_gemm_int8
+ * Queues one kernel on `stream`: a cooperative launch that takes every SM,
+ * whose CTAs wait for one another with a time limit (MOE_ERR_DEVICE_TIMEOUT
+ * from moe_scratch_get_error; the outputs are then incomplete). */
+#define MOE_LAYER_MAX_TOKENS 64
+
+size_t moe_layer_small_scratch_bytes(int32_t tokens, int32_t top_k, int32_t hidden,
+                                     int32_t inter);
+
+int moe_layer_small(const void *d_x, const int32_t *d_topk_ids, const float *d_topk_w,
+                    const void *d_w13, const float *d_w13_scale, const void *d_w2,
+                    const float *d_w2_scale, const void *d_residual, int32_t tokens,
+                    int32_t top_k, int32_t num_experts, int32_t hidden, int32_t inter,
+                    int32_t format, void *d_out, void *d_scratch, size_t scratch_bytes,
+                    void *stream);
+
+/* Prepare a scratch buffer of moe_gemm_int8 or moe_layer_small for its first
+ * call (queues one memset); every call leaves it prepared for the next. */
+int moe_scratch_init(void *d_scratch, size_t scratch_bytes, void *stream);
+
+/* Synchronise `stream` and read the flag word of a scratch buffer; if it is
+ * set, clear it and prepare the buffer anew.  MOE_OK, MOE_ERR_ROUTING,
+ * MOE_ERR_DEVICE_TIMEOUT or MOE_ERR_CUDA; if flags is not NULL it receives
+ * the raw bits. */
+int moe_scratch_get_error(void *d_scratch, void *stream, uint32_t *flags);
 
 /* ---- Routing without any device allocation --------------------------------
  * The source pages have no counterpart to this entry point; it exists for
