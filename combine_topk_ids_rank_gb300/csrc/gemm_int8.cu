@@ -45,6 +45,8 @@ constexpr int kTmemCols = 512;          // accumulators, then widened weights
 constexpr int kSlots = 4, kSlotCols = kBlockK / 2;
 constexpr int kWeightBytes = kTileRows * kBlockK;
 constexpr int kMaxStages = 12, kMaxHalves = 8;
+// dynamic shared memory: 227 KB a CTA less the static tables
+constexpr size_t kMaxDynamic = (227 - 12) * 1024;
 constexpr int kRowGroup = 16;           // row tiles of a raster group
 
 struct Ring {
@@ -185,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t slots_at = taddr + kMaxCols;
 
     if (warp == kProducerWarp) {
-        if (lane == 0) {
+        if (ptx::elect_one()) {
             uint32_t n = 0;
             Work work(ct, cut_tiles, tiles, blocks, cta, ctas);
             Segment sg;
@@ -214,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::mbar_wait_timed(&raw_full[k % ring.stages], (k / ring.stages) & 1u, kWaitNs);
         }
     } else if (warp == kMmaWarp) {
-        if (lane == 0) {
+        if (ptx::elect_one()) {
             uint32_t n = 0, h = 0, it = 0;
             Work work(ct, cut_tiles, tiles, blocks, cta, ctas);
             Segment sg;
@@ -433,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
 
+    __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
     if (tid == 0 && s_failed) atomicOr(&p.header->flags, MOE_DEVICE_FLAG_WAIT_TIMEOUT);
@@ -455,7 +458,7 @@ cudaError_t launch_gemm_int8(GemmInt8Params p, int num_sms, cudaStream_t st) {
     ring.nmax = p.nmax;
     ring.box = p.nmax < 32 ? 16 : 32;
     const int raw = kWeightBytes + ring.nmax * kAtom, half = ring.nmax * kAtom;
-    const int room = 227 * 1024 - 12 * 1024 - 1024;
+    const int room = (int)kMaxDynamic - 1024;
     // at least two widened halves, then raw stages, then more halves
     ring.halves = ring.nmax > 128 ? 2 : 4;
     ring.stages = (room - ring.halves * half) / raw;
@@ -466,7 +469,8 @@ cudaError_t launch_gemm_int8(GemmInt8Params p, int num_sms, cudaStream_t st) {
     if (!make_map(&mx, p.xq, (long long)p.G * p.M, p.H, ring.box, true) ||
         !make_map(&mw, p.wq, (long long)p.G * p.N, p.H, kTileRows, true))
         return cudaErrorInvalidValue;
-    cudaError_t err = raise_smem_limit(gemm_int8_kernel, smem);
+    static std::atomic<unsigned long long> raised{0};
+    cudaError_t err = raise_smem_limit_once(gemm_int8_kernel, kMaxDynamic, raised);
     if (err != cudaSuccess) return err;
     const int grid = num_sms < kStreamMaxCtas ? num_sms : kStreamMaxCtas;
     gemm_int8_kernel<<<grid, kThreads, smem, st>>>(mx, mw, p, ring);

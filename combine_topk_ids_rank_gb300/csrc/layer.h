@@ -63,13 +63,13 @@ struct LayerSmallParams {
     const uint16_t *residual;  // bf16 [T][H] or null
     uint16_t *out;             // bf16 [T][H]
     StreamHeader *header;
-    uint16_t *act;             // bf16 [T * K][I]
+    uint16_t *act;             // bf16 [T * K][2][I]: the activations in two terms
     float *y;                  // [T * K][H]
     float *part;               // [CTAs][2][Nmax][128]
     int T, K, E, H, I;
     int format;                // MOE_FORMAT_*
     // set by the launcher
-    int nmax, stages;
+    int nmax, ring_bytes;
 };
 cudaError_t launch_layer_small(LayerSmallParams p, int num_sms, cudaStream_t st);
 

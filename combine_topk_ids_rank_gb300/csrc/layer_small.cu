@@ -3,7 +3,7 @@
 //
 // Operation, token t with experts e_k = topk_ids[t][k] and gates g_k:
 //   h     = W13[e] x_t                       (rows 0..I-1 gate, I..2I-1 up),
-//   a     = bf16_rn( silu(h_gate * s13) * (h_up * s13) ),  silu(z) = z / (1 + e^-z),
+//   a     = silu(h_gate * s13) * (h_up * s13),  silu(z) = z / (1 + e^-z),
 //   y     = (W2[e] a) * s2,
 //   out_t = bf16_rn( sum over k ascending of g_k * y_k  (+ residual_t) ),
 // products accumulated in fp32 on the tensor cores, y and the sum in fp32;
@@ -11,8 +11,11 @@
 // twice by a token counts once, with the sum of its gates.  Id -1 (and an
 // id outside [-1, E), which raises the flag) is no expert.
 //
-// The activations are narrowed to bf16 because the tensor cores take them
-// in 16 bits beside the weights; one narrowing, before the gate.
+// The tensor cores take the activations in bf16 beside the weights.  They are
+// handed over as two of them, bf16_rn(a) and bf16_rn of what is left, which
+// keeps 16 significant bits: with few tokens the second product on the same
+// weight tile costs nothing beside reading the tile, and the output's own
+// narrowing stays the only rounding that shows (1.4 times its error without).
 //
 // GB300 design: every weight row of the experts in use is read once, and
 // nothing else is large, so the kernel is a stream of weight tiles at HBM's
@@ -25,8 +28,9 @@
 //   warp 4: weight producer (TMA, 128-byte swizzle);
 //   warp 5: tensor-memory owner and MMA issuer;
 //   warps 6-7: token rows into the stages (16-byte cp.async, swizzled alike);
-//   warps 8-11, 8-bit formats: widen a stage's weight rows to bf16 into
-//     tensor memory (exact), which the products read as their A operand.
+//   warps 8-15, 8-bit formats: two groups of four in turn widen a stage's
+//     weight rows to bf16 into tensor memory (exact), which the products read
+//     as their A operand.
 #include "kernels.h"
 #include "ptx.cuh"
 #include "smem_limit.h"
@@ -47,10 +51,11 @@ constexpr int kEpiThreads = 128;
 constexpr int kProducerWarp = 4, kMmaWarp = 5, kLoaderWarp0 = 6, kConvertWarp0 = 8;
 constexpr int kLoaderThreads = 64;
 constexpr int kHalfRows = 64;   // gate rows (and up rows) of a W13 tile
-constexpr int kLag = 2;         // stages whose token rows are in flight at once
 constexpr int kSlots = 4;       // widened weight tiles in tensor memory
 constexpr int kSlotCols = kBlockK / 2;
 constexpr int kMaxStages = 16;
+// dynamic shared memory: 227 KB a CTA less the static barriers and the exchange rows
+constexpr size_t kMaxDynamic = (227 - 6) * 1024;
 
 // Bytes of the lists at the front of dynamic shared memory.
 __host__ __device__ inline int lists_bytes(int E, int P) {
@@ -80,7 +85,7 @@ struct Lists {
 template <int FORMAT>
 struct Shape {
     static constexpr bool kWiden = FORMAT != MOE_FORMAT_BF16;
-    static constexpr int kThreads = (kWiden ? 12 : 8) * 32;
+    static constexpr int kThreads = (kWiden ? 16 : 8) * 32;
     static constexpr int kA = kTileRows * kBlockK * (kWiden ? 1 : 2);  // weight bytes a stage
     static constexpr int kCols = kWiden ? 512 : 128;                   // tensor-memory columns
 };
@@ -95,7 +100,7 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
     __shared__ uint64_t wide_full[kSlots], wide_free[kSlots];
     __shared__ uint64_t acc_full[2], acc_free[2], drained;
     __shared__ uint32_t s_taddr;
-    __shared__ int s_used, s_last;
+    __shared__ int s_used, s_most, s_last;
     __shared__ volatile int s_failed;
     __shared__ float s_up[16][kHalfRows];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -104,14 +109,8 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
     const Lists L(smem_raw, p.E, P);
     const uint32_t after = ptx::smem_u32(smem_raw) + lists_bytes(p.E, P);
     uint8_t *ring = smem_raw + lists_bytes(p.E, P) + ((1024u - (after & 1023u)) & 1023u);
-    const int b_bytes = p.nmax * kAtom * 2;  // two 64-wide halves of a unit's token rows
-    const int stage_bytes = S::kA + b_bytes;
-    const int stages = p.stages;
-    auto stage_a = [&](int s) { return ring + s * stage_bytes; };
-    auto stage_b = [&](int s) { return ring + s * stage_bytes + S::kA; };
-
     if (tid == 0) {
-        for (int s = 0; s < stages; ++s) {
+        for (int s = 0; s < kMaxStages; ++s) {
             ptx::mbar_init(&bar_a[s], 1);
             ptx::mbar_init(&bar_b[s], kLoaderThreads);
             ptx::mbar_init(&bar_free[s], 1);
@@ -160,7 +159,7 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
     }
     __syncthreads();
     if (warp == 0) {  // exclusive prefixes of the counts and of the experts in use
-        int used = 0, pairs = 0;
+        int used = 0, pairs = 0, most = 0;
         for (int e0 = 0; e0 < p.E; e0 += 32) {
             const int e = e0 + lane, c = e < p.E ? count[e] : 0;
             int s = c;
@@ -169,6 +168,7 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
                 if (lane >= o) s += v;
             }
             const unsigned m = __ballot_sync(0xffffffffu, c > 0);
+            most = max(most, c);
             if (c > 0) {
                 const int a = used + __popc(m & ((1u << lane) - 1u));
                 L.expert[a] = (uint16_t)e;
@@ -178,9 +178,11 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
             used += __popc(m);
             pairs += __shfl_sync(0xffffffffu, s, 31);
         }
+        most = __reduce_max_sync(0xffffffffu, most);
         if (lane == 0) {
             L.base[used] = (uint16_t)pairs;
             s_used = used;
+            s_most = most;
         }
     }
     __syncthreads();
@@ -199,6 +201,15 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
 
     const int A = s_used;
     const uint32_t taddr = s_taddr;
+    // A stage holds a unit's weights and the token rows of the fullest expert, in
+    // groups of 8, 64 columns at a time: two halves, and twice for the two terms
+    // of the activations.  (Products read 16 rows at a time: what they read past
+    // the rows only reaches columns that nobody reads.)
+    const int b_rows = (s_most + 7) / 8 * 8, b_half = b_rows * kAtom;
+    const int stage_bytes = S::kA + 4 * b_half;
+    const int stages = min(kMaxStages, p.ring_bytes / stage_bytes);
+    auto stage_a = [&](int s) { return ring + s * stage_bytes; };
+    auto stage_b = [&](int s) { return ring + s * stage_bytes + S::kA; };
     // phase 0: tiles (expert, 64 gate + 64 up rows); phase 1: (128 rows of H, expert)
     const int tiles0 = (p.I + kHalfRows - 1) / kHalfRows, tiles1 = (p.H + kTileRows - 1) / kTileRows;
     const int blocks0 = (p.H + kBlockK - 1) / kBlockK, blocks1 = (p.I + kBlockK - 1) / kBlockK;
@@ -215,8 +226,9 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
     };
 
     if (warp == kProducerWarp) {
-        if (lane == 0) {
-            uint32_t n = 0;
+        if (ptx::elect_one()) {
+            Turn st(stages);
+            uint32_t issued = 0;  // stages in use
             for (int phase = 0; phase < 2; ++phase) {
                 Segments segs(cuts[phase], cta, phase ? blocks1 : blocks0);
                 Segment sg;
@@ -227,12 +239,13 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
                     const void *map = phase ? (const void *)&map2 : (const void *)&map13;
                     const int row0 = phase ? e * p.H + r * kTileRows : e * 2 * p.I + r * kHalfRows;
                     const int row1 = phase ? row0 + kHalfRows : row0 + p.I;
-                    for (int kb = sg.k0; kb < sg.k1; ++kb, ++n) {
-                        const int s = (int)(n % stages);
-                        if (!ptx::mbar_wait_timed(&bar_free[s], ((n / stages) & 1u) ^ 1u, kWaitNs)) {
+                    for (int kb = sg.k0; kb < sg.k1; ++kb, st.next()) {
+                        const int s = (int)st.at;
+                        if (!ptx::mbar_wait_timed(&bar_free[s], st.parity ^ 1u, kWaitNs)) {
                             s_failed = 1;
                             break;
                         }
+                        issued |= 1u << s;
                         ptx::mbar_arrive_expect_tx(&bar_a[s], (uint32_t)S::kA);
                         uint8_t *dst = stage_a(s);
                         constexpr int kHalves = S::kWiden ? 1 : 2;
@@ -247,13 +260,15 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
                 }
             }
             // copies still in flight land before shared memory goes away
-            const uint32_t from = n > (uint32_t)stages ? n - stages : 0u;
-            for (uint32_t k = from; k < n; ++k)
-                ptx::mbar_wait_timed(&bar_a[k % stages], (k / stages) & 1u, kWaitNs);
+            for (int i = 0; i < stages; ++i, st.next()) {  // (parity: of the stage's last use)
+                const uint32_t last = st.parity ^ 1u;
+                if (issued >> st.at & 1u) ptx::mbar_wait_timed(&bar_a[st.at], last, kWaitNs);
+            }
         }
     } else if (warp == kMmaWarp) {
-        if (lane == 0) {
-            uint32_t n = 0, it = 0;
+        if (ptx::elect_one()) {
+            uint32_t it = 0;
+            Turn st(stages), wide(kSlots);
             for (int phase = 0; phase < 2; ++phase) {
                 Segments segs(cuts[phase], cta, phase ? blocks1 : blocks0);
                 Segment sg;
@@ -268,35 +283,43 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
                         break;
                     }
                     tc::fence_after_sync();
-                    for (int kb = sg.k0; kb < sg.k1; ++kb, ++n) {
-                        const int s = (int)(n % stages);
-                        bool ok = ptx::mbar_wait_timed(&bar_b[s], (n / stages) & 1u, kWaitNs);
+                    for (int kb = sg.k0; kb < sg.k1; ++kb, st.next(), wide.next()) {
+                        const int s = (int)st.at;
+                        bool ok = ptx::mbar_wait_timed(&bar_b[s], st.parity, kWaitNs);
                         if (S::kWiden)
-                            ok = ok && ptx::mbar_wait_timed(&wide_full[n % kSlots],
-                                                            (n / kSlots) & 1u, kWaitNs);
+                            ok = ok && ptx::mbar_wait_timed(&wide_full[wide.at], wide.parity,
+                                                            kWaitNs);
                         else
-                            ok = ok && ptx::mbar_wait_timed(&bar_a[s], (n / stages) & 1u, kWaitNs);
+                            ok = ok && ptx::mbar_wait_timed(&bar_a[s], st.parity, kWaitNs);
                         if (!ok) {
                             s_failed = 1;
                             break;
                         }
                         tc::fence_after_sync();
+                        // token rows: written by cp.async (generic proxy), read next by
+                        // the tensor cores (async proxy)
+                        ptx::fence_proxy_async_smem();
                         const uint64_t ad = tc::smem_desc_sw128(ptx::smem_u32(stage_a(s)));
                         const uint64_t bd = tc::smem_desc_sw128(ptx::smem_u32(stage_b(s)));
-                        const uint64_t half_a = kTileRows * kAtom / 16, half_b = p.nmax * kAtom / 16;
-                        const uint32_t at = taddr + 2 * kLayerMaxTokens + (n % kSlots) * kSlotCols;
+                        const uint64_t half_a = kTileRows * kAtom / 16, half_b = b_half / 16;
+                        const uint32_t at = taddr + 2 * kLayerMaxTokens + wide.at * kSlotCols;
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk) {  // 16 k a step
                             const uint64_t bk = bd + (kk >> 2) * half_b + 2 * (kk & 3);
                             const bool acc = kb != sg.k0 || kk != 0;
+                            const uint64_t ak = ad + (kk >> 2) * half_a + 2 * (kk & 3);
                             if constexpr (S::kWiden)
                                 tc::mma_f16_ta(d, at + 8 * kk, bk, idesc, acc);
                             else
-                                tc::mma_bf16(d, ad + (kk >> 2) * half_a + 2 * (kk & 3), bk, idesc,
-                                             acc);
+                                tc::mma_bf16(d, ak, bk, idesc, acc);
+                            if (phase == 0) continue;
+                            if constexpr (S::kWiden)  // the second term
+                                tc::mma_f16_ta(d, at + 8 * kk, bk + 2 * half_b, idesc, true);
+                            else
+                                tc::mma_bf16(d, ak, bk + 2 * half_b, idesc, true);
                         }
                         tc::commit(&bar_free[s]);
-                        if (S::kWiden) tc::commit(&wide_free[n % kSlots]);
+                        if (S::kWiden) tc::commit(&wide_free[wide.at]);
                     }
                     tc::commit(&acc_full[b]);
                 }
@@ -307,21 +330,14 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
     } else if (warp == kLoaderWarp0 || warp == kLoaderWarp0 + 1) {
         // Thread l copies 16-byte piece l % 16 (8 values) of the rows l / 16,
         // l / 16 + 4, ... of a unit: half (piece / 8), chunk piece % 8 stored at
-        // chunk ^ (row mod 8), the swizzle that TMA would apply.  A stage is
-        // handed over kLag stages later, when its copies have landed.
+        // chunk ^ (row mod 8), the swizzle that TMA would apply.
         const int l = tid - kLoaderWarp0 * 32, piece = l & 15, row0 = l >> 4;
-        uint32_t n = 0, told = 0;
-        auto tell = [&](uint32_t upto) {  // copies of stages < upto have landed
-            ptx::fence_proxy_async_smem();
-            for (; told < upto; ++told) mbar_arrive(&bar_b[told % stages]);
-        };
+        Turn st(stages);
         for (int phase = 0; phase < 2; ++phase) {
             const int width = phase ? p.I : p.H;
             Segments segs(cuts[phase], cta, phase ? blocks1 : blocks0);
             Segment sg;
             if (phase == 1) {
-                ptx::cp_async_wait_all();
-                tell(n);
                 // every activation is written before any is read
                 bool ok = true;
                 if (lane == 0) ok = wait_count(&p.header->done[0], A * tiles0, &s_failed);
@@ -331,43 +347,47 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
                 int a, r;
                 tile_of(phase, sg.tile, a, r);
                 const int base = L.base[a], rows = L.base[a + 1] - base;
-                const uint16_t *src = phase ? p.act + (size_t)base * p.I : p.x;
-                for (int kb = sg.k0; kb < sg.k1; ++kb, ++n) {
-                    const int s = (int)(n % stages);
-                    if (!__all_sync(0xffffffffu,
-                                    ptx::mbar_wait_timed(&bar_free[s], ((n / stages) & 1u) ^ 1u,
-                                                         kWaitNs))) {
+                const uint16_t *src = phase ? p.act + (size_t)base * 2 * p.I : p.x;
+                for (int kb = sg.k0; kb < sg.k1; ++kb, st.next()) {
+                    const int s = (int)st.at;
+                    if (!__all_sync(0xffffffffu, ptx::mbar_wait_timed(
+                                                     &bar_free[s], st.parity ^ 1u, kWaitNs))) {
                         s_failed = 1;
                         break;
                     }
-                    uint8_t *dst = stage_b(s) + (piece >> 3) * p.nmax * kAtom;
+                    uint8_t *dst = stage_b(s) + (piece >> 3) * b_half;
                     const int col = kb * kBlockK + piece * 8;
                     for (int row = row0; row < rows; row += 4) {
-                        const size_t off = (size_t)(phase ? row : L.token[base + row]) * width + col;
+                        const size_t at = (size_t)(phase ? 2 * row : L.token[base + row]) * width;
                         uint8_t *to = dst + row * kAtom + (((piece & 7) ^ (row & 7)) << 4);
-                        if (col < width)
-                            ptx::cp_async16(to, src + off);
-                        else  // past the end: zero, beside the weights' zero fill
-                            *reinterpret_cast<uint4 *>(to) = make_uint4(0, 0, 0, 0);
+                        if (col < width) {
+                            ptx::cp_async16(to, src + at + col);
+                            if (phase) ptx::cp_async16(to + 2 * b_half, src + at + width + col);
+                        } else {  // past the end: zero, beside the weights' zero fill
+                            ptx::cp_async16_zero(to, src);
+                            if (phase) ptx::cp_async16_zero(to + 2 * b_half, src);
+                        }
                     }
-                    ptx::cp_async_commit();
-                    ptx::cp_async_wait<kLag>();
-                    if (n >= kLag) tell(n - kLag + 1);
+                    ptx::cp_async_mbar_arrive_noinc(&bar_b[s]);
                 }
             }
         }
-        ptx::cp_async_wait_all();
-        tell(n);
+        ptx::cp_async_wait_all();  // copies land before shared memory goes away
     } else if (S::kWiden && warp >= kConvertWarp0) {
-        // Thread l of the four warps owns weight row l of the tile = lane l.
-        const int row = tid - kConvertWarp0 * 32;
+        // Thread l of a group owns weight row l of the tile = lane l; the groups
+        // take the units in turn, so that one group's loads and waits pass while
+        // the other computes.
+        const int row = (tid - kConvertWarp0 * 32) & 127, group = (warp - kConvertWarp0) >> 2;
         long long units = 0;
         for (int phase = 0; phase < 2; ++phase)
             if (cta < cuts[phase].parts) units += cuts[phase].first(cta + 1) - cuts[phase].first(cta);
-        for (uint32_t n = 0; n < (uint32_t)units && !warp_flag(&s_failed); ++n) {
-            const int s = (int)(n % stages), q = (int)(n % kSlots);
-            const bool ok = ptx::mbar_wait_timed(&bar_a[s], (n / stages) & 1u, kWaitNs) &&
-                            ptx::mbar_wait_timed(&wide_free[q], ((n / kSlots) & 1u) ^ 1u, kWaitNs);
+        Turn st(stages), wide(kSlots);
+        for (uint32_t n = 0; n < (uint32_t)units; ++n, st.next(), wide.next()) {
+            if ((n & 1u) != (uint32_t)group) continue;
+            if (warp_flag(&s_failed)) break;
+            const int s = (int)st.at, q = (int)wide.at;
+            const bool ok = ptx::mbar_wait_timed(&bar_a[s], st.parity, kWaitNs) &&
+                            ptx::mbar_wait_timed(&wide_free[q], wide.parity ^ 1u, kWaitNs);
             if (!__all_sync(0xffffffffu, ok)) {
                 s_failed = 1;
                 break;
@@ -460,7 +480,8 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
                     limit = p.H;
                     scales = p.w2_scale + (size_t)e * p.H;
                 }
-                const float sc = S::kWiden && chan < limit ? __ldg(scales + chan) : 1.0f;
+                float sc = S::kWiden && chan < limit ? __ldg(scales + chan) : 1.0f;
+                if (FORMAT == MOE_FORMAT_INT8) sc *= kInt8Bf16;
                 for (int n0 = 0; n0 < rows; n0 += 16) {
                     float v[16];
                     if (whole) {
@@ -492,9 +513,14 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
                             for (int i = 0; i < 16; ++i)
                                 if (n0 + i < rows) {
                                     const float z = v[i] / (1.0f + expf(-v[i])) * s_up[i][tid];
-                                    __nv_bfloat16 h = __float2bfloat16_rn(z);
-                                    p.act[(size_t)(base + n0 + i) * p.I + chan] =
-                                        *reinterpret_cast<uint16_t *>(&h);
+                                    const __nv_bfloat16 hi = __float2bfloat16_rn(z);
+                                    const float zh = __bfloat162float(hi);
+                                    // (nothing is left of an infinity)
+                                    const __nv_bfloat16 lo = __float2bfloat16_rn(
+                                        isinf(zh) ? 0.0f : z - zh);
+                                    uint16_t *to = p.act + (size_t)(base + n0 + i) * 2 * p.I + chan;
+                                    to[0] = *reinterpret_cast<const uint16_t *>(&hi);
+                                    to[p.I] = *reinterpret_cast<const uint16_t *>(&lo);
                                 }
                         }
                         epi_sync();
@@ -549,6 +575,7 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
         }
     }
 
+    __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
     if (tid == 0) {
@@ -571,17 +598,14 @@ cudaError_t launch_t(LayerSmallParams &p, int num_sms, cudaStream_t st) {
     if (!make_map(&m13, p.w13, (long long)p.E * 2 * p.I, p.H, kHalfRows, S::kWiden) ||
         !make_map(&m2, p.w2, (long long)p.E * p.H, p.I, kHalfRows, S::kWiden))
         return cudaErrorInvalidValue;
-    const int front = lists_bytes(p.E, p.T * p.K) + 1024;
-    const int stage = S::kA + p.nmax * kAtom * 2;
-    // 227 KB a CTA less the static barriers and the exchange rows
-    int stages = (227 * 1024 - 6 * 1024 - front) / stage;
-    if (stages > kMaxStages) stages = kMaxStages;
-    if (stages < kLag + 2) return cudaErrorInvalidValue;
+    // 1 KB aligns the ring and 1 KB stands behind it (reads of 16 rows where there are 8)
+    const int front = lists_bytes(p.E, p.T * p.K) + 2048;
+    p.ring_bytes = (int)kMaxDynamic - front;
     // the lists are built where the ring will be
-    if (2 * p.E * (int)sizeof(int) > stages * stage) return cudaErrorInvalidValue;
-    p.stages = stages;
-    const size_t smem = (size_t)front + (size_t)stages * stage;
-    cudaError_t err = raise_smem_limit(layer_small_kernel<FORMAT>, smem);
+    if (2 * p.E * (int)sizeof(int) > p.ring_bytes) return cudaErrorInvalidValue;
+    const size_t smem = (size_t)front + (size_t)p.ring_bytes;
+    static std::atomic<unsigned long long> raised{0};
+    cudaError_t err = raise_smem_limit_once(layer_small_kernel<FORMAT>, kMaxDynamic, raised);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(num_sms < kStreamMaxCtas ? num_sms : kStreamMaxCtas));

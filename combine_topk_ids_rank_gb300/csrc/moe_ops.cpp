@@ -42,7 +42,7 @@ struct LayerScratch {
     LayerScratch(int T, int K, int H, int I) {
         const size_t pairs = (size_t)T * K;
         act = kStreamHeaderBytes;
-        y = act + up256(pairs * I * 2);
+        y = act + up256(pairs * I * 4);
         part = y + up256(pairs * H * 4);
         total = part + part_bytes((T + 15) / 16 * 16);
     }
@@ -204,7 +204,7 @@ int moe_layer_small(const void *d_x, const int32_t *d_topk_ids, const float *d_t
     p.H = hidden;
     p.I = inter;
     p.format = format;
-    p.nmax = p.stages = 0;
+    p.nmax = p.ring_bytes = 0;
     return launch_layer_small(p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? MOE_OK
                : cuda_failed();

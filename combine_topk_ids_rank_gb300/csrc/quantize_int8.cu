@@ -52,53 +52,86 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], const fp8::RowScale
     return o;
 }
 
+// Eight elements of a row as loaded: one 16-byte vector of bf16, two of fp32.
 template <bool BF16>
-__device__ __forceinline__ void load8(const void *row, int v, float (&f)[8]) {
-    if (BF16) {
-        const uint4 u = __ldg(static_cast<const uint4 *>(row) + v);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Vec8 {
+    uint4 v[BF16 ? 1 : 2];
+    __device__ __forceinline__ void load(const uint4 *row, int i) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-    } else {
-        const float4 a = __ldg(static_cast<const float4 *>(row) + 2 * v);
-        const float4 b = __ldg(static_cast<const float4 *>(row) + 2 * v + 1);
-        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-        f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+        for (int k = 0; k < (BF16 ? 1 : 2); ++k) v[k] = __ldcs(row + i * (BF16 ? 1 : 2) + k);
     }
-}
+    // bits of the largest |x| (NaN above infinity above every number)
+    __device__ __forceinline__ uint32_t most() const {
+        if (BF16) {  // two 16-bit lanes at a time
+            const uint32_t k = 0x7fff7fffu;
+            const uint32_t a = __vmaxu2(__vmaxu2(v[0].x & k, v[0].y & k),
+                                        __vmaxu2(v[0].z & k, v[0].w & k));
+            return max(a << 16, a & 0xffff0000u);
+        } else {
+            const uint32_t k = 0x7fffffffu;
+            const uint32_t a = max(max(v[0].x & k, v[0].y & k), max(v[0].z & k, v[0].w & k));
+            const uint4 w = v[BF16 ? 0 : 1];
+            return max(a, max(max(w.x & k, w.y & k), max(w.z & k, w.w & k)));
+        }
+    }
+    __device__ __forceinline__ void values(float (&f)[8]) const {
+        if (BF16) {
+            const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[2 * i] = __uint_as_float(w[i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        } else {
+            const uint4 b = v[BF16 ? 0 : 1];
+            const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+        }
+    }
+};
 
-// One CTA a row; thread i takes the 8-element vectors i, i + threads, ...
+// One CTA a row; thread i takes the 8-element vectors i, i + threads, ...  The
+// next row's loads are in flight while this row is reduced and stored.
 template <int VPT, bool BF16>
 __global__ void __launch_bounds__(kMaxWarps * 32) quantize_int8_kernel(const QuantInt8Params p) {
     __shared__ uint32_t red[2][kMaxWarps];
     const int tid = threadIdx.x, nt = blockDim.x, H8 = p.H / 8;
     const long long total = (long long)p.groups * p.rows;
-    int turn = 0;
-    for (long long r = blockIdx.x; r < total; r += gridDim.x) {
-        if (p.counts != nullptr) {
+    // the first row from r on that is in use (the whole CTA alike)
+    auto used = [&](long long r) {
+        if (p.counts == nullptr) return r;
+        for (; r < total; r += gridDim.x) {
             const long long g = r / p.rows;
-            if (r - g * p.rows >= __ldg(p.counts + g)) continue;  // (the whole CTA alike)
+            if (r - g * p.rows < __ldg(p.counts + g)) break;
         }
-        const char *row = static_cast<const char *>(p.x) + r * p.row_stride * (BF16 ? 2 : 4);
-        float f[VPT][8];
-        uint32_t m = 0;  // bits of |x|: NaN above infinity above every number
+        return r;
+    };
+    auto load = [&](Vec8<BF16> (&x)[VPT], long long r) {
+        const uint4 *row = reinterpret_cast<const uint4 *>(
+            static_cast<const char *>(p.x) + r * p.row_stride * (BF16 ? 2 : 4));
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int v = tid + j * nt;
-            if (v < H8) {
-                load8<BF16>(row, v, f[j]);
+        for (int j = 0; j < VPT; ++j)
+            if (tid + j * nt < H8) x[j].load(row, tid + j * nt);
+    };
+    Vec8<BF16> next[VPT];
+    long long r = used(blockIdx.x);
+    if (r < total) load(next, r);
+    for (int turn = 0; r < total; turn ^= 1) {
+        Vec8<BF16> x[VPT];
+        uint32_t m = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[j][i]) & 0x7fffffffu);
+        for (int j = 0; j < VPT; ++j)
+            if (tid + j * nt < H8) {
+                x[j] = next[j];
+                m = max(m, x[j].most());
             }
-        }
+        const long long after = used(r + gridDim.x);
+        if (after < total) load(next, after);
         m = __reduce_max_sync(kFull, m);
         if ((tid & 31) == 0) red[turn][tid >> 5] = m;
         __syncthreads();
         for (int w = 0; w < nt / 32; ++w) m = max(m, red[turn][w]);
-        turn ^= 1;
         const bool finite = m < 0x7f800000u;
         const fp8::RowScale s = int8_scale(finite ? __uint_as_float(m) : 0.0f);
         uint2 *q = reinterpret_cast<uint2 *>(p.q + r * p.H);
@@ -106,12 +139,15 @@ __global__ void __launch_bounds__(kMaxWarps * 32) quantize_int8_kernel(const Qua
         for (int j = 0; j < VPT; ++j) {
             const int v = tid + j * nt;
             if (v < H8) {
+                float f[8];
+                x[j].values(f);
                 uint2 o = make_uint2(0, 0);
-                if (finite) o = s.m == 1.0f ? codes8<false>(f[j], s) : codes8<true>(f[j], s);
+                if (finite) o = s.m == 1.0f ? codes8<false>(f, s) : codes8<true>(f, s);
                 q[v] = o;
             }
         }
         if (tid == 0) p.scale[r] = finite ? s.s : __uint_as_float(0x7fc00000u);
+        r = after;
     }
 }
 

@@ -89,6 +89,19 @@ __device__ __forceinline__ int ld_acquire(const int *p) {
     return v;
 }
 
+// Position in a ring of `size` barriers that a role walks through: the index
+// and the parity of the phase that the role's next use of it completes.
+struct Turn {
+    uint32_t at, parity, size;
+    __device__ explicit Turn(uint32_t size_) : at(0), parity(0), size(size_) {}
+    __device__ void next() {
+        if (++at == size) {
+            at = 0;
+            parity ^= 1u;
+        }
+    }
+};
+
 // Wait until *p reaches `want` (it only grows meanwhile); false on timeout or
 // when another role of this CTA has failed.
 __device__ __forceinline__ bool wait_count(const int *p, int want, volatile int *failed) {
@@ -129,14 +142,17 @@ __device__ __forceinline__ bool warp_flag(const volatile int *f) {
 
 // ---- four 8-bit codes -> four 16-bit values (two words, ascending) -----------
 
-// int8 -> bf16, exact: the low 7 bits ride on 128 (0x4300, one unit apart),
-// the sign bit turns the subtracted 128 into 256 (0x4380).
+// int8 -> bf16, exact up to the power of two kInt8Bf16: a 16-bit lane that
+// holds the integer u = code + 128, read as bf16, is u * 2^-133 for all of
+// 0..255 (bf16's subnormals run on into its smallest normals), so one fused
+// multiply-add by 2^127 gives code * 2^-6.
+constexpr float kInt8Bf16 = 64.0f;  // what the sums are multiplied by in turn
 __device__ __forceinline__ void int8_to_bf16(uint32_t v, uint32_t &a, uint32_t &b) {
-    const uint32_t lo = v & 0x7f7f7f7fu, hi = v & 0x80808080u;
-    const uint32_t la = __byte_perm(lo, 0x43434343u, 0x5140), lb = __byte_perm(lo, 0x43434343u, 0x7362);
-    const uint32_t ha = __byte_perm(hi, 0x43434343u, 0x5140), hb = __byte_perm(hi, 0x43434343u, 0x7362);
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(la), "r"(ha));
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(lb), "r"(hb));
+    const uint32_t u = v ^ 0x80808080u;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;"
+        : "=r"(a) : "r"(__byte_perm(u, 0, 0x4140)), "r"(0x7f007f00u), "r"(0xc000c000u));  // - 2
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;"
+        : "=r"(b) : "r"(__byte_perm(u, 0, 0x4342)), "r"(0x7f007f00u), "r"(0xc000c000u));
 }
 
 // int8 -> f16, exact: code + 128 rides on 1024 (0x6400, one unit apart).
@@ -147,24 +163,23 @@ __device__ __forceinline__ void int8_to_f16(uint32_t v, uint32_t &a, uint32_t &b
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(b) : "r"(ub), "r"(0x64806480u));
 }
 
-// e4m3 -> bf16, exact: the code's exponent and mantissa moved into bf16's
-// fields are 2^-120 times the value, also for e4m3's subnormals; the codes
-// 0x7f and 0xff are NaN.
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t w) {  // codes in the high bytes
-    const uint32_t m = ((w & 0x7f007f00u) >> 4) | (w & 0x80008000u);
+// e4m3 -> bf16, exact, through f16 and fp32 (NaN stays NaN).
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t two_codes) {
     uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(0x7b807b80u));  // 2^120
+    asm("{\n\t.reg .b16 c, l, h;\n\t.reg .b32 p;\n\t.reg .f32 x, y;\n\t"
+        "cvt.u16.u32 c, %1;\n\t"
+        "cvt.rn.f16x2.e4m3x2 p, c;\n\t"
+        "mov.b32 {l, h}, p;\n\t"
+        "cvt.f32.f16 x, l;\n\t"
+        "cvt.f32.f16 y, h;\n\t"
+        "cvt.rn.bf16x2.f32 %0, y, x;\n\t}"
+        : "=r"(r)
+        : "r"(two_codes));
     return r;
 }
 __device__ __forceinline__ void e4m3_to_bf16(uint32_t v, uint32_t &a, uint32_t &b) {
-    a = e4m3_pair(__byte_perm(v, 0, 0x1404));
-    b = e4m3_pair(__byte_perm(v, 0, 0x3424));
-    if (((v & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) {  // a NaN among the four
-        if ((v & 0x7fu) == 0x7fu) a = (a & 0xffff0000u) | 0x7fffu;
-        if ((v & 0x7f00u) == 0x7f00u) a = (a & 0xffffu) | 0x7fff0000u;
-        if ((v & 0x7f0000u) == 0x7f0000u) b = (b & 0xffff0000u) | 0x7fffu;
-        if ((v & 0x7f000000u) == 0x7f000000u) b = (b & 0xffffu) | 0x7fff0000u;
-    }
+    a = e4m3_pair(v);
+    b = e4m3_pair(v >> 16);
 }
 
 }  // namespace stream

@@ -12,9 +12,15 @@
 // Both scores grow with the logit, so the logits themselves are compared,
 // as order-preserving 32-bit integers; the weights are fp32 throughout.
 //
-// GB300 design: one warp per token, the row in registers (VPL values a
-// lane), K rounds of a warp-wide integer maximum (redux.sync) over the
-// lanes' own maxima; the winner lane drops its value and looks again.
+// GB300 design: one warp per token, the row in registers (VPL consecutive
+// experts a lane, 16-byte loads), the selection in integers.  K rounds of a
+// warp-wide maximum (redux.sync) over the lanes' heads; ties between lanes go
+// to the lowest lane, which holds the lowest ids.
+//   bf16 logits: key and id share one word (16 + 16 bits), so a lane sorts
+//     its values once (a network of 2-instruction exchanges) and a round only
+//     shifts the winner's list;
+//   fp32 logits: the key fills the word; the winner lane clears the first
+//     value equal to the maximum and looks for its next.
 #include "layer.h"
 
 #include <cuda_bf16.h>
@@ -36,67 +42,157 @@ __device__ __forceinline__ float logit_of(uint32_t k) {
     return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
-template <bool BF16>
-__device__ __forceinline__ float load(const void *p, long long i) {
-    if (BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
-    return static_cast<const float *>(p)[i];
+// The lane's VPL logits, experts lane * VPL + j; -inf past E.
+template <int VPL, bool BF16, bool VEC>
+__device__ __forceinline__ void load_row(const TopkGateParams &p, long long t, int lane,
+                                         float (&l)[VPL]) {
+    const int e0 = lane * VPL;
+    if (VEC && e0 + VPL <= p.E) {
+        if (BF16) {
+            const uint16_t *row = static_cast<const uint16_t *>(p.logits) + t * p.row_stride + e0;
+            uint32_t w[(VPL + 1) / 2];
+            if constexpr (VPL >= 8) {
+#pragma unroll
+                for (int j = 0; j < VPL / 8; ++j) {
+                    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row) + j);
+                    w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
+                }
+            } else if constexpr (VPL == 4) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(row));
+                w[0] = v.x, w[1] = v.y;
+            } else {
+                w[0] = __ldg(reinterpret_cast<const uint32_t *>(row));
+            }
+#pragma unroll
+            for (int j = 0; j < VPL / 2; ++j) {
+                l[2 * j] = __uint_as_float(w[j] << 16);
+                l[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+            }
+        } else {
+            const float *row = static_cast<const float *>(p.logits) + t * p.row_stride + e0;
+            if constexpr (VPL >= 4) {
+#pragma unroll
+                for (int j = 0; j < VPL / 4; ++j) {
+                    const float4 v = __ldg(reinterpret_cast<const float4 *>(row) + j);
+                    l[4 * j] = v.x, l[4 * j + 1] = v.y, l[4 * j + 2] = v.z, l[4 * j + 3] = v.w;
+                }
+            } else {
+                const float2 v = __ldg(reinterpret_cast<const float2 *>(row));
+                l[0] = v.x, l[1] = v.y;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            const int e = e0 + j;
+            const long long at = t * p.row_stride + e;
+            if (e >= p.E)
+                l[j] = -INFINITY;
+            else if (BF16)
+                l[j] = __bfloat162float(static_cast<const __nv_bfloat16 *>(p.logits)[at]);
+            else
+                l[j] = static_cast<const float *>(p.logits)[at];
+        }
+    }
 }
 
-template <int VPL, bool BF16>
+// Sorts descending.
+template <int VPL>
+__device__ __forceinline__ void sort_down(uint32_t (&k)[VPL]) {
+    auto exchange = [&](int a, int b) {
+        const uint32_t hi = max(k[a], k[b]), lo = min(k[a], k[b]);
+        k[a] = hi;
+        k[b] = lo;
+    };
+    if constexpr (VPL == 2) {
+        exchange(0, 1);
+    } else if constexpr (VPL == 4) {
+        exchange(0, 1), exchange(2, 3), exchange(0, 2), exchange(1, 3), exchange(1, 2);
+    } else {  // Batcher's odd-even merge network for eight, 19 exchanges
+        exchange(0, 1), exchange(2, 3), exchange(4, 5), exchange(6, 7);
+        exchange(0, 2), exchange(1, 3), exchange(4, 6), exchange(5, 7);
+        exchange(1, 2), exchange(5, 6);
+        exchange(0, 4), exchange(1, 5), exchange(2, 6), exchange(3, 7);
+        exchange(2, 4), exchange(3, 5);
+        exchange(1, 2), exchange(3, 4), exchange(5, 6);
+    }
+}
+
+template <int VPL, bool BF16, bool VEC>
 __global__ void __launch_bounds__(kThreads) topk_gate_kernel(const TopkGateParams p) {
     const int lane = threadIdx.x & 31;
     const long long warps = (long long)gridDim.x * (kThreads / 32);
     for (long long t = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
          t < p.tokens; t += warps) {
+        float l[VPL];
+        load_row<VPL, BF16, VEC>(p, t, lane, l);
         uint32_t key[VPL];
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
-            const int e = j * 32 + lane;
-            key[j] = e < p.E ? key_of(load<BF16>(p.logits, t * p.row_stride + e)) : 0u;
+            key[j] = key_of(l[j]);
+            if (BF16 && key[j] != 0)  // the low half is free: lower ids are larger
+                key[j] = (key[j] & 0xffff0000u) | (uint32_t)(0xffff - lane * VPL - j);
         }
         float total = 0.0f;  // softmax over the whole row, where it is asked for
         if (!p.sigmoid && !p.renormalize) {
-            uint32_t m = 0;
+            float m = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < VPL; ++j) m = max(m, key[j]);
-            const float lm = logit_of(__reduce_max_sync(kFull, m));
+            for (int j = 0; j < VPL; ++j) m = fmaxf(m, l[j]);  // (drops NaN)
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
 #pragma unroll
-            for (int j = 0; j < VPL; ++j) {
-                const float l = logit_of(key[j]);
-                if (key[j] != 0) total += l == lm ? 1.0f : expf(l - lm);
-            }
+            for (int j = 0; j < VPL; ++j)
+                if (key[j] != 0) total += l[j] == m ? 1.0f : expf(l[j] - m);
             for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
         }
         uint32_t sel_key = 0;  // lane k holds selection k
         int sel_id = -1;
+        constexpr bool kSorted = BF16 && VPL <= 8;
+        if constexpr (kSorted) sort_down<VPL>(key);
         for (int k = 0; k < p.K; ++k) {
-            uint32_t best = 0;
-            int at = 0;
+            uint32_t best = key[0];
+            if constexpr (!kSorted) {
 #pragma unroll
-            for (int j = 0; j < VPL; ++j)
-                if (key[j] > best) {
-                    best = key[j];
-                    at = j;
-                }
+                for (int j = 1; j < VPL; ++j) best = max(best, key[j]);
+            }
             const uint32_t m = __reduce_max_sync(kFull, best);
             if (m == 0) break;
-            const int id = best == m ? at * 32 + lane : INT32_MAX;
-            const int win = __reduce_min_sync(kFull, id);
+            if constexpr (BF16) {  // keys are unique
+                if constexpr (kSorted) {
+                    if (best == m) {
 #pragma unroll
-            for (int j = 0; j < VPL; ++j)
-                if (j * 32 + lane == win) key[j] = 0;
-            if (lane == k) {
-                sel_key = m;
-                sel_id = win;
+                        for (int j = 0; j + 1 < VPL; ++j) key[j] = key[j + 1];
+                        key[VPL - 1] = 0;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < VPL; ++j) key[j] = key[j] == m ? 0u : key[j];
+                }
+                if (lane == k) {
+                    sel_key = m | 0xffffu;
+                    sel_id = (int)(0xffffu - (m & 0xffffu));
+                }
+            } else {
+                const int src = __ffs(__ballot_sync(kFull, best == m)) - 1;
+                int at = 0;  // the first value equal to the maximum, in the winner lane
+#pragma unroll
+                for (int j = VPL - 1; j >= 0; --j) at = key[j] == m ? j : at;
+#pragma unroll
+                for (int j = 0; j < VPL; ++j)
+                    if (lane == src && at == j) key[j] = 0;
+                const int id = src * VPL + __shfl_sync(kFull, at, src);
+                if (lane == k) {
+                    sel_key = m;
+                    sel_id = id;
+                }
             }
         }
+        // (a bf16 key's low half is the sign's: 0 under a positive key, all ones
+        // under the complement of a negative one)
+        if (BF16 && sel_key >= 0x80000000u) sel_key &= 0xffff0000u;
         float s = 0.0f;
-        const float l0 = logit_of(__shfl_sync(kFull, sel_key, 0));
-        if (sel_id >= 0) {
-            const float l = logit_of(sel_key);
-            // (equal to the maximum: also for +inf, whose difference is NaN)
-            s = p.sigmoid ? 1.0f / (1.0f + expf(-l)) : (l == l0 ? 1.0f : expf(l - l0));
-        }
+        const float v = logit_of(sel_key), l0 = __shfl_sync(kFull, v, 0);
+        if (sel_id >= 0)  // (equal to the maximum: also for +inf, whose difference is NaN)
+            s = p.sigmoid ? 1.0f / (1.0f + expf(-v)) : (v == l0 ? 1.0f : expf(v - l0));
         float sum = total;
         if (p.renormalize) {
             sum = s;
@@ -114,10 +210,15 @@ template <int VPL>
 cudaError_t launch_t(const TopkGateParams &p, int num_sms, cudaStream_t st) {
     const long long want = (p.tokens + kThreads / 32 - 1) / (kThreads / 32);
     const int grid = (int)(want < num_sms * 8LL ? want : num_sms * 8LL);
-    if (p.bf16)
-        topk_gate_kernel<VPL, true><<<grid, kThreads, 0, st>>>(p);
-    else
-        topk_gate_kernel<VPL, false><<<grid, kThreads, 0, st>>>(p);
+    // whole vectors a lane, where every row starts on one
+    const uintptr_t vec = VPL * (p.bf16 ? 2 : 4) < 16 ? VPL * (p.bf16 ? 2 : 4) : 16;
+    const bool aligned = reinterpret_cast<uintptr_t>(p.logits) % vec == 0 &&
+                         (uintptr_t)(p.row_stride * (p.bf16 ? 2 : 4)) % vec == 0;
+    auto kern = p.bf16 ? (aligned ? topk_gate_kernel<VPL, true, true>
+                                  : topk_gate_kernel<VPL, true, false>)
+                       : (aligned ? topk_gate_kernel<VPL, false, true>
+                                  : topk_gate_kernel<VPL, false, false>);
+    kern<<<grid, kThreads, 0, st>>>(p);
     return cudaGetLastError();
 }
 

@@ -539,10 +539,11 @@ int moe_gemm_int8(const int8_t *d_xq, const float *d_x_scale, const int8_t *d_wq
  * A mixture-of-experts layer of gated two-layer experts in one kernel, for
  * batches too small for receive planes (at most MOE_LAYER_MAX_TOKENS tokens):
  *   h   = W13[e] x_t * s13[e]      rows 0..I-1 the gate, I..2I-1 the up part,
- *   a   = bf16_rn( silu(h_gate) * h_up ),  silu(z) = z / (1 + exp(-z)),
+ *   a   = silu(h_gate) * h_up,     silu(z) = z / (1 + exp(-z)),
  *   y_k = (W2[e] a) * s2[e],       e = topk_ids[t][k],
  *   out[t] = bf16_rn( sum over k ascending of topk_w[t][k] * y_k (+ residual[t]) ),
- * fp32 accumulation and sum.  Id -1 is no expert; an id outside [-1, E) is
+ * fp32 accumulation and sum; a is carried in two bf16 terms (16 significant
+ * bits).  Id -1 is no expert; an id outside [-1, E) is
  * skipped and raises the flag; a token that names an expert twice gets it
  * once with the sum of the gates; a token without an expert gets 0 (or its
  * residual).
