@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int waves = tiles / ctas;
     if (waves > 0 && tiles % ctas != 0 && tiles % ctas * 4 < ctas) --waves;
     const int cut_tiles = tiles - waves * ctas;
-    const Cut ct = cut((long long)cut_tiles * blocks, ctas);
+    const Cut ct = cut(cut_tiles, blocks, ctas, 4, ring.nmax <= 32 ? kAlone : 16);
     const int nacc = 2 * ring.nmax <= kMaxCols ? 2 : 1;  // accumulators
     const uint32_t slots_at = taddr + kMaxCols;
 
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             T.of(sg.tile, g, r, m0, rows);
             const uint32_t acc = taddr + b * ring.nmax + ((uint32_t)(tid & ~31) << 16);
             const bool whole = sg.k0 == 0 && sg.k1 == blocks;
-            const Parts parts(whole ? Cut{blocks, 1} : ct, whole ? 0 : sg.tile, blocks);
+            const Parts parts(whole ? Cut(1, 1, blocks) : ct, whole ? 0 : sg.tile, blocks);
             auto part_of = [&](int c) {
                 return p.part + ((size_t)(2 * c + parts.slot(c)) * p.nmax) * kTileRows + tid;
             };
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __threadfence();
                 epi_sync();
                 if (tid == 0) {
-                    int *m = &p.header->merged[0][parts.c0];
+                    int *m = &p.header->merged[0][parts.c0][0];
                     s_last = atomicAdd(m, 1) == parts.count() - 1;
                     if (s_last) *m = 0;  // for the next call
                 }

@@ -42,13 +42,14 @@ cudaError_t launch_quantize_rows_int8(const QuantInt8Params &p, int num_sms, cud
 // Device memory that the two persistent kernels keep between their CTAs.
 // The header is zero between calls (the kernels leave it so).
 constexpr int kStreamMaxCtas = 192;      // CTAs of a persistent launch, at most
-constexpr size_t kStreamHeaderBytes = 4096;
+constexpr size_t kStreamHeaderBytes = 8192;
 struct StreamHeader {
     uint32_t flags;                      // sticky MOE_DEVICE_FLAG_* bits
-    int32_t done[2];                     // finished output tiles of a phase
+    int32_t done[2];                     // finished quarters of output tiles, by phase
     int32_t left;                        // CTAs that are through with the counters
     int32_t pad[12];
-    int32_t merged[2][kStreamMaxCtas];   // finished parts of the tile that CTA c began
+    int32_t merged[2][kStreamMaxCtas][4];  // finished parts of the cut tile that CTA c
+                                           // began, by quarter of its rows (warp)
 };
 static_assert(sizeof(StreamHeader) <= kStreamHeaderBytes, "header");
 

@@ -48,33 +48,42 @@ namespace {
 using namespace stream;
 
 constexpr int kEpiThreads = 128;
+constexpr int kCols = 8;        // token columns an epilogue step takes
 constexpr int kProducerWarp = 4, kMmaWarp = 5, kLoaderWarp0 = 6, kConvertWarp0 = 8;
 constexpr int kLoaderThreads = 64;
 constexpr int kHalfRows = 64;   // gate rows (and up rows) of a W13 tile
+constexpr int kQuarter = 16;    // of them in a warp's 32 lanes: 16 gate rows, then 16 up rows
 constexpr int kSlots = 4;       // widened weight tiles in tensor memory
 constexpr int kSlotCols = kBlockK / 2;
+constexpr int kAccCols = 2 * kLayerMaxTokens;  // of an accumulator: both terms' columns
 constexpr int kMaxStages = 16;
-// dynamic shared memory: 227 KB a CTA less the static barriers and the exchange rows
-constexpr size_t kMaxDynamic = (227 - 6) * 1024;
+// dynamic shared memory: 227 KB a CTA less the static barriers
+constexpr size_t kMaxDynamic = (227 - 2) * 1024;
 
-// Bytes of the lists at the front of dynamic shared memory.
-__host__ __device__ inline int lists_bytes(int E, int P) {
-    // experts in use and their first pairs; tokens, places, experts and gates of the pairs
-    const int A = E < P ? E : P;
-    return ((A * 2 + (A + 1) * 2 + P * 2 + P * 2 + P * 2) + P * 4 + 15 + 16) / 16 * 16;
-}
-
+// The lists at the front of dynamic shared memory, for E experts and P pairs
+// (token, k).
 struct Lists {
     float *gate;       // [P] gate of (t, k), set where kept
-    uint16_t *expert;  // [A]
-    uint16_t *base;    // [A + 1] first pair of an expert in use
+    float *given;      // [P] the caller's weight of (t, k)
+    int *count;        // [E] kept pairs of an expert
+    uint32_t *named;   // [32] experts in use, a bit each
+    uint16_t *first;   // [E] first pair of an expert in use
+    uint16_t *expert;  // [A] experts in use, ascending (A <= min(E, P))
+    uint16_t *base;    // [A + 1] their first pairs
     uint16_t *token;   // [P] token of a pair
     int16_t *place;    // [P] pair of (t, k), -1 where dropped (at first: its expert)
     int16_t *kept;     // [P] expert of (t, k), -1 where dropped
+    __host__ __device__ static int bytes(int E, int P) {
+        return (P * 8 + E * 4 + 128 + E * 2 + (E < P ? E : P) * 4 + 2 + P * 6 + 15) / 16 * 16;
+    }
     __device__ Lists(uint8_t *mem, int E, int P) {
         const int A = E < P ? E : P;
         gate = reinterpret_cast<float *>(mem);
-        expert = reinterpret_cast<uint16_t *>(gate + P);
+        given = gate + P;
+        count = reinterpret_cast<int *>(given + P);
+        named = reinterpret_cast<uint32_t *>(count + E);
+        first = reinterpret_cast<uint16_t *>(named + 32);
+        expert = first + E;
         base = expert + A;
         token = base + A + 1;
         place = reinterpret_cast<int16_t *>(token + P);
@@ -87,7 +96,7 @@ struct Shape {
     static constexpr bool kWiden = FORMAT != MOE_FORMAT_BF16;
     static constexpr int kThreads = (kWiden ? 16 : 8) * 32;
     static constexpr int kA = kTileRows * kBlockK * (kWiden ? 1 : 2);  // weight bytes a stage
-    static constexpr int kCols = kWiden ? 512 : 128;                   // tensor-memory columns
+    static constexpr int kTmem = kWiden ? 512 : 256;                   // tensor-memory columns
 };
 
 template <int FORMAT>
@@ -100,46 +109,55 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
     __shared__ uint64_t wide_full[kSlots], wide_free[kSlots];
     __shared__ uint64_t acc_full[2], acc_free[2], drained;
     __shared__ uint32_t s_taddr;
-    __shared__ int s_used, s_most, s_last;
+    __shared__ int s_used, s_most;
     __shared__ volatile int s_failed;
-    __shared__ float s_up[16][kHalfRows];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int P = p.T * p.K, cta = blockIdx.x, ctas = gridDim.x;
 
     const Lists L(smem_raw, p.E, P);
-    const uint32_t after = ptx::smem_u32(smem_raw) + lists_bytes(p.E, P);
-    uint8_t *ring = smem_raw + lists_bytes(p.E, P) + ((1024u - (after & 1023u)) & 1023u);
-    if (tid == 0) {
-        for (int s = 0; s < kMaxStages; ++s) {
-            ptx::mbar_init(&bar_a[s], 1);
-            ptx::mbar_init(&bar_b[s], kLoaderThreads);
-            ptx::mbar_init(&bar_free[s], 1);
-        }
-        for (int q = 0; q < kSlots; ++q) {
-            ptx::mbar_init(&wide_full[q], 4);
-            ptx::mbar_init(&wide_free[q], 1);
-        }
-        for (int b = 0; b < 2; ++b) {
-            ptx::mbar_init(&acc_full[b], 1);
-            ptx::mbar_init(&acc_free[b], 4);
-        }
-        ptx::mbar_init(&drained, 1);
-        ptx::fence_mbar_init();
-        s_failed = 0;
-    }
-    if (warp == kMmaWarp) tc::tmem_alloc(&s_taddr, S::kCols);
-
+    const uint32_t after = ptx::smem_u32(smem_raw) + Lists::bytes(p.E, P);
+    uint8_t *ring = smem_raw + Lists::bytes(p.E, P) + ((1024u - (after & 1023u)) & 1023u);
     // ---- lists: experts in use, ascending, and the pairs of each, by token ----
-    int *count = reinterpret_cast<int *>(ring);  // [E], before the ring is in use
-    int *first = count + p.E;                    // [E] first pair of an expert
-    for (int e = tid; e < p.E; e += S::kThreads) count[e] = 0;
+    // (the ids' latency passes behind the set-up)
+    int id0 = -1;
+    float w0 = 0.0f;
+    if (tid < P) {
+        id0 = __ldg(p.topk_ids + tid);
+        w0 = __ldg(p.topk_w + tid);
+    }
+    if (warp == kMmaWarp) tc::tmem_alloc(&s_taddr, S::kTmem);
+    if (tid < kMaxStages) {
+        ptx::mbar_init(&bar_a[tid], 1);
+        ptx::mbar_init(&bar_b[tid], kLoaderThreads);
+        ptx::mbar_init(&bar_free[tid], 1);
+        if (tid < kSlots) {
+            ptx::mbar_init(&wide_full[tid], 4);
+            ptx::mbar_init(&wide_free[tid], 1);
+        }
+        if (tid < 2) {
+            ptx::mbar_init(&acc_full[tid], 1);
+            ptx::mbar_init(&acc_free[tid], 4);
+        }
+        if (tid == 0) {
+            ptx::mbar_init(&drained, 1);
+            s_failed = 0;
+        }
+        ptx::fence_mbar_init();
+    }
+    if (warp == kProducerWarp && lane == 0) {
+        tc::prefetch_map(&map13);
+        tc::prefetch_map(&map2);
+    }
+    for (int e = tid; e < p.E; e += S::kThreads) L.count[e] = 0;
+    if (warp == 1) L.named[lane] = 0;
     for (int i = tid; i < P; i += S::kThreads) {
-        int id = __ldg(p.topk_ids + i);
+        int id = i == tid ? id0 : __ldg(p.topk_ids + i);
         if (id < -1 || id >= p.E) {
             if (cta == 0) atomicOr(&p.header->flags, MOE_DEVICE_FLAG_BAD_EXPERT_ID);
             id = -1;
         }
         L.place[i] = (int16_t)id;
+        L.given[i] = i == tid ? w0 : __ldg(p.topk_w + i);
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -148,34 +166,41 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
     for (int i = tid; i < P; i += S::kThreads) {
         const int t0 = i / p.K * p.K, id = L.place[i];
         bool keep = id >= 0;
-        for (int j = t0; j < i && keep; ++j) keep = L.place[j] != id;
+        for (int j = t0; j < i; ++j) keep = keep && L.place[j] != id;
         L.kept[i] = (int16_t)(keep ? id : -1);
         if (!keep) continue;
-        atomicAdd(&count[id], 1);
-        float g = __ldg(p.topk_w + i);
+        atomicAdd(&L.count[id], 1);
+        atomicOr(&L.named[id >> 5], 1u << (id & 31));
+        float g = L.given[i];
         for (int j = i + 1; j < t0 + p.K; ++j)
-            if (L.place[j] == id) g = __fadd_rn(g, __ldg(p.topk_w + j));
+            if (L.place[j] == id) g = __fadd_rn(g, L.given[j]);
         L.gate[i] = g;
     }
     __syncthreads();
-    if (warp == 0) {  // exclusive prefixes of the counts and of the experts in use
-        int used = 0, pairs = 0, most = 0;
-        for (int e0 = 0; e0 < p.E; e0 += 32) {
-            const int e = e0 + lane, c = e < p.E ? count[e] : 0;
+    if (warp == 0) {  // lane l: experts 32 l .. 32 l + 31
+        uint32_t bits = L.named[lane];
+        int used = __popc(bits);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, used, o);
+            if (lane >= o) used += v;
+        }
+        for (int a = used - __popc(bits); bits != 0; bits &= bits - 1)
+            L.expert[a++] = (uint16_t)(32 * lane + __ffs(bits) - 1);
+        used = __shfl_sync(0xffffffffu, used, 31);
+        __syncwarp();
+        int pairs = 0, most = 0;
+        for (int a0 = 0; a0 < used; a0 += 32) {
+            const int a = a0 + lane, e = a < used ? L.expert[a] : 0, c = a < used ? L.count[e] : 0;
             int s = c;
             for (int o = 1; o < 32; o <<= 1) {
                 const int v = __shfl_up_sync(0xffffffffu, s, o);
                 if (lane >= o) s += v;
             }
-            const unsigned m = __ballot_sync(0xffffffffu, c > 0);
-            most = max(most, c);
-            if (c > 0) {
-                const int a = used + __popc(m & ((1u << lane) - 1u));
-                L.expert[a] = (uint16_t)e;
+            if (a < used) {
                 L.base[a] = (uint16_t)(pairs + s - c);
-                first[e] = pairs + s - c;
+                L.first[e] = (uint16_t)(pairs + s - c);
             }
-            used += __popc(m);
+            most = max(most, c);
             pairs += __shfl_sync(0xffffffffu, s, 31);
         }
         most = __reduce_max_sync(0xffffffffu, most);
@@ -186,35 +211,40 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
         }
     }
     __syncthreads();
-    for (int i = tid; i < P; i += S::kThreads) {
-        const int id = L.kept[i];
-        int at = -1;
-        if (id >= 0) {
-            at = first[id];
-            for (int j = 0; j < i; ++j) at += L.kept[j] == id;
-            L.token[at] = (uint16_t)(i / p.K);
+    // where the pairs stand; the weight producer needs none of it and goes ahead
+    if (warp != kProducerWarp) {
+        const int me = tid < kProducerWarp * 32 ? tid : tid - 32;
+        for (int i = me; i < P; i += S::kThreads - 32) {
+            const int id = L.kept[i];
+            int at = -1;
+            if (id >= 0) {
+                at = L.first[id];
+                for (int j = 0; j < i; ++j) at += L.kept[j] == id;
+                L.token[at] = (uint16_t)(i / p.K);
+            }
+            L.place[i] = (int16_t)at;
         }
-        L.place[i] = (int16_t)at;
+        asm volatile("bar.sync 2, %0;" ::"n"(S::kThreads - 32) : "memory");
     }
-    ptx::fence_proxy_async_smem();  // the ring's memory goes to TMA
-    __syncthreads();
 
     const int A = s_used;
     const uint32_t taddr = s_taddr;
     // A stage holds a unit's weights and the token rows of the fullest expert, in
-    // groups of 8, 64 columns at a time: two halves, and twice for the two terms
-    // of the activations.  (Products read 16 rows at a time: what they read past
-    // the rows only reaches columns that nobody reads.)
-    const int b_rows = (s_most + 7) / 8 * 8, b_half = b_rows * kAtom;
-    const int stage_bytes = S::kA + 4 * b_half;
+    // groups of 8, 64 columns at a time; in phase 1 the rows of the activations'
+    // second term stand behind those of the first.  (Products read 16 rows at a
+    // time: what they read past the rows only reaches columns that nobody reads.)
+    const int b_half = (s_most + 7) / 8 * 8 * 2 * kAtom;
+    const int stage_bytes = S::kA + 2 * b_half;
     const int stages = min(kMaxStages, p.ring_bytes / stage_bytes);
     auto stage_a = [&](int s) { return ring + s * stage_bytes; };
     auto stage_b = [&](int s) { return ring + s * stage_bytes + S::kA; };
     // phase 0: tiles (expert, 64 gate + 64 up rows); phase 1: (128 rows of H, expert)
     const int tiles0 = (p.I + kHalfRows - 1) / kHalfRows, tiles1 = (p.H + kTileRows - 1) / kTileRows;
     const int blocks0 = (p.H + kBlockK - 1) / kBlockK, blocks1 = (p.I + kBlockK - 1) / kBlockK;
-    const Cut cuts[2] = {cut((long long)A * tiles0 * blocks0, ctas),
-                         cut((long long)A * tiles1 * blocks1, ctas)};
+    // (merging parts takes about 2.5 us, a unit 0.7 us of bf16 weights, half of it of 8-bit)
+    constexpr int kMerge = S::kWiden ? 7 : 4;
+    const Cut cuts[2] = {cut(A * tiles0, blocks0, ctas, kMerge, kAlone),
+                         cut(A * tiles1, blocks1, ctas, kMerge, kAlone)};
     auto tile_of = [&](int phase, int tile, int &a, int &r) {
         if (phase == 0) {
             a = tile / tiles0;
@@ -236,9 +266,6 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
                     int a, r;
                     tile_of(phase, sg.tile, a, r);
                     const int e = L.expert[a];
-                    const void *map = phase ? (const void *)&map2 : (const void *)&map13;
-                    const int row0 = phase ? e * p.H + r * kTileRows : e * 2 * p.I + r * kHalfRows;
-                    const int row1 = phase ? row0 + kHalfRows : row0 + p.I;
                     for (int kb = sg.k0; kb < sg.k1; ++kb, st.next()) {
                         const int s = (int)st.at;
                         if (!ptx::mbar_wait_timed(&bar_free[s], st.parity ^ 1u, kWaitNs)) {
@@ -253,8 +280,11 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
                         for (int h = 0; h < kHalves; ++h) {
                             const int x = kb * kBlockK + h * 64;
                             uint8_t *d = dst + h * kTileRows * kAtom;
-                            tc::tma_load_2d(d, map, x, row0, &bar_a[s]);
-                            tc::tma_load_2d(d + kHalfRows * kAtom, map, x, row1, &bar_a[s]);
+                            if (phase == 0)
+                                tc::tma_load_5d(d, &map13, x, 0, 0, r * (kHalfRows / kQuarter), e,
+                                                &bar_a[s]);
+                            else
+                                tc::tma_load_3d(d, &map2, x, r * kTileRows, e, &bar_a[s]);
                         }
                     }
                 }
@@ -275,9 +305,10 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
                 for (; !s_failed && segs.next(sg); ++it) {
                     int a, r;
                     tile_of(phase, sg.tile, a, r);
-                    const int cols = ((int)L.base[a + 1] - L.base[a] + 15) / 16 * 16;
+                    const int rows = L.base[a + 1] - L.base[a];
+                    const int cols = phase ? (rows + 7) / 8 * 16 : (rows + 15) / 16 * 16;
                     const uint32_t idesc = tc::idesc_bf16_f32(kTileRows, cols);
-                    const uint32_t b = it & 1u, d = taddr + b * kLayerMaxTokens;
+                    const uint32_t b = it & 1u, d = taddr + b * kAccCols;
                     if (!ptx::mbar_wait_timed(&acc_free[b], ((it >> 1) & 1u) ^ 1u, kWaitNs)) {
                         s_failed = 1;
                         break;
@@ -302,7 +333,7 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
                         const uint64_t ad = tc::smem_desc_sw128(ptx::smem_u32(stage_a(s)));
                         const uint64_t bd = tc::smem_desc_sw128(ptx::smem_u32(stage_b(s)));
                         const uint64_t half_a = kTileRows * kAtom / 16, half_b = b_half / 16;
-                        const uint32_t at = taddr + 2 * kLayerMaxTokens + wide.at * kSlotCols;
+                        const uint32_t at = taddr + 2 * kAccCols + wide.at * kSlotCols;
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk) {  // 16 k a step
                             const uint64_t bk = bd + (kk >> 2) * half_b + 2 * (kk & 3);
@@ -312,11 +343,6 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
                                 tc::mma_f16_ta(d, at + 8 * kk, bk, idesc, acc);
                             else
                                 tc::mma_bf16(d, ak, bk, idesc, acc);
-                            if (phase == 0) continue;
-                            if constexpr (S::kWiden)  // the second term
-                                tc::mma_f16_ta(d, at + 8 * kk, bk + 2 * half_b, idesc, true);
-                            else
-                                tc::mma_bf16(d, ak, bk + 2 * half_b, idesc, true);
                         }
                         tc::commit(&bar_free[s]);
                         if (S::kWiden) tc::commit(&wide_free[wide.at]);
@@ -340,13 +366,14 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
             if (phase == 1) {
                 // every activation is written before any is read
                 bool ok = true;
-                if (lane == 0) ok = wait_count(&p.header->done[0], A * tiles0, &s_failed);
+                if (lane == 0) ok = wait_count(&p.header->done[0], A * tiles0 * 4, &s_failed);
                 if (!__all_sync(0xffffffffu, ok)) s_failed = 1;
             }
             while (!warp_flag(&s_failed) && segs.next(sg)) {
                 int a, r;
                 tile_of(phase, sg.tile, a, r);
                 const int base = L.base[a], rows = L.base[a + 1] - base;
+                const int second = (rows + 7) / 8 * 8 * kAtom;  // where the second term's rows begin
                 const uint16_t *src = phase ? p.act + (size_t)base * 2 * p.I : p.x;
                 for (int kb = sg.k0; kb < sg.k1; ++kb, st.next()) {
                     const int s = (int)st.at;
@@ -362,10 +389,10 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
                         uint8_t *to = dst + row * kAtom + (((piece & 7) ^ (row & 7)) << 4);
                         if (col < width) {
                             ptx::cp_async16(to, src + at + col);
-                            if (phase) ptx::cp_async16(to + 2 * b_half, src + at + width + col);
+                            if (phase) ptx::cp_async16(to + second, src + at + width + col);
                         } else {  // past the end: zero, beside the weights' zero fill
                             ptx::cp_async16_zero(to, src);
-                            if (phase) ptx::cp_async16_zero(to + 2 * b_half, src);
+                            if (phase) ptx::cp_async16_zero(to + second, src);
                         }
                     }
                     ptx::cp_async_mbar_arrive_noinc(&bar_b[s]);
@@ -394,7 +421,7 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
             }
             tc::fence_after_sync();
             const uint8_t *src = stage_a(s) + row * kAtom;
-            const uint32_t dst = taddr + 2 * kLayerMaxTokens + q * kSlotCols +
+            const uint32_t dst = taddr + 2 * kAccCols + q * kSlotCols +
                                  ((uint32_t)(row & ~31) << 16);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -420,7 +447,9 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
             if (lane == 0) mbar_arrive(&wide_full[q]);
         }
     } else if (warp < 4) {
-                uint32_t it = 0;
+        // Each warp finishes its 32 rows by itself: in phase 0 the lanes below 16
+        // hold gate rows, the others the up rows of the same channels.
+        uint32_t it = 0;
         bool ok = true;
         for (int phase = 0; phase < 2 && ok; ++phase) {
             const int blocks = phase ? blocks1 : blocks0;
@@ -428,8 +457,9 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
             Segment sg;
             for (; segs.next(sg); ++it) {
                 const uint32_t b = it & 1u;
-                ok = ptx::mbar_wait_timed(&acc_full[b], (it >> 1) & 1u, kWaitNs);
-                ok = !epi_any(!ok || s_failed);  // (all four warps leave together)
+                ok = __all_sync(0xffffffffu,
+                                ptx::mbar_wait_timed(&acc_full[b], (it >> 1) & 1u, kWaitNs) &&
+                                    !s_failed);
                 if (!ok) {
                     s_failed = 1;
                     break;
@@ -438,43 +468,54 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
                 int a, r;
                 tile_of(phase, sg.tile, a, r);
                 const int e = L.expert[a], base = L.base[a], rows = L.base[a + 1] - base;
-                const uint32_t acc = taddr + b * kLayerMaxTokens + ((uint32_t)(tid & ~31) << 16);
+                const uint32_t acc = taddr + b * kAccCols + ((uint32_t)(warp * 32) << 16);
                 const bool whole = sg.k0 == 0 && sg.k1 == blocks;
-                const Parts parts(cuts[phase], sg.tile, blocks);
+                const int second = (rows + 7) / 8 * 8;  // columns of the second term, phase 1
+                auto take = [&](int n0, float (&v)[kCols]) {
+                    uint32_t u[kCols], w[kCols];
+                    tc::ld_32x8(acc + n0, u);
+                    if (phase) tc::ld_32x8(acc + second + n0, w);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int i = 0; i < kCols; ++i) {
+                        v[i] = __uint_as_float(u[i]);
+                        if (phase) v[i] += __uint_as_float(w[i]);
+                    }
+                };
+                Parts parts;
                 auto part_of = [&](int c) {
                     return p.part + ((size_t)(2 * c + parts.slot(c)) * p.nmax) * kTileRows + tid;
                 };
                 if (!whole) {
+                    parts = Parts(cuts[phase], sg.tile, blocks);
                     float *to = part_of(cta);
-                    for (int n0 = 0; n0 < rows; n0 += 16) {
-                        uint32_t v[16];
-                        tc::ld_32x16(acc + n0, v);
-                        tc::wait_ld();
+                    for (int n0 = 0; n0 < rows; n0 += kCols) {
+                        float v[kCols];
+                        take(n0, v);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (n0 + i < rows) __stcg(to + (n0 + i) * kTileRows, __uint_as_float(v[i]));
+                        for (int i = 0; i < kCols; ++i)
+                            if (n0 + i < rows) __stcg(to + (n0 + i) * kTileRows, v[i]);
                     }
                     tc::fence_before_sync();
+                    __threadfence();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&acc_free[b]);
-                    __threadfence();
-                    epi_sync();
-                    if (tid == 0) {
-                        int *m = &p.header->merged[phase][parts.c0];
-                        s_last = atomicAdd(m, 1) == parts.count() - 1;
-                        if (s_last) *m = 0;  // for the next call
+                    int last = 0;
+                    if (lane == 0) {
+                        mbar_arrive(&acc_free[b]);
+                        int *m = &p.header->merged[phase][parts.c0][warp];
+                        last = atomicAdd(m, 1) == parts.count() - 1;
+                        if (last) *m = 0;  // for the next call
+                        __threadfence();
                     }
-                    epi_sync();
-                    if (!s_last) continue;
-                    __threadfence();
+                    if (!__shfl_sync(0xffffffffu, last, 0)) continue;
                 }
-                // channel of this thread: its row, whether it is stored, its scale
+                // channel of this lane, whether it is stored, its scale
                 int chan, limit;
                 const float *scales;
                 if (phase == 0) {
-                    chan = r * kHalfRows + (tid & (kHalfRows - 1));
+                    chan = r * kHalfRows + warp * kQuarter + (lane & (kQuarter - 1));
                     limit = p.I;
-                    scales = p.w13_scale + (size_t)e * 2 * p.I + (tid < kHalfRows ? 0 : p.I);
+                    scales = p.w13_scale + (size_t)e * 2 * p.I + (lane < kQuarter ? 0 : p.I);
                 } else {
                     chan = r * kTileRows + tid;
                     limit = p.H;
@@ -482,67 +523,53 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
                 }
                 float sc = S::kWiden && chan < limit ? __ldg(scales + chan) : 1.0f;
                 if (FORMAT == MOE_FORMAT_INT8) sc *= kInt8Bf16;
-                for (int n0 = 0; n0 < rows; n0 += 16) {
-                    float v[16];
+                for (int n0 = 0; n0 < rows; n0 += kCols) {
+                    float v[kCols];
                     if (whole) {
-                        uint32_t u[16];
-                        tc::ld_32x16(acc + n0, u);
-                        tc::wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(u[i]);
+                        take(n0, v);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+                        for (int i = 0; i < kCols; ++i) v[i] = 0.0f;
                         for (int c = parts.c0; c <= parts.c1; ++c) {
                             const float *from = part_of(c);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
+                            for (int i = 0; i < kCols; ++i)
                                 if (n0 + i < rows) v[i] += __ldcg(from + (n0 + i) * kTileRows);
                         }
                     }
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] *= sc;
-                    if (phase == 0) {
-                        if (tid >= kHalfRows) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) s_up[i][tid - kHalfRows] = v[i];
+                    for (int i = 0; i < kCols; ++i) {
+                        if (n0 + i >= rows) break;  // (the warp alike)
+                        const float z = v[i] * sc;
+                        if (phase == 0) {
+                            const float up = __shfl_down_sync(0xffffffffu, z, kQuarter);
+                            const float f = z / (1.0f + expf(-z)) * up;
+                            const __nv_bfloat16 hi = __float2bfloat16_rn(f);
+                            const float fh = __bfloat162float(hi);
+                            // (nothing is left of an infinity)
+                            const __nv_bfloat16 lo =
+                                __float2bfloat16_rn(isinf(fh) ? 0.0f : f - fh);
+                            if (lane < kQuarter && chan < limit) {
+                                uint16_t *to = p.act + (size_t)(base + n0 + i) * 2 * p.I + chan;
+                                to[0] = *reinterpret_cast<const uint16_t *>(&hi);
+                                to[p.I] = *reinterpret_cast<const uint16_t *>(&lo);
+                            }
+                        } else if (chan < limit) {
+                            __stcg(p.y + (size_t)(base + n0 + i) * p.H + chan, z);
                         }
-                        epi_sync();
-                        if (tid < kHalfRows && chan < limit) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (n0 + i < rows) {
-                                    const float z = v[i] / (1.0f + expf(-v[i])) * s_up[i][tid];
-                                    const __nv_bfloat16 hi = __float2bfloat16_rn(z);
-                                    const float zh = __bfloat162float(hi);
-                                    // (nothing is left of an infinity)
-                                    const __nv_bfloat16 lo = __float2bfloat16_rn(
-                                        isinf(zh) ? 0.0f : z - zh);
-                                    uint16_t *to = p.act + (size_t)(base + n0 + i) * 2 * p.I + chan;
-                                    to[0] = *reinterpret_cast<const uint16_t *>(&hi);
-                                    to[p.I] = *reinterpret_cast<const uint16_t *>(&lo);
-                                }
-                        }
-                        epi_sync();
-                    } else if (chan < limit) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (n0 + i < rows)
-                                __stcg(p.y + (size_t)(base + n0 + i) * p.H + chan, v[i]);
                     }
                 }
-                if (whole) {
-                    tc::fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&acc_free[b]);
-                }
+                if (whole) tc::fence_before_sync();
                 __threadfence();
-                epi_sync();
-                if (tid == 0) atomicAdd(&p.header->done[phase], 1);
+                __syncwarp();
+                if (lane == 0) {
+                    if (whole) mbar_arrive(&acc_free[b]);
+                    atomicAdd(&p.header->done[phase], 1);
+                }
             }
         }
         // ---- gated sum over the token's experts, all CTAs ----
-        if (ok && tid == 0 && !wait_count(&p.header->done[1], A * tiles1, &s_failed)) s_failed = 1;
+        if (ok && tid == 0 && !wait_count(&p.header->done[1], A * tiles1 * 4, &s_failed)) s_failed = 1;
         epi_sync();
         if (!s_failed) {
             const int H4 = p.H / 4;
@@ -588,21 +615,28 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
             p.header->left = 0;
         }
     }
-    if (warp == kMmaWarp) tc::tmem_dealloc(taddr, S::kCols);
+    if (warp == kMmaWarp) tc::tmem_dealloc(taddr, S::kTmem);
 }
 
 template <int FORMAT>
 cudaError_t launch_t(LayerSmallParams &p, int num_sms, cudaStream_t st) {
     using S = Shape<FORMAT>;
     CUtensorMap m13, m2;
-    if (!make_map(&m13, p.w13, (long long)p.E * 2 * p.I, p.H, kHalfRows, S::kWiden) ||
-        !make_map(&m2, p.w2, (long long)p.E * p.H, p.I, kHalfRows, S::kWiden))
+    // W13: a box holds 4 times 16 gate rows and the up rows of the same channels;
+    // W2: 128 rows.  What a box has past its expert's rows reads as zero.
+    const long long H = p.H, I = p.I;
+    const int width = S::kWiden ? kAtom : kAtom / 2;
+    const long long ext13[5] = {H, kQuarter, 2, I / kQuarter, p.E};
+    const long long str13[5] = {1, H, I * H, kQuarter * H, 2 * I * H};
+    const int box13[5] = {width, kQuarter, 2, kHalfRows / kQuarter, 1};
+    const long long ext2[3] = {I, H, p.E}, str2[3] = {1, I, H * I};
+    const int box2[3] = {width, kTileRows, 1};
+    if (!make_map_nd(&m13, p.w13, 5, ext13, str13, box13, S::kWiden) ||
+        !make_map_nd(&m2, p.w2, 3, ext2, str2, box2, S::kWiden))
         return cudaErrorInvalidValue;
     // 1 KB aligns the ring and 1 KB stands behind it (reads of 16 rows where there are 8)
-    const int front = lists_bytes(p.E, p.T * p.K) + 2048;
+    const int front = Lists::bytes(p.E, p.T * p.K) + 2048;
     p.ring_bytes = (int)kMaxDynamic - front;
-    // the lists are built where the ring will be
-    if (2 * p.E * (int)sizeof(int) > p.ring_bytes) return cudaErrorInvalidValue;
     const size_t smem = (size_t)front + (size_t)p.ring_bytes;
     static std::atomic<unsigned long long> raised{0};
     cudaError_t err = raise_smem_limit_once(layer_small_kernel<FORMAT>, kMaxDynamic, raised);

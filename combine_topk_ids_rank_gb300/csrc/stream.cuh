@@ -28,19 +28,34 @@ constexpr int kBlockK = 128;     // k extent of a unit
 constexpr int kAtom = 128;       // bytes of a shared-memory row (128-byte swizzle)
 constexpr uint64_t kWaitNs = 500ull * 1000 * 1000;  // 0.5 s of wall time per wait
 
-// The units [0, total) cut into `parts` ranges; parts <= total (or both 0).
+// Units cut into `parts` ranges at multiples of `grain` units: the first
+// `more` parts have q + 1 grains, the others q >= 1.
 struct Cut {
-    long long total;
-    int parts;
-    __device__ long long first(int c) const { return (long long)c * total / parts; }
+    int parts, grain, q, more;
+    __device__ Cut(int grains, int parts_, int grain_) : parts(parts_), grain(grain_) {
+        q = parts ? grains / parts : 0;
+        more = parts ? grains - q * parts : 0;
+    }
+    __device__ int first(int c) const { return (c * q + min(c, more)) * grain; }
     // the part that holds unit u
-    __device__ int of(long long u) const {
-        return (int)(((u + 1) * parts - 1) / total);
+    __device__ int of(int u) const {
+        const int g = u / grain, big = more * (q + 1);
+        return g < big ? g / (q + 1) : more + (g - big) / q;
     }
 };
 
-__device__ __forceinline__ Cut cut(long long total, int ctas) {
-    return Cut{total, total < ctas ? (int)total : ctas};
+// `tiles` of `blocks` units over the CTAs: cut anywhere, or between tiles only.
+// Cutting inside tiles evens out the CTAs' work but adds the parts' way
+// through memory, about `merge` units' time.  A CTA alone can do `alone` / 16
+// of its even share of the work in the same time: where the memory's rate is
+// the bound some CTAs may idle before whole tiles cost anything.
+constexpr int kAlone = 24;
+__device__ __forceinline__ Cut cut(int tiles, int blocks, int ctas, int merge, int alone) {
+    const int total = tiles * blocks, rounds = (tiles + ctas - 1) / ctas;
+    const int even = (total + ctas - 1) / ctas;
+    const int whole = max(rounds * blocks * 16 / alone, even);
+    if (whole <= even + merge || total < ctas) return Cut(tiles, min(tiles, ctas), blocks);
+    return Cut(total, ctas, 1);
 }
 
 // A run of units of one tile: k-blocks [k0, k1) of tile `tile`.
@@ -50,8 +65,7 @@ struct Segment {
 
 // The segments of CTA c in ascending order; `blocks` k-blocks a tile.
 struct Segments {
-    long long u, end;
-    int blocks;
+    int u, end, blocks;
     __device__ Segments(const Cut &ct, int c, int blocks_) : u(0), end(0), blocks(blocks_) {
         if (c < ct.parts) {
             u = ct.first(c);
@@ -60,10 +74,9 @@ struct Segments {
     }
     __device__ bool next(Segment &s) {
         if (u >= end) return false;
-        s.tile = (int)(u / blocks);
-        s.k0 = (int)(u - (long long)s.tile * blocks);
-        const long long left = end - u;
-        s.k1 = s.k0 + left < blocks ? (int)(s.k0 + left) : blocks;
+        s.tile = u / blocks;
+        s.k0 = u - s.tile * blocks;
+        s.k1 = min(s.k0 + end - u, blocks);
         u += s.k1 - s.k0;
         return true;
     }
@@ -73,8 +86,9 @@ struct Segments {
 // begins that CTA's range, else in slot 1.
 struct Parts {
     int c0, c1, slot0;
+    Parts() = default;
     __device__ Parts(const Cut &ct, int tile, int blocks) {
-        const long long a = (long long)tile * blocks;
+        const int a = tile * blocks;
         c0 = ct.of(a);
         c1 = ct.of(a + blocks - 1);
         slot0 = ct.first(c0) == a ? 0 : 1;
