@@ -13,15 +13,19 @@
 // 2^24 in magnitude; past that each addition rounds to 24 bits.  Both
 // operands stay 8 bits wide in memory, in L2 and on the way to the SM.
 //
-// GB300 design (stream.cuh: weights are the A operand, 128 channels a tile,
-// up to 256 tokens the columns): persistent CTAs, one per SM.  Whole waves
-// of tiles go round robin; what is left over is cut evenly by k.
-//   warps 0-3: epilogue (tensor-memory lane quadrants);
-//   warps 4-7: widen a stage's 128 weight rows into tensor memory, which the
-//     products read as their A operand;
-//   warps 8-15: widen the token rows into f16 tiles in shared memory, half a
-//     k-block (64 codes) at a time;
-//   warp 16: producer (TMA, 128-byte swizzle); warp 17: MMA issuer.
+// GB300 design (stream.cuh: weights are the A operand, tokens the columns):
+// persistent pairs of CTAs, one CTA per SM.  A pair's tile is 256 channels
+// (128 per CTA) by up to 256 tokens; each CTA widens its own weight rows and
+// half of the token rows, and the pair's products (cta_group::2) read both
+// halves, so a token row is widened once for 256 channels.  Whole waves of
+// tiles go round robin; what is left over is cut by k.  In each CTA:
+//   warps 0-3: epilogue (tensor-memory lane quadrants), 32 channels each;
+//   warps 4-11: two groups widen a stage's 128 weight rows into tensor memory,
+//     which the products read as their A operand;
+//   warps 12-19: four groups widen the token rows into f16 tiles in shared
+//     memory, half a k-block (64 codes) at a time;
+//   warp 20: producer (TMA, 128-byte swizzle);
+//   warp 21 of CTA 0: MMA issuer.
 #include "kernels.h"
 #include "ptx.cuh"
 #include "smem_limit.h"
@@ -38,22 +42,28 @@ namespace {
 
 using namespace stream;
 
-constexpr int kWeightWarp0 = 4, kTokenWarp0 = 8, kTokenWarps = 8;
-constexpr int kProducerWarp = 16, kMmaWarp = 17, kThreads = 18 * 32;
-constexpr int kMaxCols = 256;           // tokens of a tile
-constexpr int kTmemCols = 512;          // accumulators, then widened weights
+constexpr int kWeightWarp0 = 4, kWeightGroups = 2;
+constexpr int kTokenWarp0 = kWeightWarp0 + 4 * kWeightGroups, kTokenWarps = 8;
+constexpr int kGroupWarps = 2, kGroups = kTokenWarps / kGroupWarps;
+constexpr int kBatch = 4;                 // rows a token lane has in hand
+constexpr int kProducerWarp = kTokenWarp0 + kTokenWarps, kMmaWarp = kProducerWarp + 1;
+constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kPairRows = 2 * kTileRows;  // channels of a tile
+constexpr int kMaxCols = 256;             // tokens of a tile
+constexpr int kTmemCols = 512;            // accumulators, then widened weights
 constexpr int kSlots = 4, kSlotCols = kBlockK / 2;
 constexpr int kWeightBytes = kTileRows * kBlockK;
 constexpr int kMaxStages = 12, kMaxHalves = 8;
+constexpr int kRowGroup = 8;              // row tiles of a raster group
+constexpr int kStepCols = 16;             // token columns an epilogue step takes
 // dynamic shared memory: 227 KB a CTA less the static tables
-constexpr size_t kMaxDynamic = (227 - 12) * 1024;
-constexpr int kRowGroup = 16;           // row tiles of a raster group
+constexpr size_t kMaxDynamic = (227 - 13) * 1024;
 
 struct Ring {
-    int nmax;      // token rows a stage holds
+    int nmax;      // tokens of a tile, at most
     int box;       // rows of a token TMA box
-    int stages;    // raw stages: 128 weight rows + nmax token rows of 128 codes
-    int halves;    // widened token tiles: nmax rows of 64 f16
+    int stages;    // raw stages: 128 weight rows + nmax / 2 token rows of 128 codes
+    int halves;    // widened token tiles: nmax / 2 rows of 64 f16
 };
 
 // The tiles of a call: groups in turn; in a group, blocks of kRowGroup row
@@ -61,12 +71,8 @@ struct Ring {
 struct Tiles {
     const int *first;   // [G + 1]
     const int *count;   // [G] token rows
-    int G, M, N, rtiles, nmax;
+    int G, rtiles, nmax;
     __device__ int token_tiles(int c) const { return (c + nmax - 1) / nmax; }
-    __device__ int width(int c) const {  // token rows of a tile: even, multiple of 16
-        const int k = token_tiles(c);
-        return ((c + k - 1) / k + 15) / 16 * 16;
-    }
     __device__ void of(int t, int &g, int &r, int &m0, int &rows) const {
         int lo = 0, hi = G - 1;
         while (lo < hi) {
@@ -74,7 +80,8 @@ struct Tiles {
             if (first[mid] <= t) lo = mid; else hi = mid - 1;
         }
         g = lo;
-        const int c = count[g], k = token_tiles(c), w = width(c);
+        // token rows of a tile: evened out over the group's tiles, a multiple of 16
+        const int c = count[g], k = token_tiles(c), w = ((c + k - 1) / k + 15) / 16 * 16;
         const int u = t - first[g], block = u / (kRowGroup * k);
         const int in = min(kRowGroup, rtiles - block * kRowGroup);
         const int v = u - block * kRowGroup * k;
@@ -84,12 +91,12 @@ struct Tiles {
     }
 };
 
-// The work of a CTA in order: its parts of the cut tiles, then whole tiles.
+// The work of a pair in order: its parts of the cut tiles, then whole tiles.
 struct Work {
     Segments segs;
     int tile, tiles, step, blocks;
-    __device__ Work(const Cut &ct, int cut_tiles, int tiles_, int blocks_, int cta, int ctas)
-        : segs(ct, cta, blocks_), tile(cut_tiles + cta), tiles(tiles_), step(ctas),
+    __device__ Work(const Cut &ct, int cut_tiles, int tiles_, int blocks_, int pair, int pairs)
+        : segs(ct, pair, blocks_), tile(cut_tiles + pair), tiles(tiles_), step(pairs),
           blocks(blocks_) {}
     __device__ bool next(Segment &s) {
         if (segs.next(s)) return true;
@@ -102,26 +109,26 @@ struct Work {
     }
 };
 
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_int8_kernel(const __grid_constant__ CUtensorMap map_x,
                      const __grid_constant__ CUtensorMap map_w, const GemmInt8Params p,
                      const Ring ring) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t raw_full[kMaxStages], raw_free[kMaxStages];
+    // (full: CTA 0's, both CTAs arrive; free: either CTA's own)
     __shared__ uint64_t wide_full[kSlots], wide_free[kSlots];
     __shared__ uint64_t half_full[kMaxHalves], half_free[kMaxHalves];
     __shared__ uint64_t acc_full[2], acc_free[2], drained;
     __shared__ int s_first[kGemmInt8MaxGroups + 1], s_count[kGemmInt8MaxGroups];
-    __shared__ float s_sx[kMaxCols];
+    __shared__ __align__(16) float s_sx[4][kMaxCols];  // the tile's token scales, a warp each
     __shared__ uint32_t s_taddr;
-    __shared__ int s_last;
     __shared__ volatile int s_failed;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int cta = blockIdx.x, ctas = gridDim.x;
+    const int rank = (int)ptx::cluster_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     const uint32_t base = ptx::smem_u32(smem_raw);
     uint8_t *smem = smem_raw + ((1024u - (base & 1023u)) & 1023u);
-    const int raw_bytes = kWeightBytes + ring.nmax * kAtom, half_bytes = ring.nmax * kAtom;
+    const int half_bytes = ring.nmax / 2 * kAtom, raw_bytes = kWeightBytes + half_bytes;
     uint8_t *wide = smem + ring.stages * raw_bytes;  // raw_bytes: a multiple of 1024
     auto raw_w = [&](int s) { return smem + s * raw_bytes; };
     auto raw_x = [&](int s) { return smem + s * raw_bytes + kWeightBytes; };
@@ -131,33 +138,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (p.counts != nullptr) c = min(max(__ldg(p.counts + g), 0), p.M);
         s_count[g] = c;
     }
-    if (tid == 0) {
-        for (int s = 0; s < ring.stages; ++s) {
-            ptx::mbar_init(&raw_full[s], 1);
-            ptx::mbar_init(&raw_free[s], 4 + kTokenWarps);
+    if (warp == kMmaWarp) tc::tmem_alloc_pair(&s_taddr, kTmemCols);
+    if (tid < kMaxStages) {
+        ptx::mbar_init(&raw_full[tid], 1);
+        ptx::mbar_init(&raw_free[tid], 4 + 2 * kGroupWarps);
+        if (tid < kSlots) {
+            ptx::mbar_init(&wide_full[tid], 2 * 4);
+            ptx::mbar_init(&wide_free[tid], 1);
         }
-        for (int q = 0; q < kSlots; ++q) {
-            ptx::mbar_init(&wide_full[q], 4);
-            ptx::mbar_init(&wide_free[q], 1);
+        if (tid < kMaxHalves) {
+            ptx::mbar_init(&half_full[tid], 2 * kGroupWarps);
+            ptx::mbar_init(&half_free[tid], 1);
         }
-        for (int q = 0; q < ring.halves; ++q) {
-            ptx::mbar_init(&half_full[q], kTokenWarps);
-            ptx::mbar_init(&half_free[q], 1);
+        if (tid < 2) {
+            ptx::mbar_init(&acc_full[tid], 1);
+            ptx::mbar_init(&acc_free[tid], 2 * 4);
         }
-        for (int b = 0; b < 2; ++b) {
-            ptx::mbar_init(&acc_full[b], 1);
-            ptx::mbar_init(&acc_free[b], 4);
+        if (tid == 0) {
+            ptx::mbar_init(&drained, 1);
+            s_failed = 0;
         }
-        ptx::mbar_init(&drained, 1);
         ptx::fence_mbar_init();
-        s_failed = 0;
     }
-    if (warp == kMmaWarp) tc::tmem_alloc(&s_taddr, kTmemCols);
+    if (warp == kProducerWarp && lane == 0) {
+        tc::prefetch_map(&map_w);
+        tc::prefetch_map(&map_x);
+    }
     tc::fence_before_sync();
     __syncthreads();
-    tc::fence_after_sync();
-    const int rtiles = (p.N + kTileRows - 1) / kTileRows;
-    const Tiles T{s_first, s_count, p.G, p.M, p.N, rtiles, ring.nmax};
+    const int rtiles = (p.N + kPairRows - 1) / kPairRows;
+    const Tiles T{s_first, s_count, p.G, rtiles, ring.nmax};
     if (warp == 0) {  // exclusive prefix of the groups' tiles
         int sum = 0;
         for (int g0 = 0; g0 < p.G; g0 += 32) {
@@ -172,111 +182,120 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0) s_first[p.G] = sum;
     }
-    __syncthreads();
+    // the pair's barriers are set up before either arrives on the other's
+    __syncwarp();
+    ptx::cluster_sync();
+    tc::fence_after_sync();
 
     const uint32_t taddr = s_taddr;
     const int tiles = s_first[p.G], blocks = (p.H + kBlockK - 1) / kBlockK;
     // Whole waves are dealt out as they are; the rest, and one wave more where
     // the rest is under a quarter of a wave (parts of a few k-blocks each cost
     // more than they balance), is cut by k.
-    int waves = tiles / ctas;
-    if (waves > 0 && tiles % ctas != 0 && tiles % ctas * 4 < ctas) --waves;
-    const int cut_tiles = tiles - waves * ctas;
-    const Cut ct = cut(cut_tiles, blocks, ctas, 4, ring.nmax <= 32 ? kAlone : 16);
+    int waves = tiles / pairs;
+    if (waves > 0 && tiles % pairs != 0 && tiles % pairs * 4 < pairs) --waves;
+    const int cut_tiles = tiles - waves * pairs;
+    // (a merge costs about 4 units' time and 16 more for every 256 token columns)
+    const Cut ct = cut(cut_tiles, blocks, pairs, 4 + ring.nmax / 16,
+                       ring.nmax <= 32 ? kAlone : 16);
     const int nacc = 2 * ring.nmax <= kMaxCols ? 2 : 1;  // accumulators
     const uint32_t slots_at = taddr + kMaxCols;
+    Work work(ct, cut_tiles, tiles, blocks, pair, pairs);
+    Segment sg;
 
     if (warp == kProducerWarp) {
         if (ptx::elect_one()) {
-            uint32_t n = 0;
-            Work work(ct, cut_tiles, tiles, blocks, cta, ctas);
-            Segment sg;
+            Turn st(ring.stages);
+            uint32_t issued = 0;  // stages in use
             while (!s_failed && work.next(sg)) {
                 int g, r, m0, rows;
                 T.of(sg.tile, g, r, m0, rows);
-                const int boxes = (rows + ring.box - 1) / ring.box;
+                const int half = (rows + 15) / 16 * 8;  // token rows of this CTA
+                const int boxes = (half + ring.box - 1) / ring.box;
                 const uint32_t bytes = kWeightBytes + boxes * ring.box * kAtom;
-                for (int kb = sg.k0; kb < sg.k1; ++kb, ++n) {
-                    const int s = (int)(n % ring.stages);
-                    if (!ptx::mbar_wait_timed(&raw_free[s], ((n / ring.stages) & 1u) ^ 1u, kWaitNs)) {
+                const int w0 = r * kPairRows + rank * kTileRows, x0 = m0 + rank * half;
+                for (int kb = sg.k0; kb < sg.k1; ++kb, st.next()) {
+                    const int s = (int)st.at;
+                    if (!ptx::mbar_park<false>(&raw_free[s], st.parity ^ 1u, kWaitNs)) {
                         s_failed = 1;
                         break;
                     }
+                    issued |= 1u << s;
                     ptx::mbar_arrive_expect_tx(&raw_full[s], bytes);
-                    tc::tma_load_2d(raw_w(s), &map_w, kb * kBlockK, g * p.N + r * kTileRows,
-                                    &raw_full[s]);
+                    tc::tma_load_3d(raw_w(s), &map_w, kb * kBlockK, w0, g, &raw_full[s]);
                     for (int b = 0; b < boxes; ++b)
-                        tc::tma_load_2d(raw_x(s) + b * ring.box * kAtom, &map_x, kb * kBlockK,
-                                        g * p.M + m0 + b * ring.box, &raw_full[s]);
+                        tc::tma_load_3d(raw_x(s) + b * ring.box * kAtom, &map_x, kb * kBlockK,
+                                        x0 + b * ring.box, g, &raw_full[s]);
                 }
             }
             // copies still in flight land before shared memory goes away
-            const uint32_t from = n > (uint32_t)ring.stages ? n - ring.stages : 0u;
-            for (uint32_t k = from; k < n; ++k)
-                ptx::mbar_wait_timed(&raw_full[k % ring.stages], (k / ring.stages) & 1u, kWaitNs);
+            for (int i = 0; i < ring.stages; ++i, st.next()) {
+                const uint32_t last = st.parity ^ 1u;
+                if (issued >> st.at & 1u) ptx::mbar_park<false>(&raw_full[st.at], last, kWaitNs);
+            }
         }
     } else if (warp == kMmaWarp) {
-        if (ptx::elect_one()) {
-            uint32_t n = 0, h = 0, it = 0;
-            Work work(ct, cut_tiles, tiles, blocks, cta, ctas);
-            Segment sg;
-            for (; !s_failed && work.next(sg); ++it) {
+        if (rank == 0 && ptx::elect_one()) {
+            Turn slot(kSlots), hf(ring.halves), acc(nacc);
+            for (; !s_failed && work.next(sg); acc.next()) {
                 int g, r, m0, rows;
                 T.of(sg.tile, g, r, m0, rows);
-                const uint32_t idesc = tc::idesc_f16_f32(kTileRows, (rows + 15) / 16 * 16);
-                const uint32_t b = it % nacc, d = taddr + b * ring.nmax;
-                if (!ptx::mbar_wait_timed(&acc_free[b], ((it / nacc) & 1u) ^ 1u, kWaitNs)) {
+                const uint32_t idesc = tc::idesc_f16_f32(kPairRows, (rows + 15) / 16 * 16);
+                const uint32_t d = taddr + acc.at * ring.nmax;
+                if (!ptx::mbar_park<true>(&acc_free[acc.at], acc.parity ^ 1u, kWaitNs)) {
                     s_failed = 1;
                     break;
                 }
                 tc::fence_after_sync();
-                for (int kb = sg.k0; kb < sg.k1 && !s_failed; ++kb, ++n) {
-                    const uint32_t q = n % kSlots, a = slots_at + q * kSlotCols;
-                    if (!ptx::mbar_wait_timed(&wide_full[q], (n / kSlots) & 1u, kWaitNs)) {
+                for (int kb = sg.k0; kb < sg.k1 && !s_failed; ++kb, slot.next()) {
+                    const uint32_t a = slots_at + slot.at * kSlotCols;
+                    if (!ptx::mbar_park<true>(&wide_full[slot.at], slot.parity, kWaitNs)) {
                         s_failed = 1;
                         break;
                     }
-                    for (int hh = 0; hh < 2; ++hh, ++h) {
-                        const uint32_t s = h % ring.halves;
-                        if (!ptx::mbar_wait_timed(&half_full[s], (h / ring.halves) & 1u, kWaitNs)) {
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh, hf.next()) {
+                        if (!ptx::mbar_park<true>(&half_full[hf.at], hf.parity, kWaitNs)) {
                             s_failed = 1;
                             break;
                         }
                         tc::fence_after_sync();
-                        const uint64_t bd = tc::smem_desc_sw128(ptx::smem_u32(wide + s * half_bytes));
+                        const uint64_t bd =
+                            tc::smem_desc_sw128(ptx::smem_u32(wide + hf.at * half_bytes));
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            tc::mma_f16_ta(d, a + 32 * hh + 8 * kk, bd + 2 * kk, idesc,
-                                           kb != sg.k0 || hh != 0 || kk != 0);
-                        tc::commit(&half_free[s]);
+                            tc::mma_f16_ta_pair(d, a + 32 * hh + 8 * kk, bd + 2 * kk, idesc,
+                                                kb != sg.k0 || hh != 0 || kk != 0);
+                        tc::commit_pair(&half_free[hf.at]);
                     }
-                    tc::commit(&wide_free[q]);
+                    tc::commit_pair(&wide_free[slot.at]);
                 }
-                tc::commit(&acc_full[b]);
+                tc::commit_pair(&acc_full[acc.at]);
             }
-            tc::commit(&drained);  // before tensor memory is freed
-            ptx::mbar_wait_timed(&drained, 0, kWaitNs);
+            tc::commit_pair(&drained);  // before tensor memory is freed
+            ptx::mbar_park<false>(&drained, 0, kWaitNs);
         }
     } else if (warp >= kWeightWarp0 && warp < kTokenWarp0) {
-        // Thread l of the four warps owns weight row l of the tile = lane l.
-        const int row = tid - kWeightWarp0 * 32;
-        Work work(ct, cut_tiles, tiles, blocks, cta, ctas);
-        Segment sg;
+        // Thread l of a group of four warps owns weight row l of the CTA's half =
+        // lane l; the groups take the units in turn.
+        const int row = (tid - kWeightWarp0 * 32) & 127, group = (warp - kWeightWarp0) >> 2;
+        Turn st(ring.stages), slot(kSlots);
+        bool ok = true;
         uint32_t n = 0;
-        while (!warp_flag(&s_failed) && work.next(sg)) {
-            bool ok = true;
-            for (int kb = sg.k0; kb < sg.k1 && ok; ++kb, ++n) {
-                const uint32_t s = n % ring.stages, q = n % kSlots;
-                ok = ptx::mbar_wait_timed(&raw_full[s], (n / ring.stages) & 1u, kWaitNs) &&
-                     ptx::mbar_wait_timed(&wide_free[q], ((n / kSlots) & 1u) ^ 1u, kWaitNs);
-                ok = __all_sync(0xffffffffu, ok);
+        while (ok && !warp_flag(&s_failed) && work.next(sg)) {
+            for (int kb = sg.k0; kb < sg.k1; ++kb, st.next(), slot.next(), ++n) {
+                if (n % kWeightGroups != (uint32_t)group) continue;
+                ok = __all_sync(0xffffffffu,
+                                ptx::mbar_park<false>(&raw_full[st.at], st.parity, kWaitNs) &&
+                                    ptx::mbar_park<false>(&wide_free[slot.at], slot.parity ^ 1u,
+                                                         kWaitNs));
                 if (!ok) {
                     s_failed = 1;
                     break;
                 }
                 tc::fence_after_sync();
-                const uint8_t *src = raw_w(s) + row * kAtom;
-                const uint32_t dst = slots_at + q * kSlotCols + ((uint32_t)(row & ~31) << 16);
+                const uint8_t *src = raw_w(st.at) + row * kAtom;
+                const uint32_t dst = slots_at + slot.at * kSlotCols + ((uint32_t)(row & ~31) << 16);
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
                     uint32_t w[32];
@@ -295,184 +314,238 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&raw_free[s]);
-                    mbar_arrive(&wide_full[q]);
+                    mbar_arrive(&raw_free[st.at]);
+                    ptx::mbar_arrive_cluster(ptx::cluster_smem(&wide_full[slot.at], 0));
                 }
             }
         }
     } else if (warp >= kTokenWarp0 && warp < kTokenWarp0 + kTokenWarps) {
-        // Warp w takes the 16-code chunk w % 4 of a half and every second block
-        // of 32 rows: 8 consecutive lanes read (and write) 8 different 16-byte
-        // columns of the swizzled rows, so no bank is hit twice.
-        const int w = warp - kTokenWarp0, c = w & 3;
-        Work work(ct, cut_tiles, tiles, blocks, cta, ctas);
-        Segment sg;
-        uint32_t n = 0, h = 0;
-        while (!warp_flag(&s_failed) && work.next(sg)) {
+        // Groups of kGroupWarps warps take the halves in turn, so that one group's
+        // loads, fence and arrival pass while the others compute.  Warp w of a
+        // group takes every kGroupWarps-th 16-code chunk: 8 consecutive lanes read
+        // (and write) 8 different 16-byte columns of the swizzled rows, so no bank
+        // is hit twice.
+        const int group = (warp - kTokenWarp0) / kGroupWarps, w = (warp - kTokenWarp0) % kGroupWarps;
+        Turn st(ring.stages), hf(ring.halves);
+        bool ok = true;
+        uint32_t h = 0;
+        while (ok && !warp_flag(&s_failed) && work.next(sg)) {
             int g, r, m0, rows;
             T.of(sg.tile, g, r, m0, rows);
-            const int cols = (rows + 15) / 16 * 16;
-            bool ok = true;
-            for (int kb = sg.k0; kb < sg.k1 && ok; ++kb, ++n) {
-                const uint32_t s = n % ring.stages;
-                ok = __all_sync(0xffffffffu, ptx::mbar_wait_timed(&raw_full[s],
-                                                                  (n / ring.stages) & 1u, kWaitNs));
-                for (int hh = 0; hh < 2 && ok; ++hh, ++h) {
-                    const uint32_t q = h % ring.halves;
+            const int half = (rows + 15) / 16 * 8;
+            for (int kb = sg.k0; kb < sg.k1 && ok; ++kb, st.next()) {
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh, hf.next(), ++h) {
+                    if (h % kGroups != (uint32_t)group) continue;
                     ok = __all_sync(0xffffffffu,
-                                    ptx::mbar_wait_timed(&half_free[q],
-                                                         ((h / ring.halves) & 1u) ^ 1u, kWaitNs));
-                    if (!ok) break;
-                    const uint8_t *src = raw_x(s);
-                    uint8_t *dst = wide + q * half_bytes;
-                    for (int row = (w >> 2) * 32 + lane; row < cols; row += 64) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(
-                            src + row * kAtom + (((4 * hh + c) ^ (row & 7)) << 4));
-                        uint4 a, b;
-                        int8_to_f16(v.x, a.x, a.y);
-                        int8_to_f16(v.y, a.z, a.w);
-                        int8_to_f16(v.z, b.x, b.y);
-                        int8_to_f16(v.w, b.z, b.w);
-                        uint8_t *to = dst + row * kAtom;
-                        *reinterpret_cast<uint4 *>(to + (((2 * c) ^ (row & 7)) << 4)) = a;
-                        *reinterpret_cast<uint4 *>(to + (((2 * c + 1) ^ (row & 7)) << 4)) = b;
+                                    ptx::mbar_park<false>(&raw_full[st.at], st.parity, kWaitNs) &&
+                                        ptx::mbar_park<false>(&half_free[hf.at], hf.parity ^ 1u,
+                                                             kWaitNs));
+                    if (!ok) {
+                        s_failed = 1;
+                        break;
+                    }
+                    const uint8_t *src = raw_x(st.at);
+                    uint8_t *dst = wide + hf.at * half_bytes;
+                    for (int row0 = lane; row0 < half; row0 += 32 * kBatch) {
+                        uint4 v[kBatch][4 / kGroupWarps];  // loads first
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+                            for (int j = 0; j < 4 / kGroupWarps; ++j) {
+                                const int row = min(row0 + 32 * i, half - 1);
+                                v[i][j] = *reinterpret_cast<const uint4 *>(
+                                    src + row * kAtom +
+                                    (((4 * hh + w + j * kGroupWarps) ^ (row & 7)) << 4));
+                            }
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+                            for (int j = 0; j < 4 / kGroupWarps; ++j) {
+                                const int row = row0 + 32 * i, c = w + j * kGroupWarps;
+                                uint4 a, b;
+                                int8_to_f16(v[i][j].x, a.x, a.y);
+                                int8_to_f16(v[i][j].y, a.z, a.w);
+                                int8_to_f16(v[i][j].z, b.x, b.y);
+                                int8_to_f16(v[i][j].w, b.z, b.w);
+                                uint8_t *to = dst + row * kAtom;
+                                if (row < half) {
+                                    *reinterpret_cast<uint4 *>(to + (((2 * c) ^ (row & 7)) << 4)) = a;
+                                    *reinterpret_cast<uint4 *>(to + (((2 * c + 1) ^ (row & 7)) << 4)) = b;
+                                }
+                            }
                     }
                     ptx::fence_proxy_async_smem();  // read next by the tensor cores
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&half_full[q]);
+                    if (lane == 0) {
+                        mbar_arrive(&raw_free[st.at]);
+                        ptx::mbar_arrive_cluster(ptx::cluster_smem(&half_full[hf.at], 0));
+                    }
                 }
-                if (!ok) {
-                    s_failed = 1;
-                    break;
-                }
-                if (lane == 0) mbar_arrive(&raw_free[s]);
             }
         }
     } else if (warp < 4) {
-        Work work(ct, cut_tiles, tiles, blocks, cta, ctas);
-        Segment sg;
-        for (uint32_t it = 0; work.next(sg); ++it) {
-            const uint32_t b = it % nacc;
-            const bool ok = ptx::mbar_wait_timed(&acc_full[b], (it / nacc) & 1u, kWaitNs);
-            if (epi_any(!ok || s_failed)) {  // (all four warps leave together)
+        // Each warp finishes 32 channels by itself.
+        Turn acc(nacc);
+        float *sx = s_sx[warp];
+        for (; work.next(sg); acc.next()) {
+            // what the tile needs is fetched while its products run
+            int g, r, m0, rows;
+            T.of(sg.tile, g, r, m0, rows);
+            const int chan = r * kPairRows + rank * kTileRows + tid;
+            const bool live = chan < p.N;
+            const float sw = live ? __ldg(p.w_scale + (size_t)g * p.N + chan) : 0.0f;
+            const float *xs = p.x_scale + (size_t)g * p.M + m0;
+            __syncwarp();
+            for (int i = lane; i < (rows + kStepCols - 1) / kStepCols * kStepCols; i += 32)
+                sx[i] = i < rows ? __ldg(xs + i) : 0.0f;
+            __syncwarp();
+            const bool whole = sg.k0 == 0 && sg.k1 == blocks;
+            Parts parts;
+            if (!whole) parts = Parts(ct, sg.tile, blocks);
+            auto part_of = [&](int c) {
+                return p.part + (size_t)(2 * (2 * c + rank) + parts.slot(c)) * p.nmax * kTileRows +
+                       tid;
+            };
+            // the pair of channels that this lane stores; N even: both or neither exist
+            uint16_t *out = p.out + ((size_t)g * p.M + m0) * p.N + (chan & ~1);
+            const bool words = p.N % 2 == 0 && reinterpret_cast<uintptr_t>(p.out) % 4 == 0;
+            // Columns n0 .. n0 + 15 of this lane's channel.  Two columns (tokens) a
+            // word; neighbouring lanes (channels) exchange, so that the even lane
+            // stores both channels of the first token and the odd lane both of the
+            // second.
+            auto store = [&](int n0, const float (&v)[kStepCols]) {
+                uint16_t *to = out + (size_t)(n0 + (lane & 1)) * p.N;
+                const int left = rows - n0 - (lane & 1);
+#pragma unroll
+                for (int i = 0; i < kStepCols; i += 2) {
+                    const float2 s2 = *reinterpret_cast<const float2 *>(&sx[n0 + i]);
+                    const __nv_bfloat162 o =
+                        __floats2bfloat162_rn(__fmul_rn(__fmul_rn(v[i], s2.x), sw),
+                                              __fmul_rn(__fmul_rn(v[i + 1], s2.y), sw));
+                    const uint32_t mine = *reinterpret_cast<const uint32_t *>(&o);
+                    const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
+                    const uint32_t both = __byte_perm(lane & 1 ? other : mine, lane & 1 ? mine : other,
+                                                      lane & 1 ? 0x7632 : 0x5410);
+                    uint16_t *at = to + (size_t)i * p.N;
+                    if (words) {
+                        if (live && i < left) *reinterpret_cast<uint32_t *>(at) = both;
+                    } else if (i < left) {  // odd N or address: rows start off a word
+                        if ((chan & ~1) < p.N) at[0] = (uint16_t)both;
+                        if ((chan | 1) < p.N) at[1] = (uint16_t)(both >> 16);
+                    }
+                }
+            };
+            bool ok = ptx::mbar_park<false>(&acc_full[acc.at], acc.parity, kWaitNs) && !s_failed;
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) {
                 s_failed = 1;
                 break;
             }
             tc::fence_after_sync();
-            int g, r, m0, rows;
-            T.of(sg.tile, g, r, m0, rows);
-            const uint32_t acc = taddr + b * ring.nmax + ((uint32_t)(tid & ~31) << 16);
-            const bool whole = sg.k0 == 0 && sg.k1 == blocks;
-            const Parts parts(whole ? Cut(1, 1, blocks) : ct, whole ? 0 : sg.tile, blocks);
-            auto part_of = [&](int c) {
-                return p.part + ((size_t)(2 * c + parts.slot(c)) * p.nmax) * kTileRows + tid;
-            };
-            for (int i = tid; i < rows; i += 128)
-                s_sx[i] = __ldg(p.x_scale + (size_t)g * p.M + m0 + i);
-            if (!whole) {
-                float *to = part_of(cta);
-                for (int n0 = 0; n0 < rows; n0 += 16) {
-                    uint32_t v[16];
-                    tc::ld_32x16(acc + n0, v);
-                    tc::wait_ld();
+            const uint32_t from = taddr + acc.at * ring.nmax + ((uint32_t)(warp * 32) << 16);
+            float *to = whole ? nullptr : part_of(pair);
+            for (int n0 = 0; n0 < rows; n0 += kStepCols) {
+                uint32_t u[kStepCols];
+                float v[kStepCols];
+                tc::ld_32x16(from + n0, u);
+                tc::wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (n0 + i < rows) __stcg(to + (n0 + i) * kTileRows, __uint_as_float(v[i]));
-                }
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&acc_free[b]);
-                __threadfence();
-                epi_sync();
-                if (tid == 0) {
-                    int *m = &p.header->merged[0][parts.c0][0];
-                    s_last = atomicAdd(m, 1) == parts.count() - 1;
-                    if (s_last) *m = 0;  // for the next call
-                }
-                epi_sync();
-                if (!s_last) continue;
-                __threadfence();
-            } else {
-                epi_sync();
-            }
-            const int chan = r * kTileRows + tid;
-            const bool live = chan < p.N;
-            const float sw = live ? __ldg(p.w_scale + (size_t)g * p.N + chan) : 0.0f;
-            uint16_t *out = p.out + ((size_t)g * p.M + m0) * p.N + chan;
-            for (int n0 = 0; n0 < rows; n0 += 16) {
-                float v[16];
+                for (int i = 0; i < kStepCols; ++i) v[i] = __uint_as_float(u[i]);
                 if (whole) {
-                    uint32_t u[16];
-                    tc::ld_32x16(acc + n0, u);
-                    tc::wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(u[i]);
+                    store(n0, v);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-                    for (int c = parts.c0; c <= parts.c1; ++c) {
-                        const float *from = part_of(c);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (n0 + i < rows) v[i] += __ldcg(from + (n0 + i) * kTileRows);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    if (n0 + i < rows && live) {
-                        const __nv_bfloat16 o = __float2bfloat16_rn(
-                            __fmul_rn(__fmul_rn(v[i], s_sx[n0 + i]), sw));
-                        out[(size_t)(n0 + i) * p.N] = *reinterpret_cast<const uint16_t *>(&o);
-                    }
+                    for (int i = 0; i < kStepCols; ++i)
+                        if (n0 + i < rows) __stcg(to + (n0 + i) * kTileRows, v[i]);
                 }
             }
-            if (whole) {
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&acc_free[b]);
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_cluster(ptx::cluster_smem(&acc_free[acc.at], 0));
+            if (whole) continue;
+            __threadfence();
+            __syncwarp();
+            int last = 0;
+            if (lane == 0) {
+                int *m = &p.header->merged[0][2 * parts.c0 + rank][warp];
+                last = atomicAdd(m, 1) == parts.count() - 1;
+                if (last) *m = 0;  // for the next call
+                __threadfence();
             }
-            epi_sync();  // s_sx is free again
+            if (!__shfl_sync(0xffffffffu, last, 0)) continue;
+            for (int n0 = 0; n0 < rows; n0 += kStepCols) {
+                float v[kStepCols];
+#pragma unroll
+                for (int i = 0; i < kStepCols; ++i) v[i] = 0.0f;
+                for (int c = parts.c0; c <= parts.c1; c += 2) {  // two parts in flight
+                    const float *f = part_of(c) + (size_t)n0 * kTileRows;
+                    const bool more = c < parts.c1;
+                    const float *f2 = more ? part_of(c + 1) + (size_t)n0 * kTileRows : f;
+                    float a[kStepCols], b[kStepCols];
+#pragma unroll
+                    for (int i = 0; i < kStepCols; ++i) {
+                        const int at = n0 + i < rows ? i * kTileRows : 0;
+                        a[i] = __ldcg(f + at);
+                        b[i] = __ldcg(f2 + at);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kStepCols; ++i) {
+                        v[i] += a[i];
+                        if (more) v[i] += b[i];
+                    }
+                }
+                store(n0, v);
+            }
         }
     }
 
     __syncwarp();
+    if (warp == kMmaWarp && rank != 0)  // CTA 0's products read this CTA's memory too
+        ptx::mbar_park<false>(&drained, 0, kWaitNs);
+    __syncwarp();
     tc::fence_before_sync();
-    __syncthreads();
+    ptx::cluster_sync();
+    tc::fence_after_sync();
     if (tid == 0 && s_failed) atomicOr(&p.header->flags, MOE_DEVICE_FLAG_WAIT_TIMEOUT);
-    if (warp == kMmaWarp) tc::tmem_dealloc(taddr, kTmemCols);
+    if (warp == kMmaWarp) tc::tmem_dealloc_pair(taddr, kTmemCols);
 }
 
 }  // namespace
 
 int gemm_int8_nmax(int M) {
-    if (M <= 16) return 16;
-    const int n = (M + 31) / 32 * 32;  // whole TMA boxes
-    return n < kMaxCols ? n : kMaxCols;
+    int n = 16;  // a power of two: halves of whole TMA boxes
+    while (n < M && n < kMaxCols) n *= 2;
+    return n;
 }
 
 cudaError_t launch_gemm_int8(GemmInt8Params p, int num_sms, cudaStream_t st) {
     if (p.G < 1 || p.G > kGemmInt8MaxGroups || p.M < 1 || p.N < 1 || p.H < 16 || p.H % 16 != 0)
         return cudaErrorInvalidValue;
     Ring ring;
-    p.nmax = gemm_int8_nmax(p.M);
-    ring.nmax = p.nmax;
-    ring.box = p.nmax < 32 ? 16 : 32;
-    const int raw = kWeightBytes + ring.nmax * kAtom, half = ring.nmax * kAtom;
-    const int room = (int)kMaxDynamic - 1024;
-    // at least two widened halves, then raw stages, then more halves
-    ring.halves = ring.nmax > 128 ? 2 : 4;
-    ring.stages = (room - ring.halves * half) / raw;
+    p.nmax = ring.nmax = gemm_int8_nmax(p.M);
+    ring.box = ring.nmax / 2 < 32 ? ring.nmax / 2 : 32;
+    const int half = ring.nmax / 2 * kAtom, raw = kWeightBytes + half;
+    // a half in each group's hands, and three ahead of the products
+    ring.halves = kGroups + 3;
+    ring.stages = ((int)kMaxDynamic - 1024 - ring.halves * half) / raw;
     if (ring.stages > kMaxStages) ring.stages = kMaxStages;
     if (ring.stages < 2) return cudaErrorInvalidValue;
     const size_t smem = 1024 + (size_t)ring.stages * raw + (size_t)ring.halves * half;
     CUtensorMap mx, mw;
-    if (!make_map(&mx, p.xq, (long long)p.G * p.M, p.H, ring.box, true) ||
-        !make_map(&mw, p.wq, (long long)p.G * p.N, p.H, kTileRows, true))
+    const long long H = p.H;
+    const long long ext_x[3] = {H, p.M, p.G}, str_x[3] = {1, H, H * p.M};
+    const long long ext_w[3] = {H, p.N, p.G}, str_w[3] = {1, H, H * p.N};
+    const int box_x[3] = {kAtom, ring.box, 1}, box_w[3] = {kAtom, kTileRows, 1};
+    if (!make_map_nd(&mx, p.xq, 3, ext_x, str_x, box_x, true) ||
+        !make_map_nd(&mw, p.wq, 3, ext_w, str_w, box_w, true))
         return cudaErrorInvalidValue;
     static std::atomic<unsigned long long> raised{0};
     cudaError_t err = raise_smem_limit_once(gemm_int8_kernel, kMaxDynamic, raised);
     if (err != cudaSuccess) return err;
-    const int grid = num_sms < kStreamMaxCtas ? num_sms : kStreamMaxCtas;
+    int grid = num_sms < kStreamMaxCtas ? num_sms : kStreamMaxCtas;
+    grid -= grid % 2;
+    if (grid < 2) return cudaErrorInvalidValue;
     gemm_int8_kernel<<<grid, kThreads, smem, st>>>(mx, mw, p, ring);
     return cudaGetLastError();
 }

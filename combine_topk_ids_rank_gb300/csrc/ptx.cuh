@@ -88,6 +88,73 @@ __device__ __forceinline__ bool mbar_wait_timed(uint64_t *bar, uint32_t parity,
     }
 }
 
+// ---- clusters ---------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// Barrier of all threads of the cluster (memory ordered at cluster scope).
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile(
+        "barrier.cluster.arrive.release.aligned;\n\t"
+        "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Address in CTA `rank` of the cluster of this CTA's shared memory at `p`.
+__device__ __forceinline__ uint32_t cluster_smem(const void *p, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+
+// One arrival on a barrier of any CTA of the cluster.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                     cluster_addr)
+                 : "memory");
+}
+
+// ---- waits of kernels with many waiting warps ---------------------------------
+
+// mbar_wait_timed whose probes suspend the warp in hardware for up to kParkNs
+// (it wakes when the phase completes) instead of coming back at once: probes
+// go through the queue that the working warps' loads, stores and shuffles use.
+// CLUSTER: also orders what other CTAs of the cluster wrote before they arrived.
+constexpr uint32_t kParkNs = 20000;
+template <bool CLUSTER>
+__device__ __forceinline__ bool mbar_park(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
+    auto probe = [&] {
+        uint32_t done;
+        if (CLUSTER)
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(done)
+                : "r"(smem_u32(bar)), "r"(parity), "r"(kParkNs)
+                : "memory");
+        else
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(done)
+                : "r"(smem_u32(bar)), "r"(parity), "r"(kParkNs)
+                : "memory");
+        return done != 0;
+    };
+    if (probe()) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        for (int i = 0; i < 4; ++i)
+            if (probe()) return true;
+        if (globaltimer_ns() - t0 > limit_ns) return false;
+    }
+}
+
 // ---- 1-D bulk copies --------------------------------------------------------
 
 // global -> shared, completion counted in bytes on `bar`.  Addresses and size
