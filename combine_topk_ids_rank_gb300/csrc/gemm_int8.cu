@@ -315,7 +315,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&raw_free[st.at]);
-                    ptx::mbar_arrive_cluster(ptx::cluster_smem(&wide_full[slot.at], 0));
+                    ptx::mbar_arrive_pair(ptx::cluster_smem(&wide_full[slot.at], 0));
                 }
             }
         }
@@ -379,7 +379,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive(&raw_free[st.at]);
-                        ptx::mbar_arrive_cluster(ptx::cluster_smem(&half_full[hf.at], 0));
+                        ptx::mbar_arrive_pair(ptx::cluster_smem(&half_full[hf.at], 0));
                     }
                 }
             }
@@ -414,20 +414,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // word; neighbouring lanes (channels) exchange, so that the even lane
             // stores both channels of the first token and the odd lane both of the
             // second.
+            const uint32_t pick = lane & 1 ? 0x3276u : 0x5410u;
             auto store = [&](int n0, const float (&v)[kStepCols]) {
-                uint16_t *to = out + (size_t)(n0 + (lane & 1)) * p.N;
+                uint16_t *at = out + (size_t)(n0 + (lane & 1)) * p.N;
                 const int left = rows - n0 - (lane & 1);
 #pragma unroll
-                for (int i = 0; i < kStepCols; i += 2) {
+                for (int i = 0; i < kStepCols; i += 2, at += 2 * (size_t)p.N) {
                     const float2 s2 = *reinterpret_cast<const float2 *>(&sx[n0 + i]);
                     const __nv_bfloat162 o =
                         __floats2bfloat162_rn(__fmul_rn(__fmul_rn(v[i], s2.x), sw),
                                               __fmul_rn(__fmul_rn(v[i + 1], s2.y), sw));
                     const uint32_t mine = *reinterpret_cast<const uint32_t *>(&o);
-                    const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
-                    const uint32_t both = __byte_perm(lane & 1 ? other : mine, lane & 1 ? mine : other,
-                                                      lane & 1 ? 0x7632 : 0x5410);
-                    uint16_t *at = to + (size_t)i * p.N;
+                    const uint32_t both =
+                        __byte_perm(mine, __shfl_xor_sync(0xffffffffu, mine, 1), pick);
                     if (words) {
                         if (live && i < left) *reinterpret_cast<uint32_t *>(at) = both;
                     } else if (i < left) {  // odd N or address: rows start off a word
@@ -462,7 +461,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_cluster(ptx::cluster_smem(&acc_free[acc.at], 0));
+            if (lane == 0) ptx::mbar_arrive_pair(ptx::cluster_smem(&acc_free[acc.at], 0));
             if (whole) continue;
             __threadfence();
             __syncwarp();
