@@ -57,7 +57,7 @@ constexpr int kMaxStages = 12, kMaxHalves = 8;
 constexpr int kRowGroup = 8;              // row tiles of a raster group
 constexpr int kStepCols = 16;             // token columns an epilogue step takes
 // dynamic shared memory: 227 KB a CTA less the static tables
-constexpr size_t kMaxDynamic = (227 - 13) * 1024;
+constexpr size_t kMaxDynamic = (227 - 15) * 1024;
 
 struct Ring {
     int nmax;      // tokens of a tile, at most
@@ -66,45 +66,61 @@ struct Ring {
     int halves;    // widened token tiles: nmax / 2 rows of 64 f16
 };
 
-// The tiles of a call: groups in turn; in a group, blocks of kRowGroup row
-// tiles, token tile outer and row tile inner.
+// The tiles of a call: groups in turn, those with the widest tiles first; in a
+// group, blocks of kRowGroup row tiles, token tile outer and row tile inner.
 struct Tiles {
-    const int *first;   // [G + 1]
-    const int *count;   // [G] token rows
+    const int *first;        // [G + 1] of the groups in this order
+    const uint16_t *order;   // [G]
+    const int *count;        // [G] token rows of a group
     int G, rtiles, nmax;
     __device__ int token_tiles(int c) const { return (c + nmax - 1) / nmax; }
+    // token rows of a tile: evened out over the group's tiles, a multiple of 16
+    __device__ int width(int c, int k) const {
+        return (k == 1 ? c + 15 : (c + k - 1) / k + 15) / 16 * 16;
+    }
     __device__ void of(int t, int &g, int &r, int &m0, int &rows) const {
         int lo = 0, hi = G - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
             if (first[mid] <= t) lo = mid; else hi = mid - 1;
         }
-        g = lo;
-        // token rows of a tile: evened out over the group's tiles, a multiple of 16
-        const int c = count[g], k = token_tiles(c), w = ((c + k - 1) / k + 15) / 16 * 16;
-        const int u = t - first[g], block = u / (kRowGroup * k);
+        g = order[lo];
+        const int c = count[g], k = token_tiles(c), u = t - first[lo];
+        if (k == 1) {
+            m0 = 0;
+            r = u;
+            rows = c;
+            return;
+        }
+        const int w = width(c, k), block = u / (kRowGroup * k);
         const int in = min(kRowGroup, rtiles - block * kRowGroup);
         const int v = u - block * kRowGroup * k;
-        m0 = v / in * w;
-        r = block * kRowGroup + v % in;
+        m0 = v / in;
+        r = block * kRowGroup + v - m0 * in;
+        m0 *= w;
         rows = min(w, c - m0);
     }
 };
 
-// The work of a pair in order: its parts of the cut tiles, then whole tiles.
+// The work of a pair in order: its parts of the cut tiles, which are the last
+// ones, then a tile of each whole wave, to and fro, so that every pair gets
+// its share of wide and narrow tiles.
 struct Work {
     Segments segs;
-    int tile, tiles, step, blocks;
-    __device__ Work(const Cut &ct, int cut_tiles, int tiles_, int blocks_, int pair, int pairs)
-        : segs(ct, pair, blocks_), tile(cut_tiles + pair), tiles(tiles_), step(pairs),
+    int wave, waves, pair, pairs, blocks;
+    __device__ Work(const Cut &ct, int waves_, int blocks_, int pair_, int pairs_)
+        : segs(ct, pair_, blocks_), wave(0), waves(waves_), pair(pair_), pairs(pairs_),
           blocks(blocks_) {}
     __device__ bool next(Segment &s) {
-        if (segs.next(s)) return true;
-        if (tile >= tiles) return false;
-        s.tile = tile;
+        if (segs.next(s)) {
+            s.tile += waves * pairs;
+            return true;
+        }
+        if (wave >= waves) return false;
+        s.tile = wave * pairs + (wave & 1 ? pairs - 1 - pair : pair);
         s.k0 = 0;
         s.k1 = blocks;
-        tile += step;
+        ++wave;
         return true;
     }
 };
@@ -120,6 +136,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __shared__ uint64_t half_full[kMaxHalves], half_free[kMaxHalves];
     __shared__ uint64_t acc_full[2], acc_free[2], drained;
     __shared__ int s_first[kGemmInt8MaxGroups + 1], s_count[kGemmInt8MaxGroups];
+    __shared__ uint16_t s_order[kGemmInt8MaxGroups];
+    __shared__ int s_widths[kMaxCols / 16 + 1];
     __shared__ __align__(16) float s_sx[4][kMaxCols];  // the tile's token scales, a warp each
     __shared__ uint32_t s_taddr;
     __shared__ volatile int s_failed;
@@ -133,11 +151,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto raw_w = [&](int s) { return smem + s * raw_bytes; };
     auto raw_x = [&](int s) { return smem + s * raw_bytes + kWeightBytes; };
 
-    for (int g = tid; g < p.G; g += kThreads) {
-        int c = p.M;
-        if (p.counts != nullptr) c = min(max(__ldg(p.counts + g), 0), p.M);
-        s_count[g] = c;
-    }
     if (warp == kMmaWarp) tc::tmem_alloc_pair(&s_taddr, kTmemCols);
     if (tid < kMaxStages) {
         ptx::mbar_init(&raw_full[tid], 1);
@@ -164,14 +177,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc::prefetch_map(&map_w);
         tc::prefetch_map(&map_x);
     }
+    if (tid <= kMaxCols / 16) s_widths[tid] = 0;
+    ptx::grid_dependency_wait();  // nothing of the caller's memory is touched before
+    ptx::launch_dependents();
+    for (int g = tid; g < p.G; g += kThreads) {
+        int c = p.M;
+        if (p.counts != nullptr) c = min(max(__ldg(p.counts + g), 0), p.M);
+        s_count[g] = c;
+        if (p.G == 1) s_order[g] = 0;
+    }
     tc::fence_before_sync();
     __syncthreads();
+    // the pair's barriers are set up before either arrives on the other's
+    ptx::cluster_arrive();
     const int rtiles = (p.N + kPairRows - 1) / kPairRows;
-    const Tiles T{s_first, s_count, p.G, rtiles, ring.nmax};
+    const Tiles T{s_first, s_order, s_count, p.G, rtiles, ring.nmax};
+    if (p.G > 1) {  // groups by the width of their tiles, stable
+        const auto width = [&](int g) {
+            const int c = s_count[g];
+            return c > 0 ? T.width(c, T.token_tiles(c)) / 16 : 0;
+        };
+        for (int g = tid; g < p.G; g += kThreads) atomicAdd(&s_widths[width(g)], 1);
+        __syncthreads();
+        if (warp <= kMaxCols / 16) {
+            const int mine = kMaxCols / 16 - warp;  // this warp's width
+            int at = 0;
+            for (int w = mine + 1; w <= kMaxCols / 16; ++w) at += s_widths[w];
+            for (int g0 = 0; g0 < p.G; g0 += 32) {
+                const bool hit = g0 + lane < p.G && width(g0 + lane) == mine;
+                const unsigned m = __ballot_sync(0xffffffffu, hit);
+                if (hit) s_order[at + __popc(m & ((1u << lane) - 1u))] = (uint16_t)(g0 + lane);
+                at += __popc(m);
+            }
+        }
+        __syncthreads();
+    }
     if (warp == 0) {  // exclusive prefix of the groups' tiles
         int sum = 0;
         for (int g0 = 0; g0 < p.G; g0 += 32) {
-            const int g = g0 + lane, n = g < p.G ? T.token_tiles(s_count[g]) * rtiles : 0;
+            const int g = g0 + lane;
+            const int n = g < p.G ? T.token_tiles(s_count[s_order[g]]) * rtiles : 0;
             int s = n;
             for (int o = 1; o < 32; o <<= 1) {
                 const int v = __shfl_up_sync(0xffffffffu, s, o);
@@ -182,10 +227,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (lane == 0) s_first[p.G] = sum;
     }
-    // the pair's barriers are set up before either arrives on the other's
-    __syncwarp();
-    ptx::cluster_sync();
-    tc::fence_after_sync();
+    __syncthreads();
 
     const uint32_t taddr = s_taddr;
     const int tiles = s_first[p.G], blocks = (p.H + kBlockK - 1) / kBlockK;
@@ -193,15 +235,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // the rest is under a quarter of a wave (parts of a few k-blocks each cost
     // more than they balance), is cut by k.
     int waves = tiles / pairs;
-    if (waves > 0 && tiles % pairs != 0 && tiles % pairs * 4 < pairs) --waves;
+    const int rest = tiles - waves * pairs;
+    if (waves > 0 && rest != 0 && rest * 4 < pairs) --waves;
     const int cut_tiles = tiles - waves * pairs;
     // (a merge costs about 4 units' time and 16 more for every 256 token columns)
-    const Cut ct = cut(cut_tiles, blocks, pairs, 4 + ring.nmax / 16,
-                       ring.nmax <= 32 ? kAlone : 16);
+    const Cut ct = ring.nmax <= 32 ? cut<true>(cut_tiles, blocks, pairs, 4 + ring.nmax / 16)
+                                   : cut<false>(cut_tiles, blocks, pairs, 4 + ring.nmax / 16);
     const int nacc = 2 * ring.nmax <= kMaxCols ? 2 : 1;  // accumulators
     const uint32_t slots_at = taddr + kMaxCols;
-    Work work(ct, cut_tiles, tiles, blocks, pair, pairs);
+    Work work(ct, waves, blocks, pair, pairs);
     Segment sg;
+    ptx::cluster_wait();
+    tc::fence_after_sync();
 
     if (warp == kProducerWarp) {
         if (ptx::elect_one()) {
@@ -402,7 +447,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             __syncwarp();
             const bool whole = sg.k0 == 0 && sg.k1 == blocks;
             Parts parts;
-            if (!whole) parts = Parts(ct, sg.tile, blocks);
+            if (!whole) parts = Parts(ct, sg.tile - waves * pairs, blocks);
             auto part_of = [&](int c) {
                 return p.part + (size_t)(2 * (2 * c + rank) + parts.slot(c)) * p.nmax * kTileRows +
                        tid;
@@ -545,8 +590,7 @@ cudaError_t launch_gemm_int8(GemmInt8Params p, int num_sms, cudaStream_t st) {
     int grid = num_sms < kStreamMaxCtas ? num_sms : kStreamMaxCtas;
     grid -= grid % 2;
     if (grid < 2) return cudaErrorInvalidValue;
-    gemm_int8_kernel<<<grid, kThreads, smem, st>>>(mx, mw, p, ring);
-    return cudaGetLastError();
+    return launch_pdl(gemm_int8_kernel, dim3(grid), dim3(kThreads), smem, st, mx, mw, p, ring);
 }
 
 }  // namespace moe

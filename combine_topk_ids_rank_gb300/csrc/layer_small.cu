@@ -243,8 +243,8 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
     const int blocks0 = (p.H + kBlockK - 1) / kBlockK, blocks1 = (p.I + kBlockK - 1) / kBlockK;
     // (merging parts takes about 2.5 us, a unit 0.7 us of bf16 weights, half of it of 8-bit)
     constexpr int kMerge = S::kWiden ? 7 : 4;
-    const Cut cuts[2] = {cut(A * tiles0, blocks0, ctas, kMerge, kAlone),
-                         cut(A * tiles1, blocks1, ctas, kMerge, kAlone)};
+    const Cut cuts[2] = {cut<true>(A * tiles0, blocks0, ctas, kMerge),
+                         cut<true>(A * tiles1, blocks1, ctas, kMerge)};
     auto tile_of = [&](int phase, int tile, int &a, int &r) {
         if (phase == 0) {
             a = tile / tiles0;

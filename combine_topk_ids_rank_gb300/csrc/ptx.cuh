@@ -96,11 +96,17 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     return r;
 }
 
-// Barrier of all threads of the cluster (memory ordered at cluster scope).
+// Barrier of all threads of the cluster (memory ordered at cluster scope), in
+// two halves and as one.
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile(
-        "barrier.cluster.arrive.release.aligned;\n\t"
-        "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 
 // Address in CTA `rank` of the cluster of this CTA's shared memory at `p`.

@@ -8,14 +8,20 @@
 // whatever is computed from it is NaN.  With counts, rows j >= counts[g] of
 // plane g are neither read nor written.
 //
-// The quotients are the correctly rounded x / scale through one reciprocal
-// per row and remainder steps (fp8.cuh explains them); the rounding to an
-// integer adds and keeps 1.5 * 2^23, whose neighbours are one apart.
+// The quotients come from one reciprocal per row and remainder steps (fp8.cuh
+// explains them): two steps, which give the correctly rounded x / scale, for
+// fp32 rows; for bf16 rows one step, which leaves the same nearest integer for
+// every pair of a bf16 maximum and a bf16 value (there are 128 x 128 pairs of
+// significands and nine binades in which a code is not zero; the tests go
+// through all of them).  The rounding to an integer adds and keeps 1.5 * 2^23,
+// whose neighbours are one apart.
 //
 // Memory bound: each element is read once and its code written once.  One
 // CTA a row, the row in registers, 16 bytes a thread and load.
 #include "fp8.cuh"
+#include "kernels.h"
 #include "layer.h"
+#include "ptx.cuh"
 
 namespace moe {
 namespace {
@@ -32,20 +38,29 @@ __device__ __forceinline__ fp8::RowScale int8_scale(float amax) {
     return r;
 }
 
-__device__ __forceinline__ uint32_t code(float q) {  // low byte: the nearest integer
-    return __float_as_uint(__fadd_rn(q, 12582912.0f));
+// The low byte of each word: the nearest integers to a / s and b / s.
+template <bool SCALED, bool BF16>
+__device__ __forceinline__ void code2(float a, float b, const fp8::RowScale &r, uint32_t &ca,
+                                      uint32_t &cb) {
+    x2::f2 xs = x2::pack(a, b);
+    if (SCALED) xs = x2::mul(xs, x2::pack(r.m, r.m));
+    const x2::f2 y = x2::pack(r.y, r.y), nsd = x2::pack(-r.sd, -r.sd);
+    x2::f2 q = x2::mul(xs, y);
+    q = x2::fma(x2::fma(q, nsd, xs), y, q);
+    if (!BF16) q = x2::fma(x2::fma(q, nsd, xs), y, q);
+    q = x2::add(q, x2::pack(12582912.0f, 12582912.0f));
+    float fa, fb;
+    x2::unpack(q, fa, fb);
+    ca = __float_as_uint(fa);
+    cb = __float_as_uint(fb);
 }
 
-template <bool SCALED>
+template <bool SCALED, bool BF16>
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], const fp8::RowScale &r) {
     uint32_t c[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float a, b;
-        fp8::quotient2<SCALED>(v[2 * i], v[2 * i + 1], r, a, b);
-        c[2 * i] = code(a);
-        c[2 * i + 1] = code(b);
-    }
+    for (int i = 0; i < 4; ++i)
+        code2<SCALED, BF16>(v[2 * i], v[2 * i + 1], r, c[2 * i], c[2 * i + 1]);
     uint2 o;
     o.x = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
     o.y = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
@@ -96,6 +111,8 @@ struct Vec8 {
 template <int VPT, bool BF16>
 __global__ void __launch_bounds__(kMaxWarps * 32) quantize_int8_kernel(const QuantInt8Params p) {
     __shared__ uint32_t red[2][kMaxWarps];
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
     const int tid = threadIdx.x, nt = blockDim.x, H8 = p.H / 8;
     const long long total = (long long)p.groups * p.rows;
     // the first row from r on that is in use (the whole CTA alike)
@@ -142,7 +159,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) quantize_int8_kernel(const Qua
                 float f[8];
                 x[j].values(f);
                 uint2 o = make_uint2(0, 0);
-                if (finite) o = s.m == 1.0f ? codes8<false>(f, s) : codes8<true>(f, s);
+                if (finite) o = s.m == 1.0f ? codes8<false, BF16>(f, s) : codes8<true, BF16>(f, s);
                 q[v] = o;
             }
         }
@@ -156,11 +173,8 @@ cudaError_t launch_t(const QuantInt8Params &p, int threads, int num_sms, cudaStr
     const long long total = (long long)p.groups * p.rows;
     const long long most = (long long)num_sms * 16;
     const unsigned grid = (unsigned)(total < most ? total : most);
-    if (p.bf16)
-        quantize_int8_kernel<VPT, true><<<grid, threads, 0, st>>>(p);
-    else
-        quantize_int8_kernel<VPT, false><<<grid, threads, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_pdl(p.bf16 ? quantize_int8_kernel<VPT, true> : quantize_int8_kernel<VPT, false>,
+                      dim3(grid), dim3(threads), 0, st, p);
 }
 
 }  // namespace
@@ -168,12 +182,13 @@ cudaError_t launch_t(const QuantInt8Params &p, int threads, int num_sms, cudaStr
 cudaError_t launch_quantize_rows_int8(const QuantInt8Params &p, int num_sms, cudaStream_t st) {
     if (p.H % 8 != 0 || p.H < 8 || p.H > 16384) return cudaErrorInvalidValue;
     const int H8 = p.H / 8;
-    int threads = (H8 + 31) / 32 * 32;
-    if (threads > kMaxWarps * 32) threads = kMaxWarps * 32;
-    const int vpt = (H8 + threads - 1) / threads;
-    if (vpt <= 1) return launch_t<1>(p, threads, num_sms, st);
-    if (vpt <= 2) return launch_t<2>(p, threads, num_sms, st);
-    if (vpt <= 4) return launch_t<4>(p, threads, num_sms, st);
+    // as many vectors a thread as 256 threads need, then as few threads as those need
+    int vpt = (H8 + kMaxWarps * 32 - 1) / (kMaxWarps * 32);
+    vpt = vpt <= 2 ? vpt : (vpt <= 4 ? 4 : 8);
+    const int threads = ((H8 + vpt - 1) / vpt + 31) / 32 * 32;
+    if (vpt == 1) return launch_t<1>(p, threads, num_sms, st);
+    if (vpt == 2) return launch_t<2>(p, threads, num_sms, st);
+    if (vpt == 4) return launch_t<4>(p, threads, num_sms, st);
     return launch_t<8>(p, threads, num_sms, st);
 }
 

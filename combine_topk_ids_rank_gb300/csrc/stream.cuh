@@ -46,14 +46,14 @@ struct Cut {
 
 // `tiles` of `blocks` units over the CTAs: cut anywhere, or between tiles only.
 // Cutting inside tiles evens out the CTAs' work but adds the parts' way
-// through memory, about `merge` units' time.  A CTA alone can do `alone` / 16
-// of its even share of the work in the same time: where the memory's rate is
-// the bound some CTAs may idle before whole tiles cost anything.
-constexpr int kAlone = 24;
-__device__ __forceinline__ Cut cut(int tiles, int blocks, int ctas, int merge, int alone) {
+// through memory, about `merge` units' time.  SHARED: the memory's rate is the
+// bound, and a CTA alone can do 1.5 times its even share of the work in the
+// same time, so some CTAs may idle before whole tiles cost anything.
+template <bool SHARED>
+__device__ __forceinline__ Cut cut(int tiles, int blocks, int ctas, int merge) {
     const int total = tiles * blocks, rounds = (tiles + ctas - 1) / ctas;
     const int even = (total + ctas - 1) / ctas;
-    const int whole = max(rounds * blocks * 16 / alone, even);
+    const int whole = max(SHARED ? rounds * blocks * 2 / 3 : rounds * blocks, even);
     if (whole <= even + merge || total < ctas) return Cut(tiles, min(tiles, ctas), blocks);
     return Cut(total, ctas, 1);
 }

@@ -21,7 +21,9 @@
 //     shifts the winner's list;
 //   fp32 logits: the key fills the word; the winner lane clears the first
 //     value equal to the maximum and looks for its next.
+#include "kernels.h"
 #include "layer.h"
+#include "ptx.cuh"
 
 #include <cuda_bf16.h>
 
@@ -96,6 +98,16 @@ __device__ __forceinline__ void load_row(const TopkGateParams &p, long long t, i
     }
 }
 
+// The logit of a bf16 key (any low half).
+__device__ __forceinline__ float value_of(uint32_t k) {
+    return __uint_as_float((k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu)) & 0xffff0000u);
+}
+
+// exp(v - top), 1 where they are equal (also for +inf, whose difference is NaN)
+__device__ __forceinline__ float exp_from(float v, float top) {
+    return v == top ? 1.0f : expf(v - top);
+}
+
 // Sorts descending.
 template <int VPL>
 __device__ __forceinline__ void sort_down(uint32_t (&k)[VPL]) {
@@ -120,6 +132,8 @@ __device__ __forceinline__ void sort_down(uint32_t (&k)[VPL]) {
 
 template <int VPL, bool BF16, bool VEC>
 __global__ void __launch_bounds__(kThreads) topk_gate_kernel(const TopkGateParams p) {
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
     const int lane = threadIdx.x & 31;
     const long long warps = (long long)gridDim.x * (kThreads / 32);
     for (long long t = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -206,6 +220,110 @@ __global__ void __launch_bounds__(kThreads) topk_gate_kernel(const TopkGateParam
     }
 }
 
+// bf16 logits, at most 256 experts and top-8: kTokens tokens a warp, whose
+// selections (eight lanes a token) are weighted together.  About 160
+// instructions a token, which is the bound beside 540 bytes of traffic.
+constexpr int kTokens = 4;
+template <int VPL, bool VEC>
+__global__ void __launch_bounds__(kThreads) topk_gate_bf16_kernel(const TopkGateParams p) {
+    static_assert(VPL == 2 || VPL == 4 || VPL == 8, "values a lane");
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
+    const int lane = threadIdx.x & 31, e0 = lane * VPL;
+    const long long stride = (long long)gridDim.x * (kThreads / 32) * kTokens;
+    // low halves of the keys, two a word: lower ids are larger
+    uint32_t tag[VPL / 2];
+#pragma unroll
+    for (int j = 0; j < VPL / 2; ++j)
+        tag[j] = (uint32_t)(0xffff - e0 - 2 * j) | ((uint32_t)(0xffff - e0 - 2 * j - 1) << 16);
+    for (long long t0 = ((long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kTokens;
+         t0 < p.tokens; t0 += stride) {
+        uint32_t w[kTokens][VPL / 2];
+#pragma unroll
+        for (int q = 0; q < kTokens; ++q) {
+            const long long t = t0 + q < p.tokens ? t0 + q : p.tokens - 1;
+            const uint16_t *row = static_cast<const uint16_t *>(p.logits) + t * p.row_stride + e0;
+            if (VEC && e0 + VPL <= p.E) {
+                if constexpr (VPL == 8) {
+                    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row));
+                    w[q][0] = v.x, w[q][1] = v.y, w[q][2] = v.z, w[q][3] = v.w;
+                } else if constexpr (VPL == 4) {
+                    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(row));
+                    w[q][0] = v.x, w[q][1] = v.y;
+                } else {
+                    w[q][0] = __ldg(reinterpret_cast<const uint32_t *>(row));
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < VPL / 2; ++j) {
+                    const uint32_t lo = e0 + 2 * j < p.E ? row[2 * j] : 0xff80u;  // -inf past E
+                    const uint32_t hi = e0 + 2 * j + 1 < p.E ? row[2 * j + 1] : 0xff80u;
+                    w[q][j] = lo | hi << 16;
+                }
+            }
+        }
+        uint32_t sel = 0;  // lane 8 q + k: selection k of token q (0: none)
+        float total = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kTokens; ++q) {
+            uint32_t key[VPL];
+            float sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < VPL / 2; ++j) {
+                // order-preserving 16-bit keys of both halves; 0 for NaN and -inf
+                __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162 *>(&w[q][j]);
+                const uint32_t open = __hgt2_mask(x, __float2bfloat162_rn(-INFINITY));
+                x = __hadd2(x, __float2bfloat162_rn(0.0f));  // -0 becomes +0: equal logits
+                const uint32_t u = *reinterpret_cast<const uint32_t *>(&x);
+                uint32_t sign;  // all ones over a negative half (prmt's sign mode)
+                asm("prmt.b32 %0, %1, 0, 0xbb99;" : "=r"(sign) : "r"(u));
+                const uint32_t k = (u ^ (sign | 0x80008000u)) & open;
+                key[2 * j] = __byte_perm(k, tag[j], 0x1054);
+                key[2 * j + 1] = __byte_perm(k, tag[j], 0x3276);
+            }
+            if (!p.sigmoid && !p.renormalize) {  // softmax over the whole row
+                uint32_t m = 0;
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) m = max(m, key[j]);
+                const float top = value_of(__reduce_max_sync(kFull, m));
+#pragma unroll
+                for (int j = 0; j < VPL; ++j)
+                    if (key[j] > 0xffffu) sum += exp_from(value_of(key[j]), top);
+                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+                if (lane >> 3 == q) total = sum;
+            }
+            sort_down<VPL>(key);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (k >= p.K) break;
+                const uint32_t m = __reduce_max_sync(kFull, key[0]);
+                if (key[0] == m) {
+                    // (what is further down than the rounds left is not looked at)
+#pragma unroll
+                    for (int j = 0; j < VPL - 1; ++j)
+                        if (j < 7 - k) key[j] = key[j + 1];
+                    if (VPL - 1 < 8 - k) key[VPL - 1] = 0;
+                }
+                if (lane == 8 * q + k) sel = m;
+            }
+        }
+        const int q = lane >> 3, k = lane & 7;
+        const bool some = sel > 0xffffu;
+        const float v = value_of(sel), top = __shfl_sync(kFull, v, lane & 24);
+        float s = 0.0f;
+        if (some) s = p.sigmoid ? 1.0f / (1.0f + expf(-v)) : exp_from(v, top);
+        if (p.renormalize) {
+            total = s;
+            for (int o = 4; o > 0; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
+        }
+        if ((p.renormalize || !p.sigmoid) && s != 0.0f) s = s / total;
+        if (k < p.K && t0 + q < p.tokens) {
+            p.topk_ids[(t0 + q) * p.K + k] = some ? (int)(0xffffu - (sel & 0xffffu)) : -1;
+            p.topk_w[(t0 + q) * p.K + k] = s * p.scale;
+        }
+    }
+}
+
 template <int VPL>
 cudaError_t launch_t(const TopkGateParams &p, int num_sms, cudaStream_t st) {
     const long long want = (p.tokens + kThreads / 32 - 1) / (kThreads / 32);
@@ -214,12 +332,21 @@ cudaError_t launch_t(const TopkGateParams &p, int num_sms, cudaStream_t st) {
     const uintptr_t vec = VPL * (p.bf16 ? 2 : 4) < 16 ? VPL * (p.bf16 ? 2 : 4) : 16;
     const bool aligned = reinterpret_cast<uintptr_t>(p.logits) % vec == 0 &&
                          (uintptr_t)(p.row_stride * (p.bf16 ? 2 : 4)) % vec == 0;
+    if constexpr (VPL <= 8) {
+        if (p.bf16 && p.K <= 8) {
+            const long long fw = (p.tokens + kTokens - 1) / kTokens;
+            const long long fc = (fw + kThreads / 32 - 1) / (kThreads / 32);
+            const int fast = (int)(fc < num_sms * 8LL ? fc : num_sms * 8LL);
+            return launch_pdl(aligned ? topk_gate_bf16_kernel<VPL, true>
+                                      : topk_gate_bf16_kernel<VPL, false>,
+                              dim3(fast), dim3(kThreads), 0, st, p);
+        }
+    }
     auto kern = p.bf16 ? (aligned ? topk_gate_kernel<VPL, true, true>
                                   : topk_gate_kernel<VPL, true, false>)
                        : (aligned ? topk_gate_kernel<VPL, false, true>
                                   : topk_gate_kernel<VPL, false, false>);
-    kern<<<grid, kThreads, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_pdl(kern, dim3(grid), dim3(kThreads), 0, st, p);
 }
 
 }  // namespace

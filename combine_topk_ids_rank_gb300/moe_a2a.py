@@ -413,7 +413,7 @@ if hasattr(getattr(_torch, "_C", None), "_cuda_getCurrentRawStream"):
 
 def _empty(shape, dtype, device, stream):
     """A new tensor that belongs to the stream it is going to be used on."""
-    if stream is None:
+    if stream is None or _raw_stream(stream, device) == _current_stream(device.index):
         return _torch.empty(shape, dtype=dtype, device=device)
     if not hasattr(stream, "cuda_stream"):
         stream = _torch.cuda.ExternalStream(int(stream), device=device)

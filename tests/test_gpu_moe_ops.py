@@ -197,6 +197,20 @@ def test_quantize_ties_extremes_and_special_rows(api):
     assert (q[6] == -127).all() and torch.isnan(s[4]) and torch.isnan(s[5])
 
 
+def test_quantize_bf16_every_pair_of_significands(api):
+    # each bf16 row maximum in a binade with every bf16 value whose code can
+    # differ from zero: 128 x 128 significands, ten binades, both signs
+    m = np.arange(128, 256).astype(np.float64)
+    x = np.ldexp(m[None, :], -np.arange(10)[:, None]).reshape(-1)
+    rows = np.minimum(x[None, :], m[:, None])
+    rows = np.concatenate([m[:, None], rows, -rows, np.zeros((128, 7))], 1)
+    for scale in (1.0, 2.0 ** -110, 2.0 ** 100):
+        t = torch.from_numpy((rows * scale).astype(np.float32)).to(DEV)
+        assert torch.equal(t.to(torch.bfloat16).float(), t)
+        check_quant(api, t.to(torch.bfloat16))
+        check_quant(api, t)
+
+
 def test_quantize_planes_leave_padding_alone(api):
     G, rows, H = 5, 7, 256
     x = torch.randn((G, rows, H), generator=gen(9), device=DEV).to(torch.bfloat16)
