@@ -51,9 +51,11 @@ constexpr int kThreads = (kMmaWarp + 1) * 32;
 constexpr int kPairRows = 2 * kTileRows;  // channels of a tile
 constexpr int kMaxCols = 256;             // tokens of a tile
 constexpr int kTmemCols = 512;            // accumulators, then widened weights
-constexpr int kSlots = 4, kSlotCols = kBlockK / 2;
+constexpr int kSlots = 3, kSlotCols = kBlockK / 2;
 constexpr int kWeightBytes = kTileRows * kBlockK;
-constexpr int kMaxStages = 12, kMaxHalves = 8;
+constexpr int kMaxStages = 12;
+// widened token tiles (64 f16 of nmax / 2 rows): one in each group's hands, three ahead
+constexpr int kHalves = kGroups + 3;
 constexpr int kRowGroup = 8;              // row tiles of a raster group
 constexpr int kStepCols = 16;             // token columns an epilogue step takes
 // dynamic shared memory: 227 KB a CTA less the static tables
@@ -63,7 +65,6 @@ struct Ring {
     int nmax;      // tokens of a tile, at most
     int box;       // rows of a token TMA box
     int stages;    // raw stages: 128 weight rows + nmax / 2 token rows of 128 codes
-    int halves;    // widened token tiles: nmax / 2 rows of 64 f16
 };
 
 // The tiles of a call: groups in turn, those with the widest tiles first; in a
@@ -132,8 +133,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t raw_full[kMaxStages], raw_free[kMaxStages];
     // (full: CTA 0's, both CTAs arrive; free: either CTA's own)
-    __shared__ uint64_t wide_full[kSlots], wide_free[kSlots];
-    __shared__ uint64_t half_full[kMaxHalves], half_free[kMaxHalves];
+    __shared__ uint64_t half_full[kHalves], half_free[kHalves];
     __shared__ uint64_t acc_full[2], acc_free[2], drained;
     __shared__ int s_first[kGemmInt8MaxGroups + 1], s_count[kGemmInt8MaxGroups];
     __shared__ uint16_t s_order[kGemmInt8MaxGroups];
@@ -155,12 +155,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (tid < kMaxStages) {
         ptx::mbar_init(&raw_full[tid], 1);
         ptx::mbar_init(&raw_free[tid], 4 + 2 * kGroupWarps);
-        if (tid < kSlots) {
-            ptx::mbar_init(&wide_full[tid], 2 * 4);
-            ptx::mbar_init(&wide_free[tid], 1);
-        }
-        if (tid < kMaxHalves) {
-            ptx::mbar_init(&half_full[tid], 2 * kGroupWarps);
+        if (tid < kHalves) {
+            ptx::mbar_init(&half_full[tid], 2 * (kGroupWarps + 4));
             ptx::mbar_init(&half_free[tid], 1);
         }
         if (tid < 2) {
@@ -261,7 +257,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int w0 = r * kPairRows + rank * kTileRows, x0 = m0 + rank * half;
                 for (int kb = sg.k0; kb < sg.k1; ++kb, st.next()) {
                     const int s = (int)st.at;
-                    if (!ptx::mbar_park<false>(&raw_free[s], st.parity ^ 1u, kWaitNs)) {
+                    if (!ptx::mbar_park(&raw_free[s], st.parity ^ 1u, kWaitNs)) {
                         s_failed = 1;
                         break;
                     }
@@ -276,71 +272,80 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // copies still in flight land before shared memory goes away
             for (int i = 0; i < ring.stages; ++i, st.next()) {
                 const uint32_t last = st.parity ^ 1u;
-                if (issued >> st.at & 1u) ptx::mbar_park<false>(&raw_full[st.at], last, kWaitNs);
+                if (issued >> st.at & 1u) ptx::mbar_park(&raw_full[st.at], last, kWaitNs);
             }
         }
     } else if (warp == kMmaWarp) {
         if (rank == 0 && ptx::elect_one()) {
-            Turn slot(kSlots), hf(ring.halves), acc(nacc);
+            Turn hf(kHalves), acc(nacc);
+            uint32_t slot = 0;  // halves of the widened weight tiles
+            const uint64_t bd0 = tc::smem_desc_sw128(ptx::smem_u32(wide));
             for (; !s_failed && work.next(sg); acc.next()) {
                 int g, r, m0, rows;
                 T.of(sg.tile, g, r, m0, rows);
                 const uint32_t idesc = tc::idesc_f16_f32(kPairRows, (rows + 15) / 16 * 16);
                 const uint32_t d = taddr + acc.at * ring.nmax;
-                if (!ptx::mbar_park<true>(&acc_free[acc.at], acc.parity ^ 1u, kWaitNs)) {
+                if (!ptx::mbar_park(&acc_free[acc.at], acc.parity ^ 1u, kWaitNs)) {
                     s_failed = 1;
                     break;
                 }
                 tc::fence_after_sync();
-                for (int kb = sg.k0; kb < sg.k1 && !s_failed; ++kb, slot.next()) {
-                    const uint32_t a = slots_at + slot.at * kSlotCols;
-                    if (!ptx::mbar_park<true>(&wide_full[slot.at], slot.parity, kWaitNs)) {
+                const int halves = 2 * (sg.k1 - sg.k0);
+                for (int h = 0; h < halves; ++h, hf.next()) {
+                    if (!ptx::mbar_park(&half_full[hf.at], hf.parity, kWaitNs)) {
                         s_failed = 1;
                         break;
                     }
+                    tc::fence_after_sync();
+                    const uint32_t a = slots_at + slot * (kSlotCols / 2);
+                    const uint64_t bd = bd0 + (uint64_t)(hf.at * (half_bytes / 16));
 #pragma unroll
-                    for (int hh = 0; hh < 2; ++hh, hf.next()) {
-                        if (!ptx::mbar_park<true>(&half_full[hf.at], hf.parity, kWaitNs)) {
-                            s_failed = 1;
-                            break;
-                        }
-                        tc::fence_after_sync();
-                        const uint64_t bd =
-                            tc::smem_desc_sw128(ptx::smem_u32(wide + hf.at * half_bytes));
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            tc::mma_f16_ta_pair(d, a + 32 * hh + 8 * kk, bd + 2 * kk, idesc,
-                                                kb != sg.k0 || hh != 0 || kk != 0);
-                        tc::commit_pair(&half_free[hf.at]);
-                    }
-                    tc::commit_pair(&wide_free[slot.at]);
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc::mma_f16_ta_pair(d, a + 8 * kk, bd + 2 * kk, idesc, h != 0 || kk != 0);
+                    tc::commit_pair(&half_free[hf.at]);
+                    slot = (slot + 1) % (2 * kSlots);
                 }
                 tc::commit_pair(&acc_full[acc.at]);
             }
             tc::commit_pair(&drained);  // before tensor memory is freed
-            ptx::mbar_park<false>(&drained, 0, kWaitNs);
+            ptx::mbar_park(&drained, 0, kWaitNs);
         }
     } else if (warp >= kWeightWarp0 && warp < kTokenWarp0) {
         // Thread l of a group of four warps owns weight row l of the CTA's half =
         // lane l; the groups take the units in turn.
         const int row = (tid - kWeightWarp0 * 32) & 127, group = (warp - kWeightWarp0) >> 2;
-        Turn st(ring.stages), slot(kSlots);
+        // A weight tile counts for both halves of its unit, on their barriers.  Its
+        // slot is free when the second half of the unit kSlots before has been
+        // multiplied; by then the barriers' last uses are over too (kHalves halves
+        // before, not later than that one), and that half's barrier completes its
+        // next phase only after this unit's products.
+        static_assert(kHalves >= 2 * kSlots, "a barrier's uses would overlap");
+        Turn st(ring.stages), hf(kHalves), done(kHalves);
+        done.next();
         bool ok = true;
         uint32_t n = 0;
         while (ok && !warp_flag(&s_failed) && work.next(sg)) {
-            for (int kb = sg.k0; kb < sg.k1; ++kb, st.next(), slot.next(), ++n) {
+            for (int kb = sg.k0; kb < sg.k1; ++kb, st.next(), ++n) {
+                const uint32_t first = hf.at;
+                hf.next();
+                const uint32_t second = hf.at;
+                hf.next();
+                const Turn free = done;
+                if (n >= kSlots) {
+                    done.next();
+                    done.next();
+                }
                 if (n % kWeightGroups != (uint32_t)group) continue;
-                ok = __all_sync(0xffffffffu,
-                                ptx::mbar_park<false>(&raw_full[st.at], st.parity, kWaitNs) &&
-                                    ptx::mbar_park<false>(&wide_free[slot.at], slot.parity ^ 1u,
-                                                         kWaitNs));
+                ok = ptx::mbar_park(&raw_full[st.at], st.parity, kWaitNs);
+                if (n >= kSlots) ok = ok && ptx::mbar_park(&half_free[free.at], free.parity, kWaitNs);
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) {
                     s_failed = 1;
                     break;
                 }
                 tc::fence_after_sync();
                 const uint8_t *src = raw_w(st.at) + row * kAtom;
-                const uint32_t dst = slots_at + slot.at * kSlotCols + ((uint32_t)(row & ~31) << 16);
+                const uint32_t dst = slots_at + n % kSlots * kSlotCols + ((uint32_t)(row & ~31) << 16);
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
                     uint32_t w[32];
@@ -360,7 +365,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&raw_free[st.at]);
-                    ptx::mbar_arrive_pair(ptx::cluster_smem(&wide_full[slot.at], 0));
+                    ptx::mbar_arrive_pair(ptx::cluster_smem(&half_full[first], 0));
+                    ptx::mbar_arrive_pair(ptx::cluster_smem(&half_full[second], 0));
                 }
             }
         }
@@ -371,7 +377,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // (and write) 8 different 16-byte columns of the swizzled rows, so no bank
         // is hit twice.
         const int group = (warp - kTokenWarp0) / kGroupWarps, w = (warp - kTokenWarp0) % kGroupWarps;
-        Turn st(ring.stages), hf(ring.halves);
+        Turn st(ring.stages), hf(kHalves);
         bool ok = true;
         uint32_t h = 0;
         while (ok && !warp_flag(&s_failed) && work.next(sg)) {
@@ -383,8 +389,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int hh = 0; hh < 2; ++hh, hf.next(), ++h) {
                     if (h % kGroups != (uint32_t)group) continue;
                     ok = __all_sync(0xffffffffu,
-                                    ptx::mbar_park<false>(&raw_full[st.at], st.parity, kWaitNs) &&
-                                        ptx::mbar_park<false>(&half_free[hf.at], hf.parity ^ 1u,
+                                    ptx::mbar_park(&raw_full[st.at], st.parity, kWaitNs) &&
+                                        ptx::mbar_park(&half_free[hf.at], hf.parity ^ 1u,
                                                              kWaitNs));
                     if (!ok) {
                         s_failed = 1;
@@ -480,7 +486,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
             };
-            bool ok = ptx::mbar_park<false>(&acc_full[acc.at], acc.parity, kWaitNs) && !s_failed;
+            bool ok = ptx::mbar_park(&acc_full[acc.at], acc.parity, kWaitNs) && !s_failed;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) {
                 s_failed = 1;
@@ -546,7 +552,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     __syncwarp();
     if (warp == kMmaWarp && rank != 0)  // CTA 0's products read this CTA's memory too
-        ptx::mbar_park<false>(&drained, 0, kWaitNs);
+        ptx::mbar_park(&drained, 0, kWaitNs);
     __syncwarp();
     tc::fence_before_sync();
     ptx::cluster_sync();
@@ -570,12 +576,10 @@ cudaError_t launch_gemm_int8(GemmInt8Params p, int num_sms, cudaStream_t st) {
     p.nmax = ring.nmax = gemm_int8_nmax(p.M);
     ring.box = ring.nmax / 2 < 32 ? ring.nmax / 2 : 32;
     const int half = ring.nmax / 2 * kAtom, raw = kWeightBytes + half;
-    // a half in each group's hands, and three ahead of the products
-    ring.halves = kGroups + 3;
-    ring.stages = ((int)kMaxDynamic - 1024 - ring.halves * half) / raw;
+    ring.stages = ((int)kMaxDynamic - 1024 - kHalves * half) / raw;
     if (ring.stages > kMaxStages) ring.stages = kMaxStages;
     if (ring.stages < 2) return cudaErrorInvalidValue;
-    const size_t smem = 1024 + (size_t)ring.stages * raw + (size_t)ring.halves * half;
+    const size_t smem = 1024 + (size_t)ring.stages * raw + (size_t)kHalves * half;
     CUtensorMap mx, mw;
     const long long H = p.H;
     const long long ext_x[3] = {H, p.M, p.G}, str_x[3] = {1, H, H * p.M};

@@ -132,28 +132,17 @@ __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
 // mbar_wait_timed whose probes suspend the warp in hardware for up to kParkNs
 // (it wakes when the phase completes) instead of coming back at once: probes
 // go through the queue that the working warps' loads, stores and shuffles use.
-// CLUSTER: also orders what other CTAs of the cluster wrote before they arrived.
 constexpr uint32_t kParkNs = 20000;
-template <bool CLUSTER>
 __device__ __forceinline__ bool mbar_park(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
     auto probe = [&] {
         uint32_t done;
-        if (CLUSTER)
-            asm volatile(
-                "{\n\t.reg .pred p;\n\t"
-                "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-                "selp.u32 %0, 1, 0, p;\n\t}"
-                : "=r"(done)
-                : "r"(smem_u32(bar)), "r"(parity), "r"(kParkNs)
-                : "memory");
-        else
-            asm volatile(
-                "{\n\t.reg .pred p;\n\t"
-                "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
-                "selp.u32 %0, 1, 0, p;\n\t}"
-                : "=r"(done)
-                : "r"(smem_u32(bar)), "r"(parity), "r"(kParkNs)
-                : "memory");
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(kParkNs)
+            : "memory");
         return done != 0;
     };
     if (probe()) return true;
