@@ -51,11 +51,10 @@ constexpr int kThreads = (kMmaWarp + 1) * 32;
 constexpr int kPairRows = 2 * kTileRows;  // channels of a tile
 constexpr int kMaxCols = 256;             // tokens of a tile
 constexpr int kTmemCols = 512;            // accumulators, then widened weights
-constexpr int kSlots = 3, kSlotCols = kBlockK / 2;
+constexpr int kSlotCols = kBlockK / 2;    // a widened weight tile
+constexpr int kMaxUnits = 4;
 constexpr int kWeightBytes = kTileRows * kBlockK;
 constexpr int kMaxStages = 12;
-// widened token tiles (64 f16 of nmax / 2 rows): one in each group's hands, three ahead
-constexpr int kHalves = kGroups + 3;
 constexpr int kRowGroup = 8;              // row tiles of a raster group
 constexpr int kStepCols = 16;             // token columns an epilogue step takes
 // dynamic shared memory: 227 KB a CTA less the static tables
@@ -65,6 +64,8 @@ struct Ring {
     int nmax;      // tokens of a tile, at most
     int box;       // rows of a token TMA box
     int stages;    // raw stages: 128 weight rows + nmax / 2 token rows of 128 codes
+    int units;     // widened units: a weight tile in tensor memory, and nmax / 2 token
+                   // rows of 128 f16, as two tiles of 64, in shared memory
 };
 
 // The tiles of a call: groups in turn, those with the widest tiles first; in a
@@ -133,7 +134,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t raw_full[kMaxStages], raw_free[kMaxStages];
     // (full: CTA 0's, both CTAs arrive; free: either CTA's own)
-    __shared__ uint64_t half_full[kHalves], half_free[kHalves];
+    __shared__ uint64_t unit_full[kMaxUnits], unit_free[kMaxUnits];
     __shared__ uint64_t acc_full[2], acc_free[2], drained;
     __shared__ int s_first[kGemmInt8MaxGroups + 1], s_count[kGemmInt8MaxGroups];
     __shared__ uint16_t s_order[kGemmInt8MaxGroups];
@@ -155,9 +156,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (tid < kMaxStages) {
         ptx::mbar_init(&raw_full[tid], 1);
         ptx::mbar_init(&raw_free[tid], 4 + 2 * kGroupWarps);
-        if (tid < kHalves) {
-            ptx::mbar_init(&half_full[tid], 2 * (kGroupWarps + 4));
-            ptx::mbar_init(&half_free[tid], 1);
+        if (tid < kMaxUnits) {
+            ptx::mbar_init(&unit_full[tid], 2 * (4 + 2 * kGroupWarps));
+            ptx::mbar_init(&unit_free[tid], 1);
         }
         if (tid < 2) {
             ptx::mbar_init(&acc_full[tid], 1);
@@ -277,8 +278,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kMmaWarp) {
         if (rank == 0 && ptx::elect_one()) {
-            Turn hf(kHalves), acc(nacc);
-            uint32_t slot = 0;  // halves of the widened weight tiles
+            Turn un(ring.units), acc(nacc);
             const uint64_t bd0 = tc::smem_desc_sw128(ptx::smem_u32(wide));
             for (; !s_failed && work.next(sg); acc.next()) {
                 int g, r, m0, rows;
@@ -290,20 +290,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     break;
                 }
                 tc::fence_after_sync();
-                const int halves = 2 * (sg.k1 - sg.k0);
-                for (int h = 0; h < halves; ++h, hf.next()) {
-                    if (!ptx::mbar_park(&half_full[hf.at], hf.parity, kWaitNs)) {
+                for (int kb = sg.k0; kb < sg.k1; ++kb, un.next()) {
+                    const uint32_t a = slots_at + un.at * kSlotCols;
+                    const uint64_t bd = bd0 + (uint64_t)(un.at * (half_bytes / 8));
+                    if (!ptx::mbar_park(&unit_full[un.at], un.parity, kWaitNs)) {
                         s_failed = 1;
                         break;
                     }
                     tc::fence_after_sync();
-                    const uint32_t a = slots_at + slot * (kSlotCols / 2);
-                    const uint64_t bd = bd0 + (uint64_t)(hf.at * (half_bytes / 16));
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        tc::mma_f16_ta_pair(d, a + 8 * kk, bd + 2 * kk, idesc, h != 0 || kk != 0);
-                    tc::commit_pair(&half_free[hf.at]);
-                    slot = (slot + 1) % (2 * kSlots);
+                    for (int kk = 0; kk < 8; ++kk)
+                        tc::mma_f16_ta_pair(d, a + 8 * kk,
+                                            bd + (kk >> 2) * (half_bytes / 16) + 2 * (kk & 3), idesc,
+                                            kb != sg.k0 || kk != 0);
+                    tc::commit_pair(&unit_free[un.at]);
                 }
                 tc::commit_pair(&acc_full[acc.at]);
             }
@@ -314,38 +314,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // Thread l of a group of four warps owns weight row l of the CTA's half =
         // lane l; the groups take the units in turn.
         const int row = (tid - kWeightWarp0 * 32) & 127, group = (warp - kWeightWarp0) >> 2;
-        // A weight tile counts for both halves of its unit, on their barriers.  Its
-        // slot is free when the second half of the unit kSlots before has been
-        // multiplied; by then the barriers' last uses are over too (kHalves halves
-        // before, not later than that one), and that half's barrier completes its
-        // next phase only after this unit's products.
-        static_assert(kHalves >= 2 * kSlots, "a barrier's uses would overlap");
-        Turn st(ring.stages), hf(kHalves), done(kHalves);
-        done.next();
+        Turn st(ring.stages), un(ring.units);
         bool ok = true;
         uint32_t n = 0;
         while (ok && !warp_flag(&s_failed) && work.next(sg)) {
-            for (int kb = sg.k0; kb < sg.k1; ++kb, st.next(), ++n) {
-                const uint32_t first = hf.at;
-                hf.next();
-                const uint32_t second = hf.at;
-                hf.next();
-                const Turn free = done;
-                if (n >= kSlots) {
-                    done.next();
-                    done.next();
-                }
+            for (int kb = sg.k0; kb < sg.k1; ++kb, st.next(), un.next(), ++n) {
                 if (n % kWeightGroups != (uint32_t)group) continue;
-                ok = ptx::mbar_park(&raw_full[st.at], st.parity, kWaitNs);
-                if (n >= kSlots) ok = ok && ptx::mbar_park(&half_free[free.at], free.parity, kWaitNs);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = __all_sync(0xffffffffu,
+                                ptx::mbar_park(&raw_full[st.at], st.parity, kWaitNs) &&
+                                    ptx::mbar_park(&unit_free[un.at], un.parity ^ 1u, kWaitNs));
                 if (!ok) {
                     s_failed = 1;
                     break;
                 }
                 tc::fence_after_sync();
                 const uint8_t *src = raw_w(st.at) + row * kAtom;
-                const uint32_t dst = slots_at + n % kSlots * kSlotCols + ((uint32_t)(row & ~31) << 16);
+                const uint32_t dst = slots_at + un.at * kSlotCols + ((uint32_t)(row & ~31) << 16);
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
                     uint32_t w[32];
@@ -365,8 +349,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&raw_free[st.at]);
-                    ptx::mbar_arrive_pair(ptx::cluster_smem(&half_full[first], 0));
-                    ptx::mbar_arrive_pair(ptx::cluster_smem(&half_full[second], 0));
+                    ptx::mbar_arrive_pair(ptx::cluster_smem(&unit_full[un.at], 0));
                 }
             }
         }
@@ -377,27 +360,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // (and write) 8 different 16-byte columns of the swizzled rows, so no bank
         // is hit twice.
         const int group = (warp - kTokenWarp0) / kGroupWarps, w = (warp - kTokenWarp0) % kGroupWarps;
-        Turn st(ring.stages), hf(kHalves);
+        Turn st(ring.stages), un(ring.units);
         bool ok = true;
         uint32_t h = 0;
         while (ok && !warp_flag(&s_failed) && work.next(sg)) {
             int g, r, m0, rows;
             T.of(sg.tile, g, r, m0, rows);
             const int half = (rows + 15) / 16 * 8;
-            for (int kb = sg.k0; kb < sg.k1 && ok; ++kb, st.next()) {
+            for (int kb = sg.k0; kb < sg.k1 && ok; ++kb, st.next(), un.next()) {
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh, hf.next(), ++h) {
+                for (int hh = 0; hh < 2; ++hh, ++h) {
                     if (h % kGroups != (uint32_t)group) continue;
                     ok = __all_sync(0xffffffffu,
                                     ptx::mbar_park(&raw_full[st.at], st.parity, kWaitNs) &&
-                                        ptx::mbar_park(&half_free[hf.at], hf.parity ^ 1u,
-                                                             kWaitNs));
+                                        ptx::mbar_park(&unit_free[un.at], un.parity ^ 1u, kWaitNs));
                     if (!ok) {
                         s_failed = 1;
                         break;
                     }
                     const uint8_t *src = raw_x(st.at);
-                    uint8_t *dst = wide + hf.at * half_bytes;
+                    uint8_t *dst = wide + (2 * un.at + hh) * half_bytes;
                     for (int row0 = lane; row0 < half; row0 += 32 * kBatch) {
                         uint4 v[kBatch][4 / kGroupWarps];  // loads first
 #pragma unroll
@@ -430,7 +412,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive(&raw_free[st.at]);
-                        ptx::mbar_arrive_pair(ptx::cluster_smem(&half_full[hf.at], 0));
+                        ptx::mbar_arrive_pair(ptx::cluster_smem(&unit_full[un.at], 0));
                     }
                 }
             }
@@ -576,10 +558,11 @@ cudaError_t launch_gemm_int8(GemmInt8Params p, int num_sms, cudaStream_t st) {
     p.nmax = ring.nmax = gemm_int8_nmax(p.M);
     ring.box = ring.nmax / 2 < 32 ? ring.nmax / 2 : 32;
     const int half = ring.nmax / 2 * kAtom, raw = kWeightBytes + half;
-    ring.stages = ((int)kMaxDynamic - 1024 - kHalves * half) / raw;
+    ring.units = ring.nmax > 128 ? 3 : kMaxUnits;
+    ring.stages = ((int)kMaxDynamic - 1024 - 2 * ring.units * half) / raw;
     if (ring.stages > kMaxStages) ring.stages = kMaxStages;
     if (ring.stages < 2) return cudaErrorInvalidValue;
-    const size_t smem = 1024 + (size_t)ring.stages * raw + (size_t)kHalves * half;
+    const size_t smem = 1024 + (size_t)ring.stages * raw + (size_t)2 * ring.units * half;
     CUtensorMap mx, mw;
     const long long H = p.H;
     const long long ext_x[3] = {H, p.M, p.G}, str_x[3] = {1, H, H * p.M};
