@@ -70,7 +70,7 @@ struct LayerSmallParams {
     int T, K, E, H, I;
     int format;                // MOE_FORMAT_*
     // set by the launcher
-    int nmax, ring_bytes;
+    int nmax, ring_bytes, kshift;
 };
 cudaError_t launch_layer_small(LayerSmallParams p, int num_sms, cudaStream_t st);
 

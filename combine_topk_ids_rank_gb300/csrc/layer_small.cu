@@ -63,31 +63,28 @@ constexpr size_t kMaxDynamic = (227 - 2) * 1024;
 // The lists at the front of dynamic shared memory, for E experts and P pairs
 // (token, k).
 struct Lists {
-    float *gate;       // [P] gate of (t, k), set where kept
-    float *given;      // [P] the caller's weight of (t, k)
+    int16_t *kept;     // [P] expert of (t, k), -1 where dropped; 16-byte aligned, whole 16 bytes
+    float *gate;       // [P] gate of (t, k)
     int *count;        // [E] kept pairs of an expert
-    uint32_t *named;   // [32] experts in use, a bit each
     uint16_t *first;   // [E] first pair of an expert in use
     uint16_t *expert;  // [A] experts in use, ascending (A <= min(E, P))
     uint16_t *base;    // [A + 1] their first pairs
     uint16_t *token;   // [P] token of a pair
-    int16_t *place;    // [P] pair of (t, k), -1 where dropped (at first: its expert)
-    int16_t *kept;     // [P] expert of (t, k), -1 where dropped
+    int16_t *place;    // [P] pair of (t, k), -1 where dropped
     __host__ __device__ static int bytes(int E, int P) {
-        return (P * 8 + E * 4 + 128 + E * 2 + (E < P ? E : P) * 4 + 2 + P * 6 + 15) / 16 * 16;
+        const int P8 = (P + 7) / 8 * 8;
+        return (P8 * 2 + P * 4 + E * 4 + E * 2 + (E < P ? E : P) * 4 + 2 + P * 4 + 15) / 16 * 16;
     }
     __device__ Lists(uint8_t *mem, int E, int P) {
         const int A = E < P ? E : P;
-        gate = reinterpret_cast<float *>(mem);
-        given = gate + P;
-        count = reinterpret_cast<int *>(given + P);
-        named = reinterpret_cast<uint32_t *>(count + E);
-        first = reinterpret_cast<uint16_t *>(named + 32);
+        kept = reinterpret_cast<int16_t *>(mem);
+        gate = reinterpret_cast<float *>(kept + (P + 7) / 8 * 8);
+        count = reinterpret_cast<int *>(gate + P);
+        first = reinterpret_cast<uint16_t *>(count + E);
         expert = first + E;
         base = expert + A;
         token = base + A + 1;
         place = reinterpret_cast<int16_t *>(token + P);
-        kept = place + P;
     }
 };
 
@@ -117,14 +114,6 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
     const Lists L(smem_raw, p.E, P);
     const uint32_t after = ptx::smem_u32(smem_raw) + Lists::bytes(p.E, P);
     uint8_t *ring = smem_raw + Lists::bytes(p.E, P) + ((1024u - (after & 1023u)) & 1023u);
-    // ---- lists: experts in use, ascending, and the pairs of each, by token ----
-    // (the ids' latency passes behind the set-up)
-    int id0 = -1;
-    float w0 = 0.0f;
-    if (tid < P) {
-        id0 = __ldg(p.topk_ids + tid);
-        w0 = __ldg(p.topk_w + tid);
-    }
     if (warp == kMmaWarp) tc::tmem_alloc(&s_taddr, S::kTmem);
     if (tid < kMaxStages) {
         ptx::mbar_init(&bar_a[tid], 1);
@@ -149,36 +138,64 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
         tc::prefetch_map(&map2);
     }
     for (int e = tid; e < p.E; e += S::kThreads) L.count[e] = 0;
-    if (warp == 1) L.named[lane] = 0;
-    for (int i = tid; i < P; i += S::kThreads) {
-        int id = i == tid ? id0 : __ldg(p.topk_ids + i);
-        if (id < -1 || id >= p.E) {
-            if (cta == 0) atomicOr(&p.header->flags, MOE_DEVICE_FLAG_BAD_EXPERT_ID);
-            id = -1;
+    ptx::launch_dependents();
+
+    // ---- lists: experts in use, ascending, and the pairs of each, by token ----
+    // Thread i takes (t, k) = (i >> kshift, i mod 2^kshift): a token's experts stand
+    // in one warp.  The first pair of a token that names an expert is kept, with the
+    // gates of all.
+    const int kshift = p.kshift, slots = p.T << kshift;
+    auto load = [&](int i, int &id, float &g) {
+        const int k = i & ((1 << kshift) - 1);
+        id = -1;
+        g = 0.0f;
+        if (i < slots && k < p.K) {
+            id = __ldg(p.topk_ids + (i >> kshift) * p.K + k);
+            g = __ldg(p.topk_w + (i >> kshift) * p.K + k);
         }
-        L.place[i] = (int16_t)id;
-        L.given[i] = i == tid ? w0 : __ldg(p.topk_w + i);
+    };
+    int id;
+    float g;
+    load(tid, id, g);
+    __syncthreads();  // the counts are zero
+    for (int i0 = warp * 32; i0 < slots; i0 += S::kThreads) {
+        const int i = i0 + lane, t = i >> kshift, k = i & ((1 << kshift) - 1);
+        const bool real = i < slots && k < p.K;
+        const int pair = t * p.K + k;
+        if (i0 >= S::kThreads) load(i, id, g);
+        if (real) {
+            if (id < -1 || id >= p.E) {
+                if (cta == 0) atomicOr(&p.header->flags, MOE_DEVICE_FLAG_BAD_EXPERT_ID);
+                id = -1;
+            }
+        }
+        // lanes of the same token and expert (a lane without one stands alone)
+        const unsigned same =
+            __match_any_sync(0xffffffffu, id >= 0 ? (t << 10 | id) : (int)(0x80000000u | lane));
+        const bool keep = id >= 0 && (same & ((1u << lane) - 1u)) == 0;
+        float sum = g;
+        for (unsigned more = __reduce_or_sync(0xffffffffu, same & (same - 1u)); more != 0;
+             more &= more - 1u) {  // repeats, by ascending lane
+            const int src = __ffs(more) - 1;
+            const float other = __shfl_sync(0xffffffffu, g, src);
+            if (keep && src != lane && (same >> src & 1u)) sum = __fadd_rn(sum, other);
+        }
+        if (real) {
+            L.kept[pair] = (int16_t)(keep ? id : -1);
+            L.gate[pair] = sum;
+        }
+        if (keep) atomicAdd(&L.count[id], 1);
     }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    // the first pair of a token that names an expert is kept, with the gates of all
-    for (int i = tid; i < P; i += S::kThreads) {
-        const int t0 = i / p.K * p.K, id = L.place[i];
-        bool keep = id >= 0;
-        for (int j = t0; j < i; ++j) keep = keep && L.place[j] != id;
-        L.kept[i] = (int16_t)(keep ? id : -1);
-        if (!keep) continue;
-        atomicAdd(&L.count[id], 1);
-        atomicOr(&L.named[id >> 5], 1u << (id & 31));
-        float g = L.given[i];
-        for (int j = i + 1; j < t0 + p.K; ++j)
-            if (L.place[j] == id) g = __fadd_rn(g, L.given[j]);
-        L.gate[i] = g;
-    }
-    __syncthreads();
     if (warp == 0) {  // lane l: experts 32 l .. 32 l + 31
-        uint32_t bits = L.named[lane];
+        uint32_t bits = 0;
+        for (int e0 = 0; e0 < p.E; e0 += 32) {
+            const unsigned m =
+                __ballot_sync(0xffffffffu, e0 + lane < p.E && L.count[e0 + lane] > 0);
+            if (lane == e0 >> 5) bits = m;
+        }
         int used = __popc(bits);
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, used, o);
@@ -214,15 +231,28 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
     // where the pairs stand; the weight producer needs none of it and goes ahead
     if (warp != kProducerWarp) {
         const int me = tid < kProducerWarp * 32 ? tid : tid - 32;
-        for (int i = me; i < P; i += S::kThreads - 32) {
-            const int id = L.kept[i];
+        for (int i0 = me & ~31; i0 < slots; i0 += S::kThreads - 32) {
+            const int i = i0 + lane, t = i >> kshift, k = i & ((1 << kshift) - 1);
+            if (i >= slots || k >= p.K) continue;
+            const int pair = t * p.K + k, id = L.kept[pair];
             int at = -1;
-            if (id >= 0) {
+            if (id >= 0) {  // behind the expert's pairs of the tokens before
                 at = L.first[id];
-                for (int j = 0; j < i; ++j) at += L.kept[j] == id;
-                L.token[at] = (uint16_t)(i / p.K);
+                const uint4 *kept8 = reinterpret_cast<const uint4 *>(L.kept);
+                const uint32_t both = (uint32_t)id << 16 | (uint32_t)id;
+                for (int j = 0; j <= pair; j += 8) {
+                    const uint4 v = kept8[j >> 3];
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t d = w[q] ^ both;
+                        at += ((d & 0xffffu) == 0 && j + 2 * q < pair) +
+                              (d < 0x10000u && j + 2 * q + 1 < pair);
+                    }
+                }
+                L.token[at] = (uint16_t)t;
             }
-            L.place[i] = (int16_t)at;
+            L.place[pair] = (int16_t)at;
         }
         asm volatile("bar.sync 2, %0;" ::"n"(S::kThreads - 32) : "memory");
     }
@@ -268,7 +298,7 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
                     const int e = L.expert[a];
                     for (int kb = sg.k0; kb < sg.k1; ++kb, st.next()) {
                         const int s = (int)st.at;
-                        if (!ptx::mbar_wait_timed(&bar_free[s], st.parity ^ 1u, kWaitNs)) {
+                        if (!ptx::mbar_park(&bar_free[s], st.parity ^ 1u, kWaitNs)) {
                             s_failed = 1;
                             break;
                         }
@@ -292,13 +322,15 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
             // copies still in flight land before shared memory goes away
             for (int i = 0; i < stages; ++i, st.next()) {  // (parity: of the stage's last use)
                 const uint32_t last = st.parity ^ 1u;
-                if (issued >> st.at & 1u) ptx::mbar_wait_timed(&bar_a[st.at], last, kWaitNs);
+                if (issued >> st.at & 1u) ptx::mbar_park(&bar_a[st.at], last, kWaitNs);
             }
         }
     } else if (warp == kMmaWarp) {
         if (ptx::elect_one()) {
             uint32_t it = 0;
             Turn st(stages), wide(kSlots);
+            const uint64_t ad0 = tc::smem_desc_sw128(ptx::smem_u32(ring));
+            const uint64_t half_a = kTileRows * kAtom / 16, half_b = b_half / 16;
             for (int phase = 0; phase < 2; ++phase) {
                 Segments segs(cuts[phase], cta, phase ? blocks1 : blocks0);
                 Segment sg;
@@ -309,19 +341,19 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
                     const int cols = phase ? (rows + 7) / 8 * 16 : (rows + 15) / 16 * 16;
                     const uint32_t idesc = tc::idesc_bf16_f32(kTileRows, cols);
                     const uint32_t b = it & 1u, d = taddr + b * kAccCols;
-                    if (!ptx::mbar_wait_timed(&acc_free[b], ((it >> 1) & 1u) ^ 1u, kWaitNs)) {
+                    if (!ptx::mbar_park(&acc_free[b], ((it >> 1) & 1u) ^ 1u, kWaitNs)) {
                         s_failed = 1;
                         break;
                     }
                     tc::fence_after_sync();
                     for (int kb = sg.k0; kb < sg.k1; ++kb, st.next(), wide.next()) {
                         const int s = (int)st.at;
-                        bool ok = ptx::mbar_wait_timed(&bar_b[s], st.parity, kWaitNs);
+                        bool ok = ptx::mbar_park(&bar_b[s], st.parity, kWaitNs);
                         if (S::kWiden)
-                            ok = ok && ptx::mbar_wait_timed(&wide_full[wide.at], wide.parity,
+                            ok = ok && ptx::mbar_park(&wide_full[wide.at], wide.parity,
                                                             kWaitNs);
                         else
-                            ok = ok && ptx::mbar_wait_timed(&bar_a[s], st.parity, kWaitNs);
+                            ok = ok && ptx::mbar_park(&bar_a[s], st.parity, kWaitNs);
                         if (!ok) {
                             s_failed = 1;
                             break;
@@ -330,9 +362,8 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
                         // token rows: written by cp.async (generic proxy), read next by
                         // the tensor cores (async proxy)
                         ptx::fence_proxy_async_smem();
-                        const uint64_t ad = tc::smem_desc_sw128(ptx::smem_u32(stage_a(s)));
-                        const uint64_t bd = tc::smem_desc_sw128(ptx::smem_u32(stage_b(s)));
-                        const uint64_t half_a = kTileRows * kAtom / 16, half_b = b_half / 16;
+                        const uint64_t ad = ad0 + (uint64_t)(s * (stage_bytes / 16));
+                        const uint64_t bd = ad + S::kA / 16;
                         const uint32_t at = taddr + 2 * kAccCols + wide.at * kSlotCols;
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk) {  // 16 k a step
@@ -351,7 +382,7 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
                 }
             }
             tc::commit(&drained);  // before tensor memory is freed
-            ptx::mbar_wait_timed(&drained, 0, kWaitNs);
+            ptx::mbar_park(&drained, 0, kWaitNs);
         }
     } else if (warp == kLoaderWarp0 || warp == kLoaderWarp0 + 1) {
         // Thread l copies 16-byte piece l % 16 (8 values) of the rows l / 16,
@@ -377,7 +408,7 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
                 const uint16_t *src = phase ? p.act + (size_t)base * 2 * p.I : p.x;
                 for (int kb = sg.k0; kb < sg.k1; ++kb, st.next()) {
                     const int s = (int)st.at;
-                    if (!__all_sync(0xffffffffu, ptx::mbar_wait_timed(
+                    if (!__all_sync(0xffffffffu, ptx::mbar_park(
                                                      &bar_free[s], st.parity ^ 1u, kWaitNs))) {
                         s_failed = 1;
                         break;
@@ -413,8 +444,8 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
             if ((n & 1u) != (uint32_t)group) continue;
             if (warp_flag(&s_failed)) break;
             const int s = (int)st.at, q = (int)wide.at;
-            const bool ok = ptx::mbar_wait_timed(&bar_a[s], st.parity, kWaitNs) &&
-                            ptx::mbar_wait_timed(&wide_free[q], wide.parity ^ 1u, kWaitNs);
+            const bool ok = ptx::mbar_park(&bar_a[s], st.parity, kWaitNs) &&
+                            ptx::mbar_park(&wide_free[q], wide.parity ^ 1u, kWaitNs);
             if (!__all_sync(0xffffffffu, ok)) {
                 s_failed = 1;
                 break;
@@ -458,7 +489,7 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
             for (; segs.next(sg); ++it) {
                 const uint32_t b = it & 1u;
                 ok = __all_sync(0xffffffffu,
-                                ptx::mbar_wait_timed(&acc_full[b], (it >> 1) & 1u, kWaitNs) &&
+                                ptx::mbar_park(&acc_full[b], (it >> 1) & 1u, kWaitNs) &&
                                     !s_failed);
                 if (!ok) {
                     s_failed = 1;
@@ -663,6 +694,8 @@ cudaError_t launch_layer_small(LayerSmallParams p, int num_sms, cudaStream_t st)
         p.H % 16 != 0 || p.I % 16 != 0 || p.H < 16 || p.I < 16)
         return cudaErrorInvalidValue;
     p.nmax = (p.T + 15) / 16 * 16;
+    p.kshift = 0;
+    while (1 << p.kshift < p.K) ++p.kshift;
     if (p.format == MOE_FORMAT_BF16) return launch_t<MOE_FORMAT_BF16>(p, num_sms, st);
     if (p.format == MOE_FORMAT_FP8_E4M3) return launch_t<MOE_FORMAT_FP8_E4M3>(p, num_sms, st);
     return launch_t<MOE_FORMAT_INT8>(p, num_sms, st);

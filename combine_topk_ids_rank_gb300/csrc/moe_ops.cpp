@@ -204,7 +204,7 @@ int moe_layer_small(const void *d_x, const int32_t *d_topk_ids, const float *d_t
     p.H = hidden;
     p.I = inter;
     p.format = format;
-    p.nmax = p.ring_bytes = 0;
+    p.nmax = p.ring_bytes = p.kshift = 0;
     return launch_layer_small(p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? MOE_OK
                : cuda_failed();

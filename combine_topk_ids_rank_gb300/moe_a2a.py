@@ -411,9 +411,9 @@ if hasattr(getattr(_torch, "_C", None), "_cuda_getCurrentRawStream"):
     _current_stream = _torch._C._cuda_getCurrentRawStream  # noqa: F811
 
 
-def _empty(shape, dtype, device, stream):
-    """A new tensor that belongs to the stream it is going to be used on."""
-    if stream is None or _raw_stream(stream, device) == _current_stream(device.index):
+def _empty(shape, dtype, device, stream, raw):
+    """A new tensor that belongs to the stream (`raw`) it is going to be used on."""
+    if stream is None or raw == _current_stream(device.index):
         return _torch.empty(shape, dtype=dtype, device=device)
     if not hasattr(stream, "cuda_stream"):
         stream = _torch.cuda.ExternalStream(int(stream), device=device)
@@ -444,17 +444,18 @@ def topk_gate(logits, top_k: int, scoring: int = MOE_SCORE_SOFTMAX, renormalize:
             raise ValueError("logits must be contiguous, or 2-D with dense rows")
         row_stride = logits.stride(0)
     shape = (*lead, top_k)
+    raw = _current_stream(device.index) if stream is None else _raw_stream(stream, device)
     if out_ids is None:
-        out_ids = _empty(shape, _torch.int32, device, stream)
+        out_ids = _empty(shape, _torch.int32, device, stream, raw)
     else:
         _expect(out_ids, _torch.int32, shape, device, "out_ids")
     if out_w is None:
-        out_w = _empty(shape, _torch.float32, device, stream)
+        out_w = _empty(shape, _torch.float32, device, stream, raw)
     else:
         _expect(out_w, _torch.float32, shape, device, "out_w")
     st = _lib.moe_topk_gate(logits.data_ptr(), bf16, logits.numel() // E if E else 0, row_stride,
                             E, top_k, scoring, bool(renormalize), scale, out_ids.data_ptr(),
-                            out_w.data_ptr(), _raw_stream(stream, device))
+                            out_w.data_ptr(), raw)
     if st != MOE_OK:
         raise MoeA2AError(st, "moe_topk_gate")
     return out_ids, out_w
@@ -482,17 +483,18 @@ def quantize_rows_int8(x, counts=None, out=None, scale=None, stream=None):
             raise ValueError("with counts x must be [groups, rows, hidden]")
         groups, rows = lead
         _expect(counts, _torch.int32, (groups,), device, "counts")
+    raw = _current_stream(device.index) if stream is None else _raw_stream(stream, device)
     if out is None:
-        out = _empty(shape, _torch.int8, device, stream)
+        out = _empty(shape, _torch.int8, device, stream, raw)
     else:
         _expect(out, _torch.int8, shape, device, "out")
     if scale is None:
-        scale = _empty(lead, _torch.float32, device, stream)
+        scale = _empty(lead, _torch.float32, device, stream, raw)
     else:
         _expect(scale, _torch.float32, tuple(lead), device, "scale")
     st = _lib.moe_quantize_rows_int8(x.data_ptr(), bf16, groups, rows, H, row_stride,
-                                     _ptr(counts), out.data_ptr(), scale.data_ptr(),
-                                     _raw_stream(stream, device))
+                                     0 if counts is None else counts.data_ptr(),
+                                     out.data_ptr(), scale.data_ptr(), raw)
     if st != MOE_OK:
         raise MoeA2AError(st, "moe_quantize_rows_int8")
     return out, scale
@@ -544,14 +546,14 @@ class MoeGemmInt8(_Scratch):
             _expect(counts, _torch.int32, (G,), dev, "counts")
         if rows > self.max_rows:
             raise MoeA2AError(MOE_ERR_CAPACITY, "moe_gemm_int8")
+        raw = _raw_stream(stream, dev)
         if out is None:
-            out = _empty((*lead, rows, N), _torch.bfloat16, dev, stream)
+            out = _empty((*lead, rows, N), _torch.bfloat16, dev, stream, raw)
         else:
             _expect(out, _torch.bfloat16, (*lead, rows, N), dev, "out")
         st = _lib.moe_gemm_int8(xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(),
                                 w_scale.data_ptr(), _ptr(counts), G, rows, N, H, out.data_ptr(),
-                                self._scratch_ptr, self._scratch_bytes,
-                                _raw_stream(stream, dev))
+                                self._scratch_ptr, self._scratch_bytes, raw)
         if st != MOE_OK:
             raise MoeA2AError(st, "moe_gemm_int8")
         return out
@@ -598,15 +600,16 @@ class MoeLayerSmall(_Scratch):
             _expect(w2_scale, _torch.float32, (E, H), dev, "w2_scale")
         if residual is not None:
             _expect(residual, _torch.bfloat16, (T, H), dev, "residual")
+        raw = _raw_stream(stream, dev)
         if out is None:
-            out = _empty((T, H), _torch.bfloat16, dev, stream)
+            out = _empty((T, H), _torch.bfloat16, dev, stream, raw)
         else:
             _expect(out, _torch.bfloat16, (T, H), dev, "out")
         st = _lib.moe_layer_small(x.data_ptr(), topk_ids.data_ptr(), topk_w.data_ptr(),
                                   w13.data_ptr(), _ptr(w13_scale), w2.data_ptr(),
                                   _ptr(w2_scale), _ptr(residual), T, K, E, H, I, self.fmt,
                                   out.data_ptr(), self._scratch_ptr, self._scratch_bytes,
-                                  _raw_stream(stream, dev))
+                                  raw)
         if st != MOE_OK:
             raise MoeA2AError(st, "moe_layer_small")
         return out
