@@ -45,7 +45,7 @@ using namespace stream;
 constexpr int kWeightWarp0 = 4, kWeightGroups = 2;
 constexpr int kTokenWarp0 = kWeightWarp0 + 4 * kWeightGroups, kTokenWarps = 8;
 constexpr int kGroupWarps = 2, kGroups = kTokenWarps / kGroupWarps;
-constexpr int kBatch = 4;                 // rows a token lane has in hand
+constexpr int kBatch = 4;                 // row blocks a token warp has in hand
 constexpr int kProducerWarp = kTokenWarp0 + kTokenWarps, kMmaWarp = kProducerWarp + 1;
 constexpr int kThreads = (kMmaWarp + 1) * 32;
 constexpr int kPairRows = 2 * kTileRows;  // channels of a tile
@@ -355,10 +355,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= kTokenWarp0 && warp < kTokenWarp0 + kTokenWarps) {
         // Groups of kGroupWarps warps take the halves in turn, so that one group's
-        // loads, fence and arrival pass while the others compute.  Warp w of a
-        // group takes every kGroupWarps-th 16-code chunk: 8 consecutive lanes read
-        // (and write) 8 different 16-byte columns of the swizzled rows, so no bank
-        // is hit twice.
+        // loads, fence and arrival pass while the others compute.  The warps of a
+        // group take blocks of 8 rows in turn, lane l the 16-code chunk l / 8 of row
+        // l % 8: 8 consecutive lanes read (and write) 8 different 16-byte columns of
+        // the swizzled rows, so no bank is hit twice.
         const int group = (warp - kTokenWarp0) / kGroupWarps, w = (warp - kTokenWarp0) % kGroupWarps;
         Turn st(ring.stages), un(ring.units);
         bool ok = true;
@@ -380,34 +380,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     const uint8_t *src = raw_x(st.at);
                     uint8_t *dst = wide + (2 * un.at + hh) * half_bytes;
-                    for (int row0 = lane; row0 < half; row0 += 32 * kBatch) {
-                        uint4 v[kBatch][4 / kGroupWarps];  // loads first
+                    const int c = lane >> 3, r8 = lane & 7, blocks8 = half >> 3;
+                    // (row mod 8 is r8: the swizzle is the lane's own)
+                    const uint8_t *from = src + r8 * kAtom + (((4 * hh + c) ^ r8) << 4);
+                    uint8_t *to0 = dst + r8 * kAtom + (((2 * c) ^ r8) << 4);
+                    uint8_t *to1 = dst + r8 * kAtom + (((2 * c + 1) ^ r8) << 4);
+                    auto put = [&](int b, const uint4 &v) {
+                        uint4 lo, hi;
+                        int8_to_f16(v.x, lo.x, lo.y);
+                        int8_to_f16(v.y, lo.z, lo.w);
+                        int8_to_f16(v.z, hi.x, hi.y);
+                        int8_to_f16(v.w, hi.z, hi.w);
+                        *reinterpret_cast<uint4 *>(to0 + b * 8 * kAtom) = lo;
+                        *reinterpret_cast<uint4 *>(to1 + b * 8 * kAtom) = hi;
+                    };
+                    auto get = [&](int b) {
+                        return *reinterpret_cast<const uint4 *>(from + b * 8 * kAtom);
+                    };
+                    int b = w;
+                    for (; b + (kBatch - 1) * kGroupWarps < blocks8; b += kBatch * kGroupWarps) {
+                        uint4 v[kBatch];  // loads first
 #pragma unroll
-                        for (int i = 0; i < kBatch; ++i)
+                        for (int i = 0; i < kBatch; ++i) v[i] = get(b + i * kGroupWarps);
 #pragma unroll
-                            for (int j = 0; j < 4 / kGroupWarps; ++j) {
-                                const int row = min(row0 + 32 * i, half - 1);
-                                v[i][j] = *reinterpret_cast<const uint4 *>(
-                                    src + row * kAtom +
-                                    (((4 * hh + w + j * kGroupWarps) ^ (row & 7)) << 4));
-                            }
-#pragma unroll
-                        for (int i = 0; i < kBatch; ++i)
-#pragma unroll
-                            for (int j = 0; j < 4 / kGroupWarps; ++j) {
-                                const int row = row0 + 32 * i, c = w + j * kGroupWarps;
-                                uint4 a, b;
-                                int8_to_f16(v[i][j].x, a.x, a.y);
-                                int8_to_f16(v[i][j].y, a.z, a.w);
-                                int8_to_f16(v[i][j].z, b.x, b.y);
-                                int8_to_f16(v[i][j].w, b.z, b.w);
-                                uint8_t *to = dst + row * kAtom;
-                                if (row < half) {
-                                    *reinterpret_cast<uint4 *>(to + (((2 * c) ^ (row & 7)) << 4)) = a;
-                                    *reinterpret_cast<uint4 *>(to + (((2 * c + 1) ^ (row & 7)) << 4)) = b;
-                                }
-                            }
+                        for (int i = 0; i < kBatch; ++i) put(b + i * kGroupWarps, v[i]);
                     }
+                    for (; b < blocks8; b += kGroupWarps) put(b, get(b));
                     ptx::fence_proxy_async_smem();  // read next by the tensor cores
                     __syncwarp();
                     if (lane == 0) {
