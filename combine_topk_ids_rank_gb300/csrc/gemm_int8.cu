@@ -552,8 +552,21 @@ int gemm_int8_nmax(int M) {
 cudaError_t launch_gemm_int8(GemmInt8Params p, int num_sms, cudaStream_t st) {
     if (p.G < 1 || p.G > kGemmInt8MaxGroups || p.M < 1 || p.N < 1 || p.H < 16 || p.H % 16 != 0)
         return cudaErrorInvalidValue;
+    int grid = num_sms < kStreamMaxCtas ? num_sms : kStreamMaxCtas;
+    grid -= grid % 2;
+    if (grid < 2) return cudaErrorInvalidValue;
     Ring ring;
-    p.nmax = ring.nmax = gemm_int8_nmax(p.M);
+    ring.nmax = gemm_int8_nmax(p.M);
+    if (p.G == 1 && p.counts == nullptr) {
+        // Narrower tiles while they still find an idle pair each: a narrow unit takes
+        // 650 cycles and its tile's reading little, a 256-column one 1024 and 5000
+        // (333 x 1000 x 1040: 11.3 us on 8 pairs, 9.3 us on 44).
+        const long long rt = (p.N + kPairRows - 1) / kPairRows;
+        while (ring.nmax > 32 &&
+               (p.M + ring.nmax / 2 - 1) / (ring.nmax / 2) * rt <= grid / 2)
+            ring.nmax /= 2;
+    }
+    p.nmax = ring.nmax;
     ring.box = ring.nmax / 2 < 32 ? ring.nmax / 2 : 32;
     const int half = ring.nmax / 2 * kAtom, raw = kWeightBytes + half;
     ring.units = ring.nmax > 128 ? 3 : kMaxUnits;
@@ -572,9 +585,6 @@ cudaError_t launch_gemm_int8(GemmInt8Params p, int num_sms, cudaStream_t st) {
     static std::atomic<unsigned long long> raised{0};
     cudaError_t err = raise_smem_limit_once(gemm_int8_kernel, kMaxDynamic, raised);
     if (err != cudaSuccess) return err;
-    int grid = num_sms < kStreamMaxCtas ? num_sms : kStreamMaxCtas;
-    grid -= grid % 2;
-    if (grid < 2) return cudaErrorInvalidValue;
     return launch_pdl(gemm_int8_kernel, dim3(grid), dim3(kThreads), smem, st, mx, mw, p, ring);
 }
 
