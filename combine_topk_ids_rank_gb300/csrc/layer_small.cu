@@ -27,7 +27,8 @@
 //   warps 0-3: epilogue (tensor-memory lane quadrants);
 //   warp 4: weight producer (TMA, 128-byte swizzle);
 //   warp 5: tensor-memory owner and MMA issuer;
-//   warps 6-7: token rows into the stages (16-byte cp.async, swizzled alike);
+//   warps 6-7: token rows into the stages, unit by unit in turn (16-byte
+//     cp.async, swizzled alike);
 //   warps 8-15, 8-bit formats: two groups of four in turn widen a stage's
 //     weight rows to bf16 into tensor memory (exact), which the products read
 //     as their A operand.
@@ -49,8 +50,13 @@ using namespace stream;
 
 constexpr int kEpiThreads = 128;
 constexpr int kCols = 8;        // token columns an epilogue step takes
-constexpr int kProducerWarp = 4, kMmaWarp = 5, kLoaderWarp0 = 6, kConvertWarp0 = 8;
-constexpr int kLoaderThreads = 64;
+constexpr int kProducerWarp = 4, kMmaWarp = 5, kLoaderWarp0 = 6;
+// Loader warps that take the units in turn.  No more than a ring has stages: a warp
+// knows of its last unit that all before the ring's length are free, and a wait by
+// parity may be at most one phase ahead of that.
+constexpr int kLoaders = 2, kMinStages = 2;
+static_assert(kLoaders <= kMinStages, "parity waits would run ahead");
+constexpr int kConvertWarp0 = (kLoaderWarp0 + kLoaders + 3) / 4 * 4;  // warp mod 4: lane quadrant
 constexpr int kHalfRows = 64;   // gate rows (and up rows) of a W13 tile
 constexpr int kQuarter = 16;    // of them in a warp's 32 lanes: 16 gate rows, then 16 up rows
 constexpr int kSlots = 4;       // widened weight tiles in tensor memory
@@ -91,7 +97,7 @@ struct Lists {
 template <int FORMAT>
 struct Shape {
     static constexpr bool kWiden = FORMAT != MOE_FORMAT_BF16;
-    static constexpr int kThreads = (kWiden ? 16 : 8) * 32;
+    static constexpr int kThreads = (kWiden ? kConvertWarp0 + 8 : kLoaderWarp0 + kLoaders) * 32;
     static constexpr int kA = kTileRows * kBlockK * (kWiden ? 1 : 2);  // weight bytes a stage
     static constexpr int kTmem = kWiden ? 512 : 256;                   // tensor-memory columns
 };
@@ -117,7 +123,7 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
     if (warp == kMmaWarp) tc::tmem_alloc(&s_taddr, S::kTmem);
     if (tid < kMaxStages) {
         ptx::mbar_init(&bar_a[tid], 1);
-        ptx::mbar_init(&bar_b[tid], kLoaderThreads);
+        ptx::mbar_init(&bar_b[tid], 32);
         ptx::mbar_init(&bar_free[tid], 1);
         if (tid < kSlots) {
             ptx::mbar_init(&wide_full[tid], 4);
@@ -384,12 +390,14 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
             tc::commit(&drained);  // before tensor memory is freed
             ptx::mbar_park(&drained, 0, kWaitNs);
         }
-    } else if (warp == kLoaderWarp0 || warp == kLoaderWarp0 + 1) {
-        // Thread l copies 16-byte piece l % 16 (8 values) of the rows l / 16,
-        // l / 16 + 4, ... of a unit: half (piece / 8), chunk piece % 8 stored at
-        // chunk ^ (row mod 8), the swizzle that TMA would apply.
-        const int l = tid - kLoaderWarp0 * 32, piece = l & 15, row0 = l >> 4;
+    } else if (warp >= kLoaderWarp0 && warp < kLoaderWarp0 + kLoaders) {
+        // The warps take the units in turn.  Lane l copies 16-byte piece l % 16 (8
+        // values) of the rows l / 16, l / 16 + 2, ... of a unit: half (piece / 8),
+        // chunk piece % 8 stored at chunk ^ (row mod 8), the swizzle that TMA would
+        // apply.
+        const int piece = lane & 15, row0 = lane >> 4;
         Turn st(stages);
+        uint32_t n = (uint32_t)(kLoaders - (warp - kLoaderWarp0));
         for (int phase = 0; phase < 2; ++phase) {
             const int width = phase ? p.I : p.H;
             Segments segs(cuts[phase], cta, phase ? blocks1 : blocks0);
@@ -406,7 +414,8 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
                 const int base = L.base[a], rows = L.base[a + 1] - base;
                 const int second = (rows + 7) / 8 * 8 * kAtom;  // where the second term's rows begin
                 const uint16_t *src = phase ? p.act + (size_t)base * 2 * p.I : p.x;
-                for (int kb = sg.k0; kb < sg.k1; ++kb, st.next()) {
+                for (int kb = sg.k0; kb < sg.k1; ++kb, st.next(), ++n) {
+                    if (n % kLoaders != 0) continue;
                     const int s = (int)st.at;
                     if (!__all_sync(0xffffffffu, ptx::mbar_park(
                                                      &bar_free[s], st.parity ^ 1u, kWaitNs))) {
@@ -415,7 +424,7 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
                     }
                     uint8_t *dst = stage_b(s) + (piece >> 3) * b_half;
                     const int col = kb * kBlockK + piece * 8;
-                    for (int row = row0; row < rows; row += 4) {
+                    for (int row = row0; row < rows; row += 2) {
                         const size_t at = (size_t)(phase ? 2 * row : L.token[base + row]) * width;
                         uint8_t *to = dst + row * kAtom + (((piece & 7) ^ (row & 7)) << 4);
                         if (col < width) {
@@ -668,6 +677,8 @@ cudaError_t launch_t(LayerSmallParams &p, int num_sms, cudaStream_t st) {
     // 1 KB aligns the ring and 1 KB stands behind it (reads of 16 rows where there are 8)
     const int front = Lists::bytes(p.E, p.T * p.K) + 2048;
     p.ring_bytes = (int)kMaxDynamic - front;
+    const int most = (p.T + 7) / 8 * 8;  // token rows of an expert
+    if (p.ring_bytes < kMinStages * (S::kA + 4 * most * kAtom)) return cudaErrorInvalidValue;
     const size_t smem = (size_t)front + (size_t)p.ring_bytes;
     static std::atomic<unsigned long long> raised{0};
     cudaError_t err = raise_smem_limit_once(layer_small_kernel<FORMAT>, kMaxDynamic, raised);
