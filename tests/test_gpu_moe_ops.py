@@ -328,6 +328,23 @@ def test_gemm_all_codes_and_the_largest_sums(api):
     assert ((out - dot).abs() <= 2.0 ** -8 * dot.abs() + H * 2.0 ** -23 * mag).all()
 
 
+def test_gemm_sums_that_cancel(api):
+    # partial sums just below 2^24, results of a few units: exact, so nothing of
+    # the small parts was lost on the way
+    H = 2080
+    xq = torch.full((1, 40, H), 127, dtype=torch.int8, device=DEV)
+    wq = torch.full((1, 300, H), 127, dtype=torch.int8, device=DEV)
+    wq[:, :, H // 2:] = -127                            # 1040 * 127^2 = 2^24 - 3056
+    for n in range(300):
+        wq[0, n, 3 + n % 500] = 127 - n % 3             # off by 0, 127 and 254
+    for m in range(40):
+        xq[0, m, H - 1 - m] = 127 - m % 2               # off by 0 and -127 (times -1)
+    one = lambda n: torch.ones((1, n), device=DEV)
+    out = api.MoeGemmInt8(1, 40, 300, H, DEV).gemm(xq, one(40), wq, one(300))
+    ref = torch.bmm(xq.double(), wq.double().transpose(1, 2))
+    assert ref.abs().max() <= 256 and torch.equal(out.double(), ref)
+
+
 def test_gemm_nan_scales_stay_in_their_rows(api):
     xq, sx, wq, sw = gemm_case(1, 30, 200, 256, 6)
     sx[0, 7] = float("nan")
@@ -359,6 +376,53 @@ def test_gemm_fewer_rows_two_dims_streams_and_errors(api):
         h.gemm(*gemm_case(1, 129, 300, 320, 7))
     with pytest.raises(api.MoeA2AError):
         api.MoeGemmInt8(1, 0, 300, 320, DEV)
+
+
+# ---- past 2^31 elements ----------------------------------------------------------
+
+def test_gate_beyond_32_bits(api):
+    T, E = 2200000, 1000
+    l = torch.empty((T, E), dtype=torch.bfloat16, device=DEV)
+    l[:100].normal_(generator=gen(1))
+    l[100:-100].zero_()
+    l[-100:].normal_(generator=gen(2))
+    ids, w = api.topk_gate(l, 4)
+    for part in (slice(0, 100), slice(T - 100, T)):
+        rids, rw = gate_ref(l[part], 4, 0, True, 1.0)
+        assert np.array_equal(ids[part].cpu().numpy(), rids)
+    assert (ids[100:-100] == torch.arange(4, device=DEV)).all()
+
+
+def test_quantize_beyond_32_bits(api):
+    rows, H = 135000, 16384
+    x = torch.zeros((rows, H), dtype=torch.bfloat16, device=DEV)
+    x[-50:].normal_(generator=gen(3))
+    q, s = api.quantize_rows_int8(x)
+    rq, rs = quant_ref(x[-50:])
+    assert np.array_equal(q[-50:].cpu().numpy(), rq) and np.array_equal(s[-50:].cpu().numpy(), rs)
+    assert (s[:-50] == 1).all() and not q[:-50].any()
+
+
+def test_gemm_beyond_32_bits(api):
+    M, N, H = 300000, 8192, 64                          # 2.4 G outputs
+    xq, sx, wq, sw = gemm_case(1, M, N, H, 8)
+    out = api.MoeGemmInt8(1, M, N, H, DEV).gemm(xq, sx, wq, sw)
+    for part in (slice(0, 300), slice(M - 300, M)):
+        ref = gemm_ref(xq[:, part].contiguous(), sx[:, part], wq, sw)
+        assert torch.equal(bits(out[:, part].contiguous()), bits(ref))
+
+
+def test_layer_beyond_32_bits(api):
+    E, H, I = 64, 7168, 2400                            # W13: 2.2 G weights
+    w13 = torch.zeros((E, 2 * I, H), dtype=torch.bfloat16, device=DEV)
+    w2 = torch.zeros((E, H, I), dtype=torch.bfloat16, device=DEV)
+    for e in (0, E - 1):
+        w13[e].normal_(0, H ** -0.5, generator=gen(e))
+        w2[e].normal_(0, I ** -0.5, generator=gen(e + 1))
+    x = torch.randn((3, H), generator=gen(5), device=DEV).to(torch.bfloat16)
+    ids = torch.tensor([[0, E - 1], [E - 1, 5], [7, 0]], dtype=torch.int32, device=DEV)
+    w = torch.rand((3, 2), generator=gen(6), device=DEV)
+    check_layer(api, (x, ids, w, w13, None, w2, None), "bf16")
 
 
 # ---- whole layer ------------------------------------------------------------------------
