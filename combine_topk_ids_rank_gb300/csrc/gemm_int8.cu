@@ -55,6 +55,10 @@ constexpr int kSlotCols = kBlockK / 2;    // a widened weight tile
 constexpr int kMaxUnits = 4;
 constexpr int kWeightBytes = kTileRows * kBlockK;
 constexpr int kMaxStages = 12;
+// Each widening warp takes every second unit of the rings: no more than the rings
+// have places, since a wait by parity may be at most one phase ahead of what the
+// warp knows to be over.
+static_assert(kWeightGroups == 2 && kGroups == 4, "every second unit");
 constexpr int kRowGroup = 8;              // row tiles of a raster group
 constexpr int kStepCols = 16;             // token columns an epilogue step takes
 // dynamic shared memory: 227 KB a CTA less the static tables
@@ -176,7 +180,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (tid <= kMaxCols / 16) s_widths[tid] = 0;
     ptx::grid_dependency_wait();  // nothing of the caller's memory is touched before
-    ptx::launch_dependents();
     for (int g = tid; g < p.G; g += kThreads) {
         int c = p.M;
         if (p.counts != nullptr) c = min(max(__ldg(p.counts + g), 0), p.M);
@@ -537,6 +540,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc::fence_before_sync();
     ptx::cluster_sync();
     tc::fence_after_sync();
+    // the output may be an input that the next kernel reads before it waits for this
+    // one: the CTA's stores (all of them are before the barrier) are visible first
+    if (tid == 0) __threadfence();
     if (tid == 0 && s_failed) atomicOr(&p.header->flags, MOE_DEVICE_FLAG_WAIT_TIMEOUT);
     if (warp == kMmaWarp) tc::tmem_dealloc_pair(taddr, kTmemCols);
 }

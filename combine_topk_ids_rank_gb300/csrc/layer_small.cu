@@ -144,7 +144,6 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
         tc::prefetch_map(&map2);
     }
     for (int e = tid; e < p.E; e += S::kThreads) L.count[e] = 0;
-    ptx::launch_dependents();
 
     // ---- lists: experts in use, ascending, and the pairs of each, by token ----
     // Thread i takes (t, k) = (i >> kshift, i mod 2^kshift): a token's experts stand

@@ -25,6 +25,16 @@ bool sm_count(int *sms) {
            cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
 }
 
+// A launcher's result as a status; nothing is thrown through the C entries.
+template <typename Launch>
+int launched(Launch &&launch) {
+    try {
+        return launch() == cudaSuccess ? MOE_OK : cuda_failed();
+    } catch (...) {
+        return cuda_failed();
+    }
+}
+
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 size_t part_bytes(int nmax) {
@@ -77,9 +87,7 @@ int moe_topk_gate(const void *d_logits, int32_t bf16, int64_t tokens, int64_t ro
     p.sigmoid = scoring == MOE_SCORE_SIGMOID;
     p.renormalize = renormalize != 0;
     p.scale = scale;
-    return launch_topk_gate(p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
-               ? MOE_OK
-               : cuda_failed();
+    return launched([&] { return launch_topk_gate(p, sms, static_cast<cudaStream_t>(stream)); });
 }
 
 int moe_quantize_rows_int8(const void *d_x, int32_t bf16, int32_t groups, int32_t rows,
@@ -105,9 +113,7 @@ int moe_quantize_rows_int8(const void *d_x, int32_t bf16, int32_t groups, int32_
     p.rows = rows;
     p.H = hidden;
     p.bf16 = bf16 != 0;
-    return launch_quantize_rows_int8(p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
-               ? MOE_OK
-               : cuda_failed();
+    return launched([&] { return launch_quantize_rows_int8(p, sms, static_cast<cudaStream_t>(stream)); });
 }
 
 size_t moe_gemm_int8_scratch_bytes(int32_t rows) {
@@ -124,7 +130,7 @@ int moe_gemm_int8(const int8_t *d_xq, const float *d_x_scale, const int8_t *d_wq
         hidden % 16 != 0 || (int64_t)groups * rows > INT32_MAX || (int64_t)groups * N > INT32_MAX)
         return MOE_ERR_INVALID_ARG;
     if (groups == 0 || rows == 0) return MOE_OK;
-    // every (128-row, 16-token) tile in k-blocks of 128 has to be countable
+    // tiles are counted in 32 bits
     const int64_t tiles = (int64_t)groups * ((N + 127) / 128) *
                           ((rows + gemm_int8_nmax(rows) - 1) / gemm_int8_nmax(rows));
     if (tiles > INT32_MAX / 2) return MOE_ERR_INVALID_ARG;
@@ -150,9 +156,7 @@ int moe_gemm_int8(const int8_t *d_xq, const float *d_x_scale, const int8_t *d_wq
     p.N = N;
     p.H = hidden;
     p.nmax = 0;
-    return launch_gemm_int8(p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
-               ? MOE_OK
-               : cuda_failed();
+    return launched([&] { return launch_gemm_int8(p, sms, static_cast<cudaStream_t>(stream)); });
 }
 
 size_t moe_layer_small_scratch_bytes(int32_t tokens, int32_t top_k, int32_t hidden,
@@ -205,9 +209,7 @@ int moe_layer_small(const void *d_x, const int32_t *d_topk_ids, const float *d_t
     p.I = inter;
     p.format = format;
     p.nmax = p.ring_bytes = p.kshift = 0;
-    return launch_layer_small(p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
-               ? MOE_OK
-               : cuda_failed();
+    return launched([&] { return launch_layer_small(p, sms, static_cast<cudaStream_t>(stream)); });
 }
 
 int moe_scratch_init(void *d_scratch, size_t scratch_bytes, void *stream) {

@@ -112,7 +112,6 @@ template <int VPT, bool BF16>
 __global__ void __launch_bounds__(kMaxWarps * 32) quantize_int8_kernel(const QuantInt8Params p) {
     __shared__ uint32_t red[2][kMaxWarps];
     ptx::grid_dependency_wait();
-    ptx::launch_dependents();
     const int tid = threadIdx.x, nt = blockDim.x, H8 = p.H / 8;
     const long long total = (long long)p.groups * p.rows;
     // the first row from r on that is in use (the whole CTA alike)

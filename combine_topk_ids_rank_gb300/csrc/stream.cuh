@@ -134,20 +134,8 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
                  : "memory");
 }
 
-// Barrier 1 of the 128 epilogue threads; true where any of them says so.
+// Barrier 1 of the 128 epilogue threads.
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool epi_any(bool v) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"(v ? 1u : 0u)
-        : "memory");
-    return r != 0;
-}
 
 // A flag in shared memory, read alike by all lanes of a warp.
 __device__ __forceinline__ bool warp_flag(const volatile int *f) {

@@ -33,6 +33,11 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kThreads = 256;
 
+// The one-launch dispatches read ids and weights, their inputs, before they wait
+// for the kernels in front of them.  So this kernel does not let dependents
+// start early, and its stores are visible to the device before a CTA is gone.
+__device__ __forceinline__ void publish() { __threadfence(); }
+
 // Order-preserving key of a logit; 0 for NaN and -inf.
 __device__ __forceinline__ uint32_t key_of(float l) {
     const uint32_t u = __float_as_uint(__fadd_rn(l, 0.0f));  // -0 becomes +0: equal logits
@@ -133,7 +138,6 @@ __device__ __forceinline__ void sort_down(uint32_t (&k)[VPL]) {
 template <int VPL, bool BF16, bool VEC>
 __global__ void __launch_bounds__(kThreads) topk_gate_kernel(const TopkGateParams p) {
     ptx::grid_dependency_wait();
-    ptx::launch_dependents();
     const int lane = threadIdx.x & 31;
     const long long warps = (long long)gridDim.x * (kThreads / 32);
     for (long long t = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -218,6 +222,7 @@ __global__ void __launch_bounds__(kThreads) topk_gate_kernel(const TopkGateParam
             p.topk_w[t * p.K + lane] = s * p.scale;
         }
     }
+    publish();
 }
 
 // bf16 logits, at most 256 experts and top-8: kTokens tokens a warp, whose
@@ -228,7 +233,6 @@ template <int VPL, bool VEC>
 __global__ void __launch_bounds__(kThreads) topk_gate_bf16_kernel(const TopkGateParams p) {
     static_assert(VPL == 2 || VPL == 4 || VPL == 8, "values a lane");
     ptx::grid_dependency_wait();
-    ptx::launch_dependents();
     const int lane = threadIdx.x & 31, e0 = lane * VPL;
     const long long stride = (long long)gridDim.x * (kThreads / 32) * kTokens;
     // low halves of the keys, two a word: lower ids are larger
@@ -322,6 +326,7 @@ __global__ void __launch_bounds__(kThreads) topk_gate_bf16_kernel(const TopkGate
             p.topk_w[(t0 + q) * p.K + k] = s * p.scale;
         }
     }
+    publish();
 }
 
 template <int VPL>
