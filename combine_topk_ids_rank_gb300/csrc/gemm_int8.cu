@@ -26,6 +26,12 @@
 //     memory, half a k-block (64 codes) at a time;
 //   warp 20: producer (TMA, 128-byte swizzle);
 //   warp 21 of CTA 0: MMA issuer.
+// Bounds.  8192 tokens x 4096 x 7168: 253 us, 1900 TFLOP/s (8-bit codes at the
+// rate of a bf16 product), bound by the tensor cores.  One CTA a tile took 593
+// us: it widens each token row twice as often.  16 tokens x 7168 x 4096: 15 us
+// for 29 MB (4.4 us); bound by the widening of a unit (about 650 cycles) and
+// the joining of cut tiles.  32 groups of up to 1024 rows, 4096 x 2048: 155 us;
+// the products are 77 us of it, the reading of accumulators between them 17 %.
 #include "kernels.h"
 #include "ptx.cuh"
 #include "smem_limit.h"

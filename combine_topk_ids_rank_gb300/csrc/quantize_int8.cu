@@ -17,7 +17,10 @@
 // whose neighbours are one apart.
 //
 // Memory bound: each element is read once and its code written once.  One
-// CTA a row, the row in registers, 16 bytes a thread and load.
+// CTA a row, the row in registers, 16 bytes a thread and load, the next row's
+// loads in flight (without them 198 us).  32768 bf16 rows of 7168 take 108 us,
+// 6.5 TB/s; with two remainder steps and a quarter of the threads idle in the
+// last vector 127 us.
 #include "fp8.cuh"
 #include "kernels.h"
 #include "layer.h"

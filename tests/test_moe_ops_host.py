@@ -118,28 +118,36 @@ def test_scratch_entry_refusals(abi):
 
 def test_cut_covers_every_unit_once():
     # The even split of tiles x k-blocks over CTAs that the persistent products
-    # use, restated: ranges cover all units once, the owner of a unit is found
-    # from the unit alone, and every part of a tile has a slot of its own.
-    first = lambda c, total, parts: c * total // parts
-    for tiles, blocks, ctas in [(1, 1, 152), (1, 7, 152), (3, 5, 4), (152, 3, 152),
-                                (153, 56, 152), (700, 17, 152), (5, 1000, 152)]:
-        total = tiles * blocks
-        parts = min(total, ctas)
-        owner = []
-        for c in range(parts):
-            n = first(c + 1, total, parts) - first(c, total, parts)
-            assert n >= 1
-            owner += [c] * n
-        assert len(owner) == total
-        for u in range(total):
-            assert ((u + 1) * parts - 1) // total == owner[u]
+    # use (stream.cuh), restated: ranges cover all units once, the owner of a unit
+    # is found from the unit alone, and every part of a tile has a slot of its own.
+    # grain 1 cuts anywhere, grain = blocks between tiles only.
+    for tiles, blocks, ctas, whole in [(1, 1, 152, True), (1, 7, 152, True), (3, 5, 4, False),
+                                       (152, 3, 152, False), (153, 56, 152, False),
+                                       (700, 17, 152, False), (5, 1000, 152, False),
+                                       (160, 9, 152, True), (76, 4, 76, True),
+                                       (28, 32, 76, False)]:
+        grain = blocks if whole else 1
+        grains = tiles * blocks // grain
+        parts = min(tiles, ctas) if whole else ctas
+        q, more = divmod(grains, parts)
+        assert q >= 1
+        first = lambda c: (c * q + min(c, more)) * grain
+
+        def owner_of(u):
+            g, big = u // grain, more * (q + 1)
+            return g // (q + 1) if g < big else more + (g - big) // q
+
+        owner = [c for c in range(parts) for _ in range(first(c), first(c + 1))]
+        assert len(owner) == tiles * blocks == first(parts)
+        assert all(owner_of(u) == owner[u] for u in range(len(owner)))
         used = set()
         for t in range(tiles):
             own = sorted(set(owner[t * blocks:(t + 1) * blocks]))
             assert own == list(range(own[0], own[-1] + 1))
             if len(own) == 1:
                 continue
+            assert not whole
             for c in own:
-                slot = 0 if c != own[0] or first(c, total, parts) == t * blocks else 1
+                slot = 0 if c != own[0] or first(c) == t * blocks else 1
                 assert (c, slot) not in used
                 used.add((c, slot))
