@@ -33,8 +33,8 @@
 // the joining of cut tiles.  32 groups of up to 1024 rows, 4096 x 2048: 155 us;
 // the products are 77 us of it, the reading of accumulators between them 17 %.
 #include "kernels.h"
-#include "ptx.cuh"
-#include "smem_limit.h"
+#include "pair.cuh"
+#include "smem_limit_once.h"
 #include "stream.cuh"
 #include "tcgen05.cuh"
 #include "tensor_map.h"

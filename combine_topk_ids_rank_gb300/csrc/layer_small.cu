@@ -39,8 +39,8 @@
 // about 6 the way through the two phases (first weights, activations visible to
 // all CTAs, outputs visible to all).
 #include "kernels.h"
-#include "ptx.cuh"
-#include "smem_limit.h"
+#include "pair.cuh"
+#include "smem_limit_once.h"
 #include "stream.cuh"
 #include "tcgen05.cuh"
 #include "tensor_map.h"
