@@ -283,7 +283,7 @@ def test_gemm_exact(api, G, M, N, H):
 
 
 @pytest.mark.parametrize("G,M,N,H", [(6, 33, 136, 256), (32, 1024, 512, 512), (9, 300, 384, 784),
-                                     (64, 16, 256, 128)])
+                                     (64, 16, 256, 128), (1024, 3, 40, 48), (5, 600, 130, 6000)])
 def test_gemm_ragged_groups(api, G, M, N, H):
     xq, sx, wq, sw = gemm_case(G, M, N, H, 3)
     counts = torch.randint(0, M + 1, (G,), generator=gen(4), device=DEV).to(torch.int32)
@@ -520,6 +520,21 @@ def test_layer(api, fmt, T, E, H, I, K):
         again = h.forward(x, ids, w, w13, w2, s13, s2)
         assert torch.equal(bits(again), bits(out))
     assert h.get_error() == (0, 0)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("hot", [False, True])
+def test_layer_at_its_limits(api, fmt, hot):
+    # 64 tokens, 1024 experts, top-32: the longest lists, and (hot) every token on
+    # the same 32 experts, the fewest stages
+    x, ids, w, w13, s13, w2, s2 = layer_case(64, 1024, 64, 16, 32, fmt, 91)
+    if hot:
+        ids[:] = torch.arange(992, 1024, dtype=torch.int32, device=DEV)
+    check_layer(api, (x, ids, w, w13, s13, w2, s2), fmt)
+
+
+def test_layer_widest(api):
+    check_layer(api, layer_case(2, 2, 16384, 16384, 1, "int8", 92), "int8")
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
