@@ -16,14 +16,14 @@
 // experts a lane, 16-byte loads), the selection in integers.  K rounds of a
 // warp-wide maximum (redux.sync) over the lanes' heads; ties between lanes go
 // to the lowest lane, which holds the lowest ids.
-//   bf16 logits: key and id share one word (16 + 16 bits), so a lane sorts
-//     its values once (a network of 2-instruction exchanges) and a round only
-//     shifts the winner's list;
-//   fp32 logits: the key fills the word; the winner lane clears the first
-//     value equal to the maximum and looks for its next.
-// Bound by instruction issue (66 % of the slots busy): 32768 tokens x 256 bf16
-// logits, top-8, take 10.0 us (scalar loads and unsorted keys took 29 us, one
-// token a warp with sorted keys 17 us); their 18.9 MB would take 2.8 us.
+// At most 256 experts and top-8, the usual gate: key and id share one word, so a
+// lane sorts its values once (a network of 2-instruction exchanges) and a round
+// only shifts the winner's list.  Otherwise fp32 keys fill the word; the winner
+// lane clears the first value equal to the maximum and looks for its next.
+// Bound by instruction issue (66 % of the slots busy for bf16).  32768 tokens x
+// 256 logits, top-8: bf16 10.3 us (its 18.9 MB would take 2.8 us; scalar loads
+// and unsorted keys took 29 us, one token a warp 13.5 us), fp32 14.5 us (its
+// 35.7 MB would take 5.3 us; unsorted whole keys took 27.7 us).
 #include "kernels.h"
 #include "layer.h"
 #include "ptx.cuh"
@@ -34,7 +34,9 @@ namespace moe {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kThreads = 256;
+// Of a CTA; with 256 the waves are coarser: 9.7 us for 16384 x 256 fp32 logits,
+// 8.5 with 128.
+constexpr int kThreads = 128;
 
 // The one-launch dispatches read ids and weights, their inputs, before they wait
 // for the kernels in front of them.  So this kernel does not let dependents
@@ -138,6 +140,48 @@ __device__ __forceinline__ void sort_down(uint32_t (&k)[VPL]) {
     }
 }
 
+// The K largest of a warp's whole keys: lane at + k gets the k-th and its id.
+template <int VPL>
+__device__ __forceinline__ void select_whole(uint32_t (&key)[VPL], int K, int lane, int at,
+                                             uint32_t &sel_key, int &sel_id) {
+    for (int k = 0; k < K; ++k) {
+        uint32_t best = key[0];
+#pragma unroll
+        for (int j = 1; j < VPL; ++j) best = max(best, key[j]);
+        const uint32_t m = __reduce_max_sync(kFull, best);
+        if (m == 0) break;
+        const int src = __ffs(__ballot_sync(kFull, best == m)) - 1;
+        int first = 0;  // the first value equal to the maximum, in the winner lane
+#pragma unroll
+        for (int j = VPL - 1; j >= 0; --j) first = key[j] == m ? j : first;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j)
+            if (lane == src && first == j) key[j] = 0;
+        const int id = src * VPL + __shfl_sync(kFull, first, src);
+        if (lane == at + k) {
+            sel_key = m;
+            sel_id = id;
+        }
+    }
+}
+
+// N words, from an address that is a multiple of their size (16 bytes at most).
+template <int N>
+__device__ __forceinline__ void load_words(const void *from, uint32_t (&w)[N]) {
+    if constexpr (N >= 4) {
+#pragma unroll
+        for (int j = 0; j < N / 4; ++j) {
+            const uint4 v = __ldg(static_cast<const uint4 *>(from) + j);
+            w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
+        }
+    } else if constexpr (N == 2) {
+        const uint2 v = __ldg(static_cast<const uint2 *>(from));
+        w[0] = v.x, w[1] = v.y;
+    } else {
+        w[0] = __ldg(static_cast<const uint32_t *>(from));
+    }
+}
+
 template <int VPL, bool BF16, bool VEC>
 __global__ void __launch_bounds__(kThreads) topk_gate_kernel(const TopkGateParams p) {
     ptx::grid_dependency_wait();
@@ -169,15 +213,15 @@ __global__ void __launch_bounds__(kThreads) topk_gate_kernel(const TopkGateParam
         int sel_id = -1;
         constexpr bool kSorted = BF16 && VPL <= 8;
         if constexpr (kSorted) sort_down<VPL>(key);
-        for (int k = 0; k < p.K; ++k) {
-            uint32_t best = key[0];
-            if constexpr (!kSorted) {
+        if constexpr (BF16) {  // keys are unique
+            for (int k = 0; k < p.K; ++k) {
+                uint32_t best = key[0];
+                if constexpr (!kSorted) {
 #pragma unroll
-                for (int j = 1; j < VPL; ++j) best = max(best, key[j]);
-            }
-            const uint32_t m = __reduce_max_sync(kFull, best);
-            if (m == 0) break;
-            if constexpr (BF16) {  // keys are unique
+                    for (int j = 1; j < VPL; ++j) best = max(best, key[j]);
+                }
+                const uint32_t m = __reduce_max_sync(kFull, best);
+                if (m == 0) break;
                 if constexpr (kSorted) {
                     if (best == m) {
 #pragma unroll
@@ -192,20 +236,9 @@ __global__ void __launch_bounds__(kThreads) topk_gate_kernel(const TopkGateParam
                     sel_key = m | 0xffffu;
                     sel_id = (int)(0xffffu - (m & 0xffffu));
                 }
-            } else {
-                const int src = __ffs(__ballot_sync(kFull, best == m)) - 1;
-                int at = 0;  // the first value equal to the maximum, in the winner lane
-#pragma unroll
-                for (int j = VPL - 1; j >= 0; --j) at = key[j] == m ? j : at;
-#pragma unroll
-                for (int j = 0; j < VPL; ++j)
-                    if (lane == src && at == j) key[j] = 0;
-                const int id = src * VPL + __shfl_sync(kFull, at, src);
-                if (lane == k) {
-                    sel_key = m;
-                    sel_id = id;
-                }
             }
+        } else {
+            select_whole<VPL>(key, p.K, lane, 0, sel_key, sel_id);
         }
         // (a bf16 key's low half is the sign's: 0 under a positive key, all ones
         // under the complement of a negative one)
@@ -228,95 +261,168 @@ __global__ void __launch_bounds__(kThreads) topk_gate_kernel(const TopkGateParam
     publish();
 }
 
-// bf16 logits, at most 256 experts and top-8: kTokens tokens a warp, whose
-// selections (eight lanes a token) are weighted together.  About 160
-// instructions a token, which is the bound beside 540 bytes of traffic.
+// At most 256 experts and top-8: NT tokens a warp, whose selections (eight lanes
+// a token) are weighted together.  Keys and ids share a word: 16 + 16 bits for
+// bf16; for fp32 the key's upper 24 bits and the id, which may put logits that
+// agree to 2^-15 in the wrong order.  So the selected logits are read again
+// (their weights need them) and compared; a token that has two of them in the
+// wrong order, or the last of them no further than 2^-15 from the next one, is
+// selected anew on whole keys.  About 160 instructions a bf16 token, which is the
+// bound beside 540 bytes of traffic.
 constexpr int kTokens = 4;
-template <int VPL, bool VEC>
-__global__ void __launch_bounds__(kThreads) topk_gate_bf16_kernel(const TopkGateParams p) {
+// Tokens an SM, up to which a warp takes one: 8 tokens of 256 fp32 logits take
+// 2.3 us with one a warp and 3.4 us with four, 2048 3.2 and 4.7 us, 4864 (32 an
+// SM) 4.2 and 4.8 us, 9728 7.1 and 6.2 us; bf16 2.0 and 2.8, 2.5 and 3.4, 3.3
+// and 3.4, 5.7 and 4.3 us.
+constexpr long long kSpread = 32;
+template <int VPL, bool BF16, int NT, bool VEC>
+__global__ void __launch_bounds__(kThreads) topk_gate_packed_kernel(const TopkGateParams p) {
     static_assert(VPL == 2 || VPL == 4 || VPL == 8, "values a lane");
+    constexpr int kWords = BF16 ? VPL / 2 : VPL;       // of a lane's part of a row
+    constexpr uint32_t kIdMask = BF16 ? 0xffffu : 0xffu;  // id bits of a packed key
+    constexpr int kLooks = BF16 ? 8 : 9;               // rounds that look at the heads
     ptx::grid_dependency_wait();
     const int lane = threadIdx.x & 31, e0 = lane * VPL;
-    const long long stride = (long long)gridDim.x * (kThreads / 32) * kTokens;
-    // low halves of the keys, two a word: lower ids are larger
-    uint32_t tag[VPL / 2];
+    const long long stride = (long long)gridDim.x * (kThreads / 32) * NT;
+    // low halves of the bf16 keys, two a word: lower ids are larger
+    uint32_t tag[(VPL + 1) / 2];
 #pragma unroll
     for (int j = 0; j < VPL / 2; ++j)
         tag[j] = (uint32_t)(0xffff - e0 - 2 * j) | ((uint32_t)(0xffff - e0 - 2 * j - 1) << 16);
-    for (long long t0 = ((long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kTokens;
+    for (long long t0 = ((long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * NT;
          t0 < p.tokens; t0 += stride) {
-        uint32_t w[kTokens][VPL / 2];
+        uint32_t w[NT][kWords];
 #pragma unroll
-        for (int q = 0; q < kTokens; ++q) {
+        for (int q = 0; q < NT; ++q) {
             const long long t = t0 + q < p.tokens ? t0 + q : p.tokens - 1;
-            const uint16_t *row = static_cast<const uint16_t *>(p.logits) + t * p.row_stride + e0;
-            if (VEC && e0 + VPL <= p.E) {
-                if constexpr (VPL == 8) {
-                    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row));
-                    w[q][0] = v.x, w[q][1] = v.y, w[q][2] = v.z, w[q][3] = v.w;
-                } else if constexpr (VPL == 4) {
-                    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(row));
-                    w[q][0] = v.x, w[q][1] = v.y;
+            if constexpr (BF16) {
+                const uint16_t *row =
+                    static_cast<const uint16_t *>(p.logits) + t * p.row_stride + e0;
+                if (VEC && e0 + VPL <= p.E) {
+                    load_words<kWords>(row, w[q]);
                 } else {
-                    w[q][0] = __ldg(reinterpret_cast<const uint32_t *>(row));
+#pragma unroll
+                    for (int j = 0; j < VPL / 2; ++j) {
+                        const uint32_t lo = e0 + 2 * j < p.E ? row[2 * j] : 0xff80u;  // -inf past E
+                        const uint32_t hi = e0 + 2 * j + 1 < p.E ? row[2 * j + 1] : 0xff80u;
+                        w[q][j] = lo | hi << 16;
+                    }
                 }
             } else {
+                const uint32_t *row =
+                    static_cast<const uint32_t *>(p.logits) + t * p.row_stride + e0;
+                if (VEC && e0 + VPL <= p.E) {
+                    load_words<kWords>(row, w[q]);
+                } else {
 #pragma unroll
-                for (int j = 0; j < VPL / 2; ++j) {
-                    const uint32_t lo = e0 + 2 * j < p.E ? row[2 * j] : 0xff80u;  // -inf past E
-                    const uint32_t hi = e0 + 2 * j + 1 < p.E ? row[2 * j + 1] : 0xff80u;
-                    w[q][j] = lo | hi << 16;
+                    for (int j = 0; j < VPL; ++j) w[q][j] = e0 + j < p.E ? row[j] : 0xff800000u;
                 }
             }
         }
         uint32_t sel = 0;  // lane 8 q + k: selection k of token q (0: none)
+        bool unsure = false;
         float total = 0.0f;
 #pragma unroll
-        for (int q = 0; q < kTokens; ++q) {
+        for (int q = 0; q < NT; ++q) {
             uint32_t key[VPL];
             float sum = 0.0f;
+            const bool whole_row = !p.sigmoid && !p.renormalize;  // softmax over it
+            if constexpr (BF16) {
 #pragma unroll
-            for (int j = 0; j < VPL / 2; ++j) {
-                // order-preserving 16-bit keys of both halves; 0 for NaN and -inf
-                __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162 *>(&w[q][j]);
-                const uint32_t open = __hgt2_mask(x, __float2bfloat162_rn(-INFINITY));
-                x = __hadd2(x, __float2bfloat162_rn(0.0f));  // -0 becomes +0: equal logits
-                const uint32_t u = *reinterpret_cast<const uint32_t *>(&x);
-                uint32_t sign;  // all ones over a negative half (prmt's sign mode)
-                asm("prmt.b32 %0, %1, 0, 0xbb99;" : "=r"(sign) : "r"(u));
-                const uint32_t k = (u ^ (sign | 0x80008000u)) & open;
-                key[2 * j] = __byte_perm(k, tag[j], 0x1054);
-                key[2 * j + 1] = __byte_perm(k, tag[j], 0x3276);
-            }
-            if (!p.sigmoid && !p.renormalize) {  // softmax over the whole row
-                uint32_t m = 0;
+                for (int j = 0; j < VPL / 2; ++j) {
+                    // order-preserving 16-bit keys of both halves; 0 for NaN and -inf
+                    __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162 *>(&w[q][j]);
+                    const uint32_t open = __hgt2_mask(x, __float2bfloat162_rn(-INFINITY));
+                    x = __hadd2(x, __float2bfloat162_rn(0.0f));  // -0 becomes +0: equal logits
+                    const uint32_t u = *reinterpret_cast<const uint32_t *>(&x);
+                    uint32_t sign;  // all ones over a negative half (prmt's sign mode)
+                    asm("prmt.b32 %0, %1, 0, 0xbb99;" : "=r"(sign) : "r"(u));
+                    const uint32_t k = (u ^ (sign | 0x80008000u)) & open;
+                    key[2 * j] = __byte_perm(k, tag[j], 0x1054);
+                    key[2 * j + 1] = __byte_perm(k, tag[j], 0x3276);
+                }
+                if (whole_row) {
+                    uint32_t m = 0;
 #pragma unroll
-                for (int j = 0; j < VPL; ++j) m = max(m, key[j]);
-                const float top = value_of(__reduce_max_sync(kFull, m));
+                    for (int j = 0; j < VPL; ++j) m = max(m, key[j]);
+                    const float top = value_of(__reduce_max_sync(kFull, m));
+#pragma unroll
+                    for (int j = 0; j < VPL; ++j)
+                        if (key[j] > kIdMask) sum += exp_from(value_of(key[j]), top);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) key[j] = key_of(__uint_as_float(w[q][j]));
+                if (whole_row) {
+                    uint32_t m = 0;
+#pragma unroll
+                    for (int j = 0; j < VPL; ++j) m = max(m, key[j]);
+                    const float top = logit_of(__reduce_max_sync(kFull, m));
+#pragma unroll
+                    for (int j = 0; j < VPL; ++j)
+                        if (key[j] != 0) sum += exp_from(__uint_as_float(w[q][j]), top);
+                }
+                // (an open expert's key is 0x00800000 at least; a closed one's
+                // packed key is its id bits alone)
 #pragma unroll
                 for (int j = 0; j < VPL; ++j)
-                    if (key[j] > 0xffffu) sum += exp_from(value_of(key[j]), top);
+                    key[j] = (key[j] & ~kIdMask) | (kIdMask - (uint32_t)(e0 + j));
+            }
+            if (whole_row) {
                 for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
                 if (lane >> 3 == q) total = sum;
             }
             sort_down<VPL>(key);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                if (k >= p.K) break;
+            for (int k = 0; k < kLooks; ++k) {
+                if (k > p.K || (BF16 && k == p.K)) break;
                 const uint32_t m = __reduce_max_sync(kFull, key[0]);
+                if (k == p.K) {  // the one that comes after the selected ones
+                    if (lane == 8 * q + k - 1) unsure = m > kIdMask && (m ^ sel) <= kIdMask;
+                    break;
+                }
                 if (key[0] == m) {
-                    // (what is further down than the rounds left is not looked at)
+                    // (what is further down than the looks left is not looked at)
 #pragma unroll
                     for (int j = 0; j < VPL - 1; ++j)
-                        if (j < 7 - k) key[j] = key[j + 1];
-                    if (VPL - 1 < 8 - k) key[VPL - 1] = 0;
+                        if (j < kLooks - 1 - k) key[j] = key[j + 1];
+                    if (VPL - 1 < kLooks - k) key[VPL - 1] = 0;
                 }
                 if (lane == 8 * q + k) sel = m;
             }
         }
         const int q = lane >> 3, k = lane & 7;
-        const bool some = sel > 0xffffu;
-        const float v = value_of(sel), top = __shfl_sync(kFull, v, lane & 24);
+        bool some = sel > kIdMask;
+        int id = some ? (int)(kIdMask - (sel & kIdMask)) : -1;
+        float v;
+        if constexpr (BF16) {
+            v = value_of(sel);
+        } else {
+            const long long t = t0 + q < p.tokens ? t0 + q : p.tokens - 1;
+            v = some ? static_cast<const float *>(p.logits)[t * p.row_stride + id] : 0.0f;
+            const float after = __shfl_down_sync(kFull, v, 1);
+            const uint32_t sel_after = __shfl_down_sync(kFull, sel, 1);
+            if (k + 1 < p.K && sel_after > kIdMask && v < after) unsure = true;
+            const unsigned again = __ballot_sync(kFull, unsure);
+            if (again != 0) {
+                for (int r = 0; r < NT; ++r) {
+                    if ((again >> (8 * r) & 0xffu) == 0) continue;
+                    float l[VPL];
+                    uint32_t key[VPL], whole = 0;
+                    const long long tr = t0 + r < p.tokens ? t0 + r : p.tokens - 1;
+                    load_row<VPL, false, VEC>(p, tr, lane, l);
+#pragma unroll
+                    for (int j = 0; j < VPL; ++j) key[j] = key_of(l[j]);
+                    int found = -1;
+                    select_whole<VPL>(key, p.K, lane, 8 * r, whole, found);
+                    if (q == r && found >= 0) {  // (as many as there were)
+                        id = found;
+                        v = logit_of(whole);
+                    }
+                }
+            }
+        }
+        const float top = __shfl_sync(kFull, v, lane & 24);
         float s = 0.0f;
         if (some) s = p.sigmoid ? 1.0f / (1.0f + expf(-v)) : exp_from(v, top);
         if (p.renormalize) {
@@ -324,31 +430,38 @@ __global__ void __launch_bounds__(kThreads) topk_gate_bf16_kernel(const TopkGate
             for (int o = 4; o > 0; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
         }
         if ((p.renormalize || !p.sigmoid) && s != 0.0f) s = s / total;
-        if (k < p.K && t0 + q < p.tokens) {
-            p.topk_ids[(t0 + q) * p.K + k] = some ? (int)(0xffffu - (sel & 0xffffu)) : -1;
+        if (q < NT && k < p.K && t0 + q < p.tokens) {
+            p.topk_ids[(t0 + q) * p.K + k] = id;
             p.topk_w[(t0 + q) * p.K + k] = s * p.scale;
         }
     }
     publish();
 }
 
+template <int VPL, bool BF16>
+cudaError_t launch_packed(const TopkGateParams &p, bool aligned, int num_sms, cudaStream_t st) {
+    const int per = p.tokens > kSpread * num_sms ? kTokens : 1;  // tokens a warp
+    const long long want = (p.tokens + per * (kThreads / 32) - 1) / (per * (kThreads / 32));
+    const dim3 grid((unsigned)(want < num_sms * 16LL ? want : num_sms * 16LL));
+    auto kern = per == 1 ? (aligned ? topk_gate_packed_kernel<VPL, BF16, 1, true>
+                                    : topk_gate_packed_kernel<VPL, BF16, 1, false>)
+                         : (aligned ? topk_gate_packed_kernel<VPL, BF16, kTokens, true>
+                                    : topk_gate_packed_kernel<VPL, BF16, kTokens, false>);
+    return launch_pdl(kern, grid, dim3(kThreads), 0, st, p);
+}
+
 template <int VPL>
 cudaError_t launch_t(const TopkGateParams &p, int num_sms, cudaStream_t st) {
     const long long want = (p.tokens + kThreads / 32 - 1) / (kThreads / 32);
-    const int grid = (int)(want < num_sms * 8LL ? want : num_sms * 8LL);
+    const int grid = (int)(want < num_sms * 16LL ? want : num_sms * 16LL);
     // whole vectors a lane, where every row starts on one
     const uintptr_t vec = VPL * (p.bf16 ? 2 : 4) < 16 ? VPL * (p.bf16 ? 2 : 4) : 16;
     const bool aligned = reinterpret_cast<uintptr_t>(p.logits) % vec == 0 &&
                          (uintptr_t)(p.row_stride * (p.bf16 ? 2 : 4)) % vec == 0;
     if constexpr (VPL <= 8) {
-        if (p.bf16 && p.K <= 8) {
-            const long long fw = (p.tokens + kTokens - 1) / kTokens;
-            const long long fc = (fw + kThreads / 32 - 1) / (kThreads / 32);
-            const int fast = (int)(fc < num_sms * 8LL ? fc : num_sms * 8LL);
-            return launch_pdl(aligned ? topk_gate_bf16_kernel<VPL, true>
-                                      : topk_gate_bf16_kernel<VPL, false>,
-                              dim3(fast), dim3(kThreads), 0, st, p);
-        }
+        if (p.K <= 8)
+            return p.bf16 ? launch_packed<VPL, true>(p, aligned, num_sms, st)
+                          : launch_packed<VPL, false>(p, aligned, num_sms, st);
     }
     auto kern = p.bf16 ? (aligned ? topk_gate_kernel<VPL, true, true>
                                   : topk_gate_kernel<VPL, true, false>)

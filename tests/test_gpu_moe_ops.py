@@ -84,6 +84,32 @@ def test_gate(api, T, E, K, sigmoid):
         check_gate(api, l.to(torch.bfloat16), K, sigmoid, renorm)  # many equal logits
 
 
+@pytest.mark.parametrize("T,E,K", [(5001, 256, 8), (6003, 100, 5), (4999, 33, 3), (20005, 20, 8)])
+@pytest.mark.parametrize("sigmoid", [0, 1])
+def test_gate_many_tokens(api, T, E, K, sigmoid):
+    l = torch.randn((T, E), generator=gen(T), device=DEV)
+    l[::7, 2:] = -float("inf")                          # fewer open than K
+    l[3::11] = -float("inf")
+    check_gate(api, l, K, sigmoid, not sigmoid)
+    check_gate(api, l.to(torch.bfloat16), K, sigmoid, bool(sigmoid))
+
+
+@pytest.mark.parametrize("T", [24, 5003])
+@pytest.mark.parametrize("E,K", [(256, 8), (200, 1), (128, 7), (64, 3), (12, 8)])
+def test_gate_logits_that_differ_in_their_last_bits(api, T, E, K):
+    g = gen(T + E + K)
+    l = torch.randn((T, E), generator=g, device=DEV)
+    last = torch.randint(0, 64, (T, E), generator=g, device=DEV).float() * 2.0 ** -23
+    l[0::6] = 1.5 + last[0::6]                          # all of them
+    l[1::6] = -(1.5 + last[1::6])
+    l[2::6] = torch.where(last[2::6] < 2.0 ** -19, 3.5 + last[2::6], l[2::6])  # some
+    l[3::6, E // 2] = l[3::6].max(-1).values            # two at the top, equal
+    l[4::6, E // 3] = torch.nextafter(l[4::6].max(-1).values, torch.tensor(9.0, device=DEV))
+    # (and a sixth of the rows as they are)
+    check_gate(api, l, K)
+    check_gate(api, l, K, 1, False)
+
+
 def test_gate_ties_take_the_lowest_id(api):
     l = torch.zeros((4, 200), device=DEV)
     l[1, 150:] = 1.0
