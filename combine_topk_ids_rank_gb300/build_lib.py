@@ -21,7 +21,7 @@ SOURCES = ["route.cu", "dispatch.cu", "combine.cu", "combine_ring.cu", "combine_
            "expert_gemm.cu", "expert_rank.cu", "topk_gate.cu", "quantize_int8.cu", "gemm_int8.cu",
            "layer_small.cu", "moe_a2a.cpp", "moe_ops.cpp", "moe_noalloc.cu"]
 HEADERS = ["kernels.h", "expert.h", "layer.h", "stream.cuh", "tensor_map.h",
-           "pair.cuh", "smem_limit_once.h", "dispatch_small.h", "smem_limit.h", "ptx.cuh", "fp8.cuh",
+           "pair.cuh", "ring.h", "smem_limit_once.h", "dispatch_small.h", "smem_limit.h", "ptx.cuh", "fp8.cuh",
            "tcgen05.cuh", "f32x2.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -34,6 +34,7 @@
 // the products are 77 us of it, the reading of accumulators between them 17 %.
 #include "kernels.h"
 #include "pair.cuh"
+#include "ring.h"
 #include "smem_limit_once.h"
 #include "stream.cuh"
 #include "tcgen05.cuh"
@@ -58,25 +59,15 @@ constexpr int kPairRows = 2 * kTileRows;  // channels of a tile
 constexpr int kMaxCols = 256;             // tokens of a tile
 constexpr int kTmemCols = 512;            // accumulators, then widened weights
 constexpr int kSlotCols = kBlockK / 2;    // a widened weight tile
-constexpr int kMaxUnits = 4;
-constexpr int kWeightBytes = kTileRows * kBlockK;
-constexpr int kMaxStages = 12;
-// Each widening warp takes every second unit of the rings: no more than the rings
-// have places, since a wait by parity may be at most one phase ahead of what the
-// warp knows to be over.
-static_assert(kWeightGroups == 2 && kGroups == 4, "every second unit");
+constexpr int kMaxUnits = ring::kGemmMaxUnits;
+constexpr int kWeightBytes = ring::kGemmWeightBytes;
+constexpr int kMaxStages = ring::kGemmMaxStages;
+static_assert(kWeightBytes == kTileRows * kBlockK && kAtom == ring::kGemmRowBytes, "a unit");
+// Each widening warp takes every second unit (two groups of the halves a unit).
+static_assert(kWeightGroups == ring::kTurns && kGroups == 2 * ring::kTurns, "every second unit");
 constexpr int kRowGroup = 8;              // row tiles of a raster group
 constexpr int kStepCols = 16;             // token columns an epilogue step takes
-// dynamic shared memory: 227 KB a CTA less the static tables
-constexpr size_t kMaxDynamic = (227 - 15) * 1024;
-
-struct Ring {
-    int nmax;      // tokens of a tile, at most
-    int box;       // rows of a token TMA box
-    int stages;    // raw stages: 128 weight rows + nmax / 2 token rows of 128 codes
-    int units;     // widened units: a weight tile in tensor memory, and nmax / 2 token
-                   // rows of 128 f16, as two tiles of 64, in shared memory
-};
+constexpr size_t kMaxDynamic = ring::kGemmDynamic;
 
 // The tiles of a call: groups in turn, those with the widest tiles first; in a
 // group, blocks of kRowGroup row tiles, token tile outer and row tile inner.
@@ -140,7 +131,7 @@ struct Work {
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_int8_kernel(const __grid_constant__ CUtensorMap map_x,
                      const __grid_constant__ CUtensorMap map_w, const GemmInt8Params p,
-                     const Ring ring) {
+                     const ring::Gemm rings) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t raw_full[kMaxStages], raw_free[kMaxStages];
     // (full: CTA 0's, both CTAs arrive; free: either CTA's own)
@@ -157,8 +148,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     const uint32_t base = ptx::smem_u32(smem_raw);
     uint8_t *smem = smem_raw + ((1024u - (base & 1023u)) & 1023u);
-    const int half_bytes = ring.nmax / 2 * kAtom, raw_bytes = kWeightBytes + half_bytes;
-    uint8_t *wide = smem + ring.stages * raw_bytes;  // raw_bytes: a multiple of 1024
+    const int half_bytes = rings.nmax / 2 * kAtom, raw_bytes = kWeightBytes + half_bytes;
+    uint8_t *wide = smem + rings.stages * raw_bytes;  // raw_bytes: a multiple of 1024
     auto raw_w = [&](int s) { return smem + s * raw_bytes; };
     auto raw_x = [&](int s) { return smem + s * raw_bytes + kWeightBytes; };
 
@@ -197,7 +188,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // the pair's barriers are set up before either arrives on the other's
     ptx::cluster_arrive();
     const int rtiles = (p.N + kPairRows - 1) / kPairRows;
-    const Tiles T{s_first, s_order, s_count, p.G, rtiles, ring.nmax};
+    const Tiles T{s_first, s_order, s_count, p.G, rtiles, rings.nmax};
     if (p.G > 1) {  // groups by the width of their tiles, stable
         const auto width = [&](int g) {
             const int c = s_count[g];
@@ -245,25 +236,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (waves > 0 && rest != 0 && rest * 4 < pairs) --waves;
     const int cut_tiles = tiles - waves * pairs;
     // (a merge costs about 4 units' time and 16 more for every 256 token columns)
-    const Cut ct = ring.nmax <= 32 ? cut<true>(cut_tiles, blocks, pairs, 4 + ring.nmax / 16)
-                                   : cut<false>(cut_tiles, blocks, pairs, 4 + ring.nmax / 16);
-    const int nacc = 2 * ring.nmax <= kMaxCols ? 2 : 1;  // accumulators
+    const Cut ct = rings.nmax <= 32 ? cut<true>(cut_tiles, blocks, pairs, 4 + rings.nmax / 16)
+                                   : cut<false>(cut_tiles, blocks, pairs, 4 + rings.nmax / 16);
+    const int nacc = 2 * rings.nmax <= kMaxCols ? 2 : 1;  // accumulators
     const uint32_t slots_at = taddr + kMaxCols;
     Work work(ct, waves, blocks, pair, pairs);
     Segment sg;
     ptx::cluster_wait();
     tc::fence_after_sync();
 
+    // the widening warps' waits for a unit
+    auto ready = [&](const Turn &st, const Turn &un) {
+        return ring::widen_ready(
+            [&] { return ptx::mbar_park(&unit_free[un.at], un.parity ^ 1u, kWaitNs); },
+            [&] { return ptx::mbar_park(&raw_full[st.at], st.parity, kWaitNs); });
+    };
+
     if (warp == kProducerWarp) {
         if (ptx::elect_one()) {
-            Turn st(ring.stages);
+            Turn st(rings.stages);
             uint32_t issued = 0;  // stages in use
             while (!s_failed && work.next(sg)) {
                 int g, r, m0, rows;
                 T.of(sg.tile, g, r, m0, rows);
                 const int half = (rows + 15) / 16 * 8;  // token rows of this CTA
-                const int boxes = (half + ring.box - 1) / ring.box;
-                const uint32_t bytes = kWeightBytes + boxes * ring.box * kAtom;
+                const int boxes = (half + rings.box - 1) / rings.box;
+                const uint32_t bytes = kWeightBytes + boxes * rings.box * kAtom;
                 const int w0 = r * kPairRows + rank * kTileRows, x0 = m0 + rank * half;
                 for (int kb = sg.k0; kb < sg.k1; ++kb, st.next()) {
                     const int s = (int)st.at;
@@ -275,25 +273,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     ptx::mbar_arrive_expect_tx(&raw_full[s], bytes);
                     tc::tma_load_3d(raw_w(s), &map_w, kb * kBlockK, w0, g, &raw_full[s]);
                     for (int b = 0; b < boxes; ++b)
-                        tc::tma_load_3d(raw_x(s) + b * ring.box * kAtom, &map_x, kb * kBlockK,
-                                        x0 + b * ring.box, g, &raw_full[s]);
+                        tc::tma_load_3d(raw_x(s) + b * rings.box * kAtom, &map_x, kb * kBlockK,
+                                        x0 + b * rings.box, g, &raw_full[s]);
                 }
             }
             // copies still in flight land before shared memory goes away
-            for (int i = 0; i < ring.stages; ++i, st.next()) {
+            for (int i = 0; i < rings.stages; ++i, st.next()) {
                 const uint32_t last = st.parity ^ 1u;
                 if (issued >> st.at & 1u) ptx::mbar_park(&raw_full[st.at], last, kWaitNs);
             }
         }
     } else if (warp == kMmaWarp) {
         if (rank == 0 && ptx::elect_one()) {
-            Turn un(ring.units), acc(nacc);
+            Turn un(rings.units), acc(nacc);
             const uint64_t bd0 = tc::smem_desc_sw128(ptx::smem_u32(wide));
             for (; !s_failed && work.next(sg); acc.next()) {
                 int g, r, m0, rows;
                 T.of(sg.tile, g, r, m0, rows);
                 const uint32_t idesc = tc::idesc_f16_f32(kPairRows, (rows + 15) / 16 * 16);
-                const uint32_t d = taddr + acc.at * ring.nmax;
+                const uint32_t d = taddr + acc.at * rings.nmax;
                 if (!ptx::mbar_park(&acc_free[acc.at], acc.parity ^ 1u, kWaitNs)) {
                     s_failed = 1;
                     break;
@@ -323,15 +321,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // Thread l of a group of four warps owns weight row l of the CTA's half =
         // lane l; the groups take the units in turn.
         const int row = (tid - kWeightWarp0 * 32) & 127, group = (warp - kWeightWarp0) >> 2;
-        Turn st(ring.stages), un(ring.units);
+        Turn st(rings.stages), un(rings.units);
         bool ok = true;
         uint32_t n = 0;
         while (ok && !warp_flag(&s_failed) && work.next(sg)) {
             for (int kb = sg.k0; kb < sg.k1; ++kb, st.next(), un.next(), ++n) {
                 if (n % kWeightGroups != (uint32_t)group) continue;
-                ok = __all_sync(0xffffffffu,
-                                ptx::mbar_park(&raw_full[st.at], st.parity, kWaitNs) &&
-                                    ptx::mbar_park(&unit_free[un.at], un.parity ^ 1u, kWaitNs));
+                ok = __all_sync(0xffffffffu, ready(st, un));
                 if (!ok) {
                     s_failed = 1;
                     break;
@@ -369,7 +365,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // l % 8: 8 consecutive lanes read (and write) 8 different 16-byte columns of
         // the swizzled rows, so no bank is hit twice.
         const int group = (warp - kTokenWarp0) / kGroupWarps, w = (warp - kTokenWarp0) % kGroupWarps;
-        Turn st(ring.stages), un(ring.units);
+        Turn st(rings.stages), un(rings.units);
         bool ok = true;
         uint32_t h = 0;
         while (ok && !warp_flag(&s_failed) && work.next(sg)) {
@@ -380,9 +376,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh, ++h) {
                     if (h % kGroups != (uint32_t)group) continue;
-                    ok = __all_sync(0xffffffffu,
-                                    ptx::mbar_park(&raw_full[st.at], st.parity, kWaitNs) &&
-                                        ptx::mbar_park(&unit_free[un.at], un.parity ^ 1u, kWaitNs));
+                    ok = __all_sync(0xffffffffu, ready(st, un));
                     if (!ok) {
                         s_failed = 1;
                         break;
@@ -482,7 +476,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 break;
             }
             tc::fence_after_sync();
-            const uint32_t from = taddr + acc.at * ring.nmax + ((uint32_t)(warp * 32) << 16);
+            const uint32_t from = taddr + acc.at * rings.nmax + ((uint32_t)(warp * 32) << 16);
             float *to = whole ? nullptr : part_of(pair);
             for (int n0 = 0; n0 < rows; n0 += kStepCols) {
                 uint32_t u[kStepCols];
@@ -567,37 +561,30 @@ cudaError_t launch_gemm_int8(GemmInt8Params p, int num_sms, cudaStream_t st) {
     int grid = num_sms < kStreamMaxCtas ? num_sms : kStreamMaxCtas;
     grid -= grid % 2;
     if (grid < 2) return cudaErrorInvalidValue;
-    Ring ring;
-    ring.nmax = gemm_int8_nmax(p.M);
+    int nmax = gemm_int8_nmax(p.M);
     if (p.G == 1 && p.counts == nullptr) {
         // Narrower tiles while they still find an idle pair each: a narrow unit takes
         // 650 cycles and its tile's reading little, a 256-column one 1024 and 5000
         // (333 x 1000 x 1040: 11.3 us on 8 pairs, 9.3 us on 44).
         const long long rt = (p.N + kPairRows - 1) / kPairRows;
-        while (ring.nmax > 32 &&
-               (p.M + ring.nmax / 2 - 1) / (ring.nmax / 2) * rt <= grid / 2)
-            ring.nmax /= 2;
+        while (nmax > 32 && (p.M + nmax / 2 - 1) / (nmax / 2) * rt <= grid / 2) nmax /= 2;
     }
-    p.nmax = ring.nmax;
-    ring.box = ring.nmax / 2 < 32 ? ring.nmax / 2 : 32;
-    const int half = ring.nmax / 2 * kAtom, raw = kWeightBytes + half;
-    ring.units = ring.nmax > 128 ? 3 : kMaxUnits;
-    ring.stages = ((int)kMaxDynamic - 1024 - 2 * ring.units * half) / raw;
-    if (ring.stages > kMaxStages) ring.stages = kMaxStages;
-    if (ring.stages < 2) return cudaErrorInvalidValue;
-    const size_t smem = 1024 + (size_t)ring.stages * raw + (size_t)2 * ring.units * half;
+    p.nmax = nmax;
+    const ring::Gemm rings = ring::gemm(nmax);
+    if (!ring::order_holds(rings.stages, rings.units)) return cudaErrorInvalidValue;
+    const size_t smem = (size_t)ring::gemm_bytes(rings);
     CUtensorMap mx, mw;
     const long long H = p.H;
     const long long ext_x[3] = {H, p.M, p.G}, str_x[3] = {1, H, H * p.M};
     const long long ext_w[3] = {H, p.N, p.G}, str_w[3] = {1, H, H * p.N};
-    const int box_x[3] = {kAtom, ring.box, 1}, box_w[3] = {kAtom, kTileRows, 1};
+    const int box_x[3] = {kAtom, rings.box, 1}, box_w[3] = {kAtom, kTileRows, 1};
     if (!make_map_nd(&mx, p.xq, 3, ext_x, str_x, box_x, true) ||
         !make_map_nd(&mw, p.wq, 3, ext_w, str_w, box_w, true))
         return cudaErrorInvalidValue;
     static std::atomic<unsigned long long> raised{0};
     cudaError_t err = raise_smem_limit_once(gemm_int8_kernel, kMaxDynamic, raised);
     if (err != cudaSuccess) return err;
-    return launch_pdl(gemm_int8_kernel, dim3(grid), dim3(kThreads), smem, st, mx, mw, p, ring);
+    return launch_pdl(gemm_int8_kernel, dim3(grid), dim3(kThreads), smem, st, mx, mw, p, rings);
 }
 
 }  // namespace moe
