@@ -40,6 +40,7 @@
 // all CTAs, outputs visible to all).
 #include "kernels.h"
 #include "pair.cuh"
+#include "ring.h"
 #include "smem_limit_once.h"
 #include "stream.cuh"
 #include "tcgen05.cuh"
@@ -60,17 +61,16 @@ constexpr int kProducerWarp = 4, kMmaWarp = 5, kLoaderWarp0 = 6;
 // Loader warps that take the units in turn.  No more than a ring has stages: a warp
 // knows of its last unit that all before the ring's length are free, and a wait by
 // parity may be at most one phase ahead of that.
-constexpr int kLoaders = 2, kMinStages = 2;
-static_assert(kLoaders <= kMinStages, "parity waits would run ahead");
+constexpr int kLoaders = 2;
+static_assert(kLoaders <= ring::kLayerMinStages, "parity waits would run ahead");
 constexpr int kConvertWarp0 = (kLoaderWarp0 + kLoaders + 3) / 4 * 4;  // warp mod 4: lane quadrant
 constexpr int kHalfRows = 64;   // gate rows (and up rows) of a W13 tile
 constexpr int kQuarter = 16;    // of them in a warp's 32 lanes: 16 gate rows, then 16 up rows
-constexpr int kSlots = 4;       // widened weight tiles in tensor memory
+constexpr int kSlots = ring::kLayerSlots;  // widened weight tiles in tensor memory
 constexpr int kSlotCols = kBlockK / 2;
 constexpr int kAccCols = 2 * kLayerMaxTokens;  // of an accumulator: both terms' columns
-constexpr int kMaxStages = 16;
-// dynamic shared memory: 227 KB a CTA less the static barriers
-constexpr size_t kMaxDynamic = (227 - 2) * 1024;
+constexpr int kMaxStages = ring::kLayerMaxStages;
+constexpr size_t kMaxDynamic = ring::kLayerDynamic;
 
 // The lists at the front of dynamic shared memory, for E experts and P pairs
 // (token, k).
@@ -83,10 +83,6 @@ struct Lists {
     uint16_t *base;    // [A + 1] their first pairs
     uint16_t *token;   // [P] token of a pair
     int16_t *place;    // [P] pair of (t, k), -1 where dropped
-    __host__ __device__ static int bytes(int E, int P) {
-        const int P8 = (P + 7) / 8 * 8;
-        return (P8 * 2 + P * 4 + E * 4 + E * 2 + (E < P ? E : P) * 4 + 2 + P * 4 + 15) / 16 * 16;
-    }
     __device__ Lists(uint8_t *mem, int E, int P) {
         const int A = E < P ? E : P;
         kept = reinterpret_cast<int16_t *>(mem);
@@ -104,7 +100,8 @@ template <int FORMAT>
 struct Shape {
     static constexpr bool kWiden = FORMAT != MOE_FORMAT_BF16;
     static constexpr int kThreads = (kWiden ? kConvertWarp0 + 8 : kLoaderWarp0 + kLoaders) * 32;
-    static constexpr int kA = kTileRows * kBlockK * (kWiden ? 1 : 2);  // weight bytes a stage
+    static constexpr int kValue = kWiden ? 1 : 2;                     // bytes of a weight
+    static constexpr int kA = kTileRows * kBlockK * kValue;           // weight bytes a stage
     static constexpr int kTmem = kWiden ? 512 : 256;                   // tensor-memory columns
 };
 
@@ -124,8 +121,9 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
     const int P = p.T * p.K, cta = blockIdx.x, ctas = gridDim.x;
 
     const Lists L(smem_raw, p.E, P);
-    const uint32_t after = ptx::smem_u32(smem_raw) + Lists::bytes(p.E, P);
-    uint8_t *ring = smem_raw + Lists::bytes(p.E, P) + ((1024u - (after & 1023u)) & 1023u);
+    const uint32_t after = ptx::smem_u32(smem_raw) + ring::layer_list_bytes(p.E, P);
+    uint8_t *stage0 =
+        smem_raw + ring::layer_list_bytes(p.E, P) + ((1024u - (after & 1023u)) & 1023u);
     if (warp == kMmaWarp) tc::tmem_alloc(&s_taddr, S::kTmem);
     if (tid < kMaxStages) {
         ptx::mbar_init(&bar_a[tid], 1);
@@ -274,11 +272,11 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
     // groups of 8, 64 columns at a time; in phase 1 the rows of the activations'
     // second term stand behind those of the first.  (Products read 16 rows at a
     // time: what they read past the rows only reaches columns that nobody reads.)
-    const int b_half = (s_most + 7) / 8 * 8 * 2 * kAtom;
-    const int stage_bytes = S::kA + 2 * b_half;
-    const int stages = min(kMaxStages, p.ring_bytes / stage_bytes);
-    auto stage_a = [&](int s) { return ring + s * stage_bytes; };
-    auto stage_b = [&](int s) { return ring + s * stage_bytes + S::kA; };
+    const int b_half = ring::layer_half_bytes(s_most);
+    const int stage_bytes = ring::layer_stage_bytes(S::kValue, s_most);
+    const int stages = ring::layer_stages(p.ring_bytes, S::kValue, s_most);
+    auto stage_a = [&](int s) { return stage0 + s * stage_bytes; };
+    auto stage_b = [&](int s) { return stage0 + s * stage_bytes + S::kA; };
     // phase 0: tiles (expert, 64 gate + 64 up rows); phase 1: (128 rows of H, expert)
     const int tiles0 = (p.I + kHalfRows - 1) / kHalfRows, tiles1 = (p.H + kTileRows - 1) / kTileRows;
     const int blocks0 = (p.H + kBlockK - 1) / kBlockK, blocks1 = (p.I + kBlockK - 1) / kBlockK;
@@ -340,7 +338,7 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
         if (ptx::elect_one()) {
             uint32_t it = 0;
             Turn st(stages), wide(kSlots);
-            const uint64_t ad0 = tc::smem_desc_sw128(ptx::smem_u32(ring));
+            const uint64_t ad0 = tc::smem_desc_sw128(ptx::smem_u32(stage0));
             const uint64_t half_a = kTileRows * kAtom / 16, half_b = b_half / 16;
             for (int phase = 0; phase < 2; ++phase) {
                 Segments segs(cuts[phase], cta, phase ? blocks1 : blocks0);
@@ -458,8 +456,9 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
             if ((n & 1u) != (uint32_t)group) continue;
             if (warp_flag(&s_failed)) break;
             const int s = (int)st.at, q = (int)wide.at;
-            const bool ok = ptx::mbar_park(&bar_a[s], st.parity, kWaitNs) &&
-                            ptx::mbar_park(&wide_free[q], wide.parity ^ 1u, kWaitNs);
+            const bool ok = ring::widen_ready(
+                [&] { return ptx::mbar_park(&wide_free[q], wide.parity ^ 1u, kWaitNs); },
+                [&] { return ptx::mbar_park(&bar_a[s], st.parity, kWaitNs); });
             if (!__all_sync(0xffffffffu, ok)) {
                 s_failed = 1;
                 break;
@@ -679,12 +678,11 @@ cudaError_t launch_t(LayerSmallParams &p, int num_sms, cudaStream_t st) {
     if (!make_map_nd(&m13, p.w13, 5, ext13, str13, box13, S::kWiden) ||
         !make_map_nd(&m2, p.w2, 3, ext2, str2, box2, S::kWiden))
         return cudaErrorInvalidValue;
-    // 1 KB aligns the ring and 1 KB stands behind it (reads of 16 rows where there are 8)
-    const int front = Lists::bytes(p.E, p.T * p.K) + 2048;
-    p.ring_bytes = (int)kMaxDynamic - front;
-    const int most = (p.T + 7) / 8 * 8;  // token rows of an expert
-    if (p.ring_bytes < kMinStages * (S::kA + 4 * most * kAtom)) return cudaErrorInvalidValue;
-    const size_t smem = (size_t)front + (size_t)p.ring_bytes;
+    const int P = p.T * p.K;
+    p.ring_bytes = ring::layer_ring_bytes(p.E, P);
+    if (!ring::layer_holds(S::kValue, ring::layer_stages(p.ring_bytes, S::kValue, p.T)))
+        return cudaErrorInvalidValue;
+    const size_t smem = (size_t)ring::layer_front_bytes(p.E, P) + (size_t)p.ring_bytes;
     static std::atomic<unsigned long long> raised{0};
     cudaError_t err = raise_smem_limit_once(layer_small_kernel<FORMAT>, kMaxDynamic, raised);
     if (err != cudaSuccess) return err;

@@ -1,6 +1,6 @@
-// ring.h -- the rings of the persistent products (gemm_int8.cu): what they
-// hold, and the order in which a widening warp waits on them.  Plain C++, so
-// that the host can go through the rule (tests/test_moe_rings.py).
+// ring.h -- the rings of the persistent products (gemm_int8.cu, layer_small.cu):
+// what they hold, and the order in which a widening warp waits on them.  Plain
+// C++, so that the host can go through the rule (tests/test_moe_rings.py).
 // Internal to libmoe_a2a.so.
 //
 // A stage holds a unit's 8-bit rows as TMA brought them, a place what they
@@ -73,6 +73,46 @@ inline Gemm gemm(int nmax) {
 inline int gemm_bytes(const Gemm &r) {
     const int half = r.nmax / 2 * kGemmRowBytes;
     return 1024 + r.stages * (kGemmWeightBytes + half) + 2 * r.units * half;
+}
+
+// ---- layer for a few tokens -----------------------------------------------------
+
+constexpr int kLayerSlots = 4;        // places: widened weight tiles in tensor memory
+constexpr int kLayerMaxStages = 16;
+constexpr int kLayerMinStages = 2;
+// dynamic shared memory: 227 KB a CTA less the static barriers
+constexpr int kLayerDynamic = (227 - 2) * 1024;
+
+// Bytes of the lists of E experts and P pairs (token, k), in front of the stages.
+MOE_RING_FN constexpr int layer_list_bytes(int E, int P) {
+    const int P8 = (P + 7) / 8 * 8;
+    return (P8 * 2 + P * 4 + E * 4 + E * 2 + (E < P ? E : P) * 4 + 2 + P * 4 + 15) / 16 * 16;
+}
+
+// Bytes in front of the stages and behind them: 1 KB aligns the ring and 1 KB
+// stands behind it (reads of 16 rows where there are 8).
+MOE_RING_FN constexpr int layer_front_bytes(int E, int P) { return layer_list_bytes(E, P) + 2048; }
+MOE_RING_FN constexpr int layer_ring_bytes(int E, int P) {
+    return kLayerDynamic - layer_front_bytes(E, P);
+}
+
+// Token rows of a stage, twice: the halves of 64 columns in phase 0, the two
+// terms of the activations in phase 1.
+MOE_RING_FN constexpr int layer_half_bytes(int rows) { return (rows + 7) / 8 * 8 * 2 * 128; }
+
+// Stages of 128 weight rows (128 columns of `value_bytes` each) and the token rows of
+// an expert of `rows` pairs.
+MOE_RING_FN constexpr int layer_stage_bytes(int value_bytes, int rows) {
+    return 128 * 128 * value_bytes + 2 * layer_half_bytes(rows);
+}
+MOE_RING_FN constexpr int layer_stages(int ring_bytes, int value_bytes, int rows) {
+    const int n = ring_bytes / layer_stage_bytes(value_bytes, rows);
+    return n < kLayerMaxStages ? n : kLayerMaxStages;
+}
+
+// Whether a ring of `stages` serves: 8-bit weights (value_bytes 1) are widened.
+MOE_RING_FN constexpr bool layer_holds(int value_bytes, int stages) {
+    return stages >= kLayerMinStages && (value_bytes != 1 || order_holds(stages, kLayerSlots));
 }
 
 }  // namespace ring

@@ -35,6 +35,17 @@ void gemm_ring(int nmax, int *out) {
     out[0] = r.nmax, out[1] = r.box, out[2] = r.stages, out[3] = r.units;
     out[4] = moe::ring::gemm_bytes(r);
 }
+int layer_stages(int E, int P, int value_bytes, int rows) {
+    return moe::ring::layer_stages(moe::ring::layer_ring_bytes(E, P), value_bytes, rows);
+}
+int layer_bytes(int E, int P, int value_bytes, int rows) {
+    return moe::ring::layer_front_bytes(E, P) +
+           layer_stages(E, P, value_bytes, rows) * moe::ring::layer_stage_bytes(value_bytes, rows);
+}
+int layer_holds(int value_bytes, int stages) {
+    return moe::ring::layer_holds(value_bytes, stages);
+}
+int layer_slots() { return moe::ring::kLayerSlots; }
 }
 """
 
@@ -154,3 +165,35 @@ def test_product_waits(ring):
     assert first in (0, 1)
     for S, U in sorted(shapes):
         assert not reads_unlanded_unit(S, U, place_first=first == 0, turns=ring.turns()), (S, U)
+
+
+def layer_sizes():
+    """Experts, top-k and tokens up to their limits; the fullest expert takes 1 .. all tokens."""
+    for E in (1, 2, 31, 64, 300, 1024):
+        for K in (1, 2, 8, 32):
+            for T in (1, 7, 8, 33, 41, 48, 56, 64):
+                for rows in range(1, T + 1):
+                    yield E, K, T, rows
+
+
+def test_layer_rings(ring):
+    stages = set()
+    for E, K, T, rows in layer_sizes():
+        for size in (1, 2):
+            n = ring.layer_stages(E, T * K, size, rows)
+            assert ring.layer_holds(size, n), (E, K, T, rows, size)
+            assert ring.layer_bytes(E, T * K, size, rows) <= (227 - 2) * 1024
+            if size == 1:
+                stages.add(n)
+    assert {4, 5, 7} <= stages                          # odd rings are met
+    assert not ring.layer_holds(1, 3) and ring.layer_holds(2, 3)
+    assert not ring.layer_holds(2, 1)
+
+
+def test_layer_waits(ring):
+    U = ring.layer_slots()
+    assert reads_unlanded_unit(5, U, place_first=False, freed_by_products=True)
+    first = ring.first_wait()
+    for S in {min(ring.layer_stages(E, T * K, 1, rows), 7) for E, K, T, rows in layer_sizes()}:
+        assert not reads_unlanded_unit(S, U, place_first=first == 0, freed_by_products=True,
+                                       turns=ring.turns()), S
