@@ -101,3 +101,47 @@ def test_layer_hot_expert_with_rings_that_turn(api, fmt, T):
         assert (err <= tol).all(), (float((err / tol).max()), float(err.max()))
         first = out if first is None else first
         assert torch.equal(out.view(torch.int16), first.view(torch.int16))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("H,I", [(2048, 1024), (2048, 8192), (272, 144)])  # whole, cut, ragged
+def test_layer_keeps_the_second_term_of_the_activations(api, fmt, H, I):
+    # W2 subtracts activations that are all near 3, so outputs are small beside what
+    # the leading terms leave out (up to 2^-7 each).  Experts of 1, 9 and 54 tokens.
+    E, T = 3, 64
+    g = gen(H + I)
+    d = torch.randint(-15, 16, (E, I), generator=g, device=DEV).float()  # exact in 8 bits
+    w13 = torch.zeros((E, 2 * I, H), device=DEV)
+    w13[:, :I, 0], w13[:, :I, H - 1], w13[:, I:, 0] = 3.0, d, 1.0
+    i = torch.randint(0, I, (E, H), generator=g, device=DEV)
+    j = (i + torch.randint(1, I, (E, H), generator=g, device=DEV)) % I
+    w2 = torch.zeros((E, H, I), device=DEV)
+    w2.scatter_(2, i[:, :, None], 1.0)
+    w2.scatter_(2, j[:, :, None], -1.0)
+    x = torch.zeros((T, H), device=DEV)
+    x[:, 0] = 1.0
+    x[:, H - 1] = (1.0 + torch.arange(T, device=DEV) / 64) / 64
+    x = x.to(torch.bfloat16)
+    ids = torch.full((T, 1), 2, dtype=torch.int32, device=DEV)
+    ids[20], ids[3:12] = 0, 1
+    w = torch.ones((T, 1), device=DEV)
+    one = [None if fmt == "bf16" else torch.ones((E, n), device=DEV) for n in (2 * I, H)]
+    kind = {"bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn, "int8": torch.int8}[fmt]
+    h = handle(api, E, H, I, 1, T, fmt)
+    out = h.forward(x, ids, w, w13.to(kind), w2.to(kind), *one).double()
+    assert h.get_error() == (0, 0)
+    # two products of a row are not zero, and sums with zeros are exact
+    X = x.double()
+    for e in range(E):
+        t = (ids[:, 0] == e).nonzero()[:, 0]
+        gate = X[t] @ w13[e, :I].double().T             # up is 1, exactly
+        a = gate * torch.sigmoid(gate)
+        B = w2[e].double()
+        da = 1.1 * 4 * 2.0 ** -23 * gate.abs() + (2.0 ** -16 + 2.0 ** -20) * a
+        dy = da @ B.abs().T + 4 * 2.0 ** -23 * (1.01 * a) @ B.abs().T
+        y = a @ B.T
+        tol = dy + 2.0 ** -8 * (y.abs() + dy)
+        assert ((out[t] - y).abs() <= tol).all(), (e, float(((out[t] - y).abs() / tol).max()))
+        # the leading terms alone would not pass, whatever the token
+        lead = a.to(torch.bfloat16).double() @ B.T
+        assert ((lead - y).abs() > tol).any(1).all()
