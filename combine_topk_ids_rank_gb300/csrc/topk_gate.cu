@@ -6,7 +6,7 @@
 //   ids[0..K) = the K experts of S with the largest logits, descending, equal
 //               logits by ascending expert id; -1 past |S|,
 //   softmax:  s_e = exp(l_e - m) / sum_{f in S} exp(l_f - m), m = max over S,
-//   sigmoid:  s_e = 1 / (1 + exp(-l_e)),
+//   sigmoid:  s_e = 1 / (1 + exp(-l_e)), 0 where exp(-l_e) leaves binary64,
 //   w[k] = scale * s_{ids[k]} (/ sum of the K selected s if renormalised; 0
 //          where ids[k] = -1).
 // Both scores grow with the logit, so the logits themselves are compared,
@@ -116,6 +116,15 @@ __device__ __forceinline__ float value_of(uint32_t k) {
 // exp(v - top), 1 where they are equal (also for +inf, whose difference is NaN)
 __device__ __forceinline__ float exp_from(float v, float top) {
     return v == top ? 1.0f : expf(v - top);
+}
+
+// 1 / (1 + exp(-v)), times exp(-shift) for v < 0.  A renormalised token whose
+// largest logit is negative takes that logit for the shift: its scores are fractions
+// of one another, and may all be below what fp32 holds (from -87 down).  What
+// binary64 does not hold either counts as 0: exp(-v) past its largest number, exp(709.78).
+__device__ __forceinline__ float sigmoid_from(float v, float shift) {
+    if (v >= 0.0f) return 1.0f / (1.0f + expf(-v));
+    return v < -709.7827f ? 0.0f : expf(v - shift) / (1.0f + expf(v));
 }
 
 // Sorts descending.
@@ -245,8 +254,9 @@ __global__ void __launch_bounds__(kThreads) topk_gate_kernel(const TopkGateParam
         if (BF16 && sel_key >= 0x80000000u) sel_key &= 0xffff0000u;
         float s = 0.0f;
         const float v = logit_of(sel_key), l0 = __shfl_sync(kFull, v, 0);
-        if (sel_id >= 0)  // (equal to the maximum: also for +inf, whose difference is NaN)
-            s = p.sigmoid ? 1.0f / (1.0f + expf(-v)) : (v == l0 ? 1.0f : expf(v - l0));
+        if (sel_id >= 0)
+            s = p.sigmoid ? sigmoid_from(v, p.renormalize ? fminf(l0, 0.0f) : 0.0f)
+                          : exp_from(v, l0);
         float sum = total;
         if (p.renormalize) {
             sum = s;
@@ -424,7 +434,9 @@ __global__ void __launch_bounds__(kThreads) topk_gate_packed_kernel(const TopkGa
         }
         const float top = __shfl_sync(kFull, v, lane & 24);
         float s = 0.0f;
-        if (some) s = p.sigmoid ? 1.0f / (1.0f + expf(-v)) : exp_from(v, top);
+        if (some)
+            s = p.sigmoid ? sigmoid_from(v, p.renormalize ? fminf(top, 0.0f) : 0.0f)
+                          : exp_from(v, top);
         if (p.renormalize) {
             total = s;
             for (int o = 4; o > 0; o >>= 1) total += __shfl_xor_sync(kFull, total, o);

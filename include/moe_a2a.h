@@ -478,7 +478,7 @@ int moe_quantize_rows_fp8(const float *d_x, int64_t rows, int32_t hidden, void *
  *     descending order, equal logits by ascending id; -1 past |S|;
  *   score s_e = exp(l_e - max) / sum over S (MOE_SCORE_SOFTMAX; a row with
  *     +inf shares the weight among its infinities), or 1 / (1 + exp(-l_e))
- *     (MOE_SCORE_SIGMOID);
+ *     (MOE_SCORE_SIGMOID), 0 where exp(-l_e) leaves binary64 (l_e < -709.78);
  *   d_topk_w[t][k] = scale * s, divided by the sum of the K selected scores
  *     if renormalize; 0 where the id is -1.
  * fp32 arithmetic whatever the logits' type.
