@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kThreads) topk_gate_kernel(const TopkGateParam
         if ((p.renormalize || !p.sigmoid) && s != 0.0f) s = s / sum;
         if (lane < p.K) {
             p.topk_ids[t * p.K + lane] = sel_id;
-            p.topk_w[t * p.K + lane] = s * p.scale;
+            p.topk_w[t * p.K + lane] = sel_id >= 0 ? s * p.scale : 0.0f;  // (any scale)
         }
     }
     publish();
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(kThreads) topk_gate_packed_kernel(const TopkGa
         if ((p.renormalize || !p.sigmoid) && s != 0.0f) s = s / total;
         if (q < NT && k < p.K && t0 + q < p.tokens) {
             p.topk_ids[(t0 + q) * p.K + k] = id;
-            p.topk_w[(t0 + q) * p.K + k] = s * p.scale;
+            p.topk_w[(t0 + q) * p.K + k] = id >= 0 ? s * p.scale : 0.0f;  // (any scale)
         }
     }
     publish();

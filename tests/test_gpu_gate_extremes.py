@@ -56,3 +56,17 @@ def test_sigmoid_weights_far_below_zero(api, E, K, T, dtype, renorm):
     assert (np.abs(got - rw) <= tol).all(), float((np.abs(got - rw) / tol).max())
     if renorm:
         assert np.abs(got.sum(-1) / 2.5 - 1.0).max() < 1e-5
+
+
+@pytest.mark.parametrize("E,K", [(40, 8), (256, 8), (64, 20), (600, 8)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("scale", [float("inf"), float("nan")])
+def test_places_without_an_expert_weigh_nothing_at_any_scale(api, E, K, dtype, scale):
+    l = torch.full((5, E), -float("inf"), device=DEV)
+    l[1, 3], l[2, :K], l[4, :2] = 0.5, 1.0, float("nan")
+    for sigmoid in (api.MOE_SCORE_SOFTMAX, api.MOE_SCORE_SIGMOID):
+        for renorm in (True, False):
+            ids, w = api.topk_gate(l.to(dtype), K, sigmoid, renorm, scale)
+            assert (ids >= 0).sum(-1).tolist() == [0, 1, K, 0, 0]
+            assert (w[ids < 0] == 0).all()
+            assert not torch.isfinite(w[ids >= 0]).any()
