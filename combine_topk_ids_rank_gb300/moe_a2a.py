@@ -396,10 +396,25 @@ def moe_scratch_get_error(d_scratch: int, stream: int = 0):
 
 # ---- torch forms of the operators around dispatch and combine ------------------
 
+def _on_current(device):
+    """The C entries launch on the current device and size their grids for it: refuse
+    tensors of another one (its default stream has the same number, 0)."""
+    if device.index != _current_device():
+        raise ValueError("%s is not the current CUDA device (%s): call under "
+                         "torch.cuda.device(%s)" % (device, _current_device(), device.index))
+
+
 def _raw_stream(stream, device) -> int:
+    _on_current(device)
     if stream is None:
         return _current_stream(device.index)
+    if getattr(stream, "device", device) != device:
+        raise ValueError("a stream of %s for tensors of %s" % (stream.device, device))
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _current_device() -> int:
+    return _torch.cuda.current_device()
 
 
 def _current_stream(index: int) -> int:
@@ -409,6 +424,8 @@ def _current_stream(index: int) -> int:
 if hasattr(getattr(_torch, "_C", None), "_cuda_getCurrentRawStream"):
     # the same number without the Stream object around it (1.9 us less a call)
     _current_stream = _torch._C._cuda_getCurrentRawStream  # noqa: F811
+if hasattr(getattr(_torch, "_C", None), "_cuda_getDevice"):
+    _current_device = _torch._C._cuda_getDevice  # noqa: F811  (a tensor is there: initialised)
 
 
 def _empty(shape, dtype, device, stream, raw):
@@ -444,7 +461,7 @@ def topk_gate(logits, top_k: int, scoring: int = MOE_SCORE_SOFTMAX, renormalize:
             raise ValueError("logits must be contiguous, or 2-D with dense rows")
         row_stride = logits.stride(0)
     shape = (*lead, top_k)
-    raw = _current_stream(device.index) if stream is None else _raw_stream(stream, device)
+    raw = _raw_stream(stream, device)
     if out_ids is None:
         out_ids = _empty(shape, _torch.int32, device, stream, raw)
     else:
@@ -483,7 +500,7 @@ def quantize_rows_int8(x, counts=None, out=None, scale=None, stream=None):
             raise ValueError("with counts x must be [groups, rows, hidden]")
         groups, rows = lead
         _expect(counts, _torch.int32, (groups,), device, "counts")
-    raw = _current_stream(device.index) if stream is None else _raw_stream(stream, device)
+    raw = _raw_stream(stream, device)
     if out is None:
         out = _empty(shape, _torch.int8, device, stream, raw)
     else:
@@ -509,6 +526,7 @@ class _Scratch:
         self.device = _torch.device(device if device is not None else "cuda")
         self.scratch = _torch.empty(nbytes, dtype=_torch.uint8, device=self.device)
         self.device = self.scratch.device
+        _on_current(self.device)
         self._scratch_ptr, self._scratch_bytes = self.scratch.data_ptr(), nbytes
         stream = _torch.cuda.current_stream(self.device)
         st = moe_scratch_init(self.scratch.data_ptr(), nbytes, stream.cuda_stream)
