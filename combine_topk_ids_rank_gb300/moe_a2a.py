@@ -252,11 +252,8 @@ def quantize_rows_fp8(x, out=None, scale=None, stream=None):
         out = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
     if scale is None:
         scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    if stream is None:
-        stream = torch.cuda.current_stream(x.device)
     st = moe_quantize_rows_fp8(x.data_ptr(), rows, H, out.data_ptr(), scale.data_ptr(),
-                               stream.cuda_stream if hasattr(stream, "cuda_stream")
-                               else int(stream))
+                               _raw_stream(stream, x.device))
     if st != MOE_OK:
         raise MoeA2AError(st, "moe_quantize_rows_fp8")
     return out, scale
@@ -699,6 +696,7 @@ class MoeA2A:
             raise MoeA2AError(MOE_ERR_INVALID_ARG, "moe_a2a_workspace_bytes_layout")
         self.device = torch.device(device if device is not None else "cuda")
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        _on_current(self.workspace.device)  # the handle is prepared for the current device
         st, self.handle = moe_a2a_create_layout(self.cfg, layout, self.workspace.data_ptr(),
                                                 nbytes)
         if st != MOE_OK:
@@ -708,10 +706,7 @@ class MoeA2A:
         self._payload = None
 
     def _stream(self, stream) -> int:
-        import torch
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        return _raw_stream(stream, self.workspace.device)
 
     def _check(self, t, dtype, shape, name):
         if t.dtype != dtype or tuple(t.shape) != tuple(shape):

@@ -119,3 +119,37 @@ def test_scratch_on_another_device_is_refused(api, monkeypatch):
     with pytest.raises(ValueError, match="not the current CUDA device"):
         api.MoeGemmInt8(1, 4, 8, 16, "cuda:1")
     assert api._lib.calls == []
+
+
+def a2a(api, index):
+    a = api.MoeA2A.__new__(api.MoeA2A)
+    a.__dict__.update(ep_size=2, hidden=16, top_k=2, num_experts=4, layout=api.MOE_LAYOUT_RANK,
+                      handle=None, last_view=None, workspace=Stand((1 << 20,), torch.uint8, index),
+                      device=torch.device("cuda", index))
+    return a
+
+
+def test_dispatch_and_combine_on_another_device_are_refused(api):
+    S = lambda shape, dtype: Stand(shape, dtype, 1)
+    a = a2a(api, 1)
+    ids, w, x = (S((2, 3, 2), torch.int32), S((2, 3, 2), torch.float32),
+                 S((2, 3, 16), torch.bfloat16))
+    for call in (lambda: a.dispatch(ids, w, x), lambda: a.dispatch_varlen(ids, w, x, [3, 1]),
+                 lambda: a.combine(), lambda: a.combine_fp8(), lambda: a.get_error(),
+                 lambda: a.get_error(StandStream(1)),
+                 lambda: api.quantize_rows_fp8(S((3, 16), torch.float32),
+                                               S((3, 16), torch.float8_e4m3fn),
+                                               S((3,), torch.float32))):
+        with pytest.raises(ValueError, match="not the current CUDA device"):
+            call()
+    assert api._lib.calls == []
+    assert a2a(api, 0).get_error()[0] == api.MOE_OK and api._lib.calls == ["moe_a2a_get_error"]
+
+
+def test_workspace_on_another_device_is_refused(api, monkeypatch):
+    monkeypatch.setattr(torch, "empty",
+                        lambda n, dtype, device: Stand((n,), dtype, torch.device(device).index))
+    monkeypatch.setattr(api, "moe_a2a_workspace_bytes_layout", lambda cfg, layout: 1 << 20)
+    with pytest.raises(ValueError, match="not the current CUDA device"):
+        api.MoeA2A(2, 8, 16, 4, 2, "cuda:1")
+    assert api._lib.calls == []
