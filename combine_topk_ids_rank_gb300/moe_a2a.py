@@ -515,7 +515,10 @@ def quantize_rows_int8(x, counts=None, out=None, scale=None, stream=None):
 
 
 class _Scratch:
-    """Device memory that one operator keeps between its calls."""
+    """Device memory that one operator keeps between its calls.  The allocator is
+    told of every torch stream that it is used on, so the handle may be dropped
+    while a call runs.  For a stream given as a bare number the caller keeps the
+    handle until that call is through."""
 
     def __init__(self, nbytes: int, device, where: str):
         if nbytes == 0:
@@ -530,6 +533,18 @@ class _Scratch:
         if st != MOE_OK:
             raise MoeA2AError(st, "moe_scratch_init")
         stream.synchronize()  # calls may come on any stream
+        self._streams = {stream.cuda_stream}
+
+    def _launch_stream(self, stream) -> int:
+        """The raw stream of a call that is about to use the scratch memory."""
+        raw = _raw_stream(stream, self.device)
+        if raw not in self._streams:
+            if stream is None:
+                stream = _torch.cuda.current_stream(self.device)
+            if hasattr(stream, "cuda_stream"):
+                self.scratch.record_stream(stream)
+                self._streams.add(raw)
+        return raw
 
     def get_error(self, stream=None):
         """Synchronise, read and clear the device flag word: (status, bits)."""
@@ -561,7 +576,7 @@ class MoeGemmInt8(_Scratch):
             _expect(counts, _torch.int32, (G,), dev, "counts")
         if rows > self.max_rows:
             raise MoeA2AError(MOE_ERR_CAPACITY, "moe_gemm_int8")
-        raw = _raw_stream(stream, dev)
+        raw = self._launch_stream(stream)
         if out is None:
             out = _empty((*lead, rows, N), _torch.bfloat16, dev, stream, raw)
         else:
@@ -615,7 +630,7 @@ class MoeLayerSmall(_Scratch):
             _expect(w2_scale, _torch.float32, (E, H), dev, "w2_scale")
         if residual is not None:
             _expect(residual, _torch.bfloat16, (T, H), dev, "residual")
-        raw = _raw_stream(stream, dev)
+        raw = self._launch_stream(stream)
         if out is None:
             out = _empty((T, H), _torch.bfloat16, dev, stream, raw)
         else:

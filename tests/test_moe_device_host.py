@@ -27,10 +27,13 @@ class Stand:
     def data_ptr(self):
         return 1 << 20
 
+    def record_stream(self, stream):
+        self.recorded = getattr(self, "recorded", []) + [stream.cuda_stream]
+
 
 class StandStream:
-    def __init__(self, index):
-        self.device, self.cuda_stream = torch.device("cuda", index), 0
+    def __init__(self, index, raw=0):
+        self.device, self.cuda_stream = torch.device("cuda", index), raw
 
 
 class Library:
@@ -61,7 +64,7 @@ def handle(cls, index, **fields):
     h = cls.__new__(cls)
     h.__dict__.update(fields, device=torch.device("cuda", index), _scratch_ptr=1 << 20,
                       _scratch_bytes=1 << 20, scratch=Stand((1 << 20,), torch.uint8, index),
-                      _home=0, _streams={0})
+                      _streams={0})
     return h
 
 
@@ -153,3 +156,25 @@ def test_workspace_on_another_device_is_refused(api, monkeypatch):
     with pytest.raises(ValueError, match="not the current CUDA device"):
         api.MoeA2A(2, 8, 16, 4, 2, "cuda:1")
     assert api._lib.calls == []
+
+
+def test_scratch_is_tied_to_the_streams_it_is_used_on(api, monkeypatch):
+    h = handle(api.MoeGemmInt8, 0, groups=1, max_rows=4, N=8, hidden=16)
+    S = lambda shape, dtype: Stand(shape, dtype, 0)
+    args = (S((4, 16), torch.int8), S((4,), torch.float32), S((8, 16), torch.int8),
+            S((8,), torch.float32), None, S((4, 8), torch.bfloat16))
+    recorded = lambda: getattr(h.scratch, "recorded", [])
+    h.gemm(*args)                                       # where it was allocated
+    h.gemm(*args, stream=StandStream(0, 0))
+    assert recorded() == []
+    side = StandStream(0, 7)
+    h.gemm(*args, stream=side)
+    h.gemm(*args, stream=side)
+    assert recorded() == [7]                            # once a stream
+    h.gemm(*args, stream=9)                             # a bare number: the caller's part
+    assert recorded() == [7]
+    monkeypatch.setattr(api, "_current_stream", lambda index: 11)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: StandStream(0, 11))
+    h.gemm(*args)                                       # another stream made current
+    assert recorded() == [7, 11]
+    assert api._lib.calls == ["moe_gemm_int8"] * 6
