@@ -76,6 +76,9 @@ cudaError_t launch_layer_small(LayerSmallParams p, int num_sms, cudaStream_t st)
 
 // 8-bit integer product, dense or grouped.
 constexpr int kGemmInt8MaxGroups = 1024;
+// Rows, channels and hidden size: 32-bit coordinates, with room for rounding up to
+// whole tiles and for the evened width of a tile (rows + tiles, at most 2^23 of them).
+constexpr int kGemmInt8MaxExtent = INT32_MAX - (1 << 24);
 struct GemmInt8Params {
     const int8_t *xq;          // [G][M][H]
     const float *x_scale;      // [G][M]

@@ -125,9 +125,9 @@ int moe_gemm_int8(const int8_t *d_xq, const float *d_x_scale, const int8_t *d_wq
                   const float *d_w_scale, const int32_t *d_counts, int32_t groups, int32_t rows,
                   int32_t N, int32_t hidden, void *d_out, void *d_scratch, size_t scratch_bytes,
                   void *stream) {
-    // (2^31 rows of a plane set is the limit of a TMA coordinate)
     if (groups < 0 || groups > kGemmInt8MaxGroups || rows < 0 || N < 1 || hidden < 16 ||
-        hidden % 16 != 0 || (int64_t)groups * rows > INT32_MAX || (int64_t)groups * N > INT32_MAX)
+        hidden % 16 != 0 || hidden > kGemmInt8MaxExtent ||
+        (int64_t)groups * rows > kGemmInt8MaxExtent || (int64_t)groups * N > kGemmInt8MaxExtent)
         return MOE_ERR_INVALID_ARG;
     if (groups == 0 || rows == 0) return MOE_OK;
     // tiles are counted in 32 bits

@@ -522,7 +522,7 @@ int moe_quantize_rows_int8(const void *d_x, int32_t bf16, int32_t groups, int32_
  *   d_counts int32 [groups] or NULL (all rows): rows m >= d_counts[g] are not
  *           written (counts are clamped to 0..rows)
  *   hidden  a multiple of 16; N and rows any; groups <= 1024;
- *           groups * rows, groups * N < 2^31
+ *           hidden, groups * rows, groups * N < 2^31 - 2^24
  *   d_out   bf16 [groups][rows][N]
  *   d_scratch at least moe_gemm_int8_scratch_bytes(rows) bytes, 256-byte
  *           aligned, prepared once by moe_scratch_init and then used by one
