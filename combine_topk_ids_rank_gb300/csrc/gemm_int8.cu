@@ -497,8 +497,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive_pair(ptx::cluster_smem(&acc_free[acc.at], 0));
             if (whole) continue;
-            __threadfence();
+            // the warp's parts, then lane 0's fence and count; and the other way round: what
+            // lane 0 finds counted, its fence, then the warp's reads (a shuffle orders no memory)
             __syncwarp();
+            __threadfence();
             int last = 0;
             if (lane == 0) {
                 int *m = &p.header->merged[0][2 * parts.c0 + rank][warp];
@@ -507,6 +509,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 __threadfence();
             }
             if (!__shfl_sync(0xffffffffu, last, 0)) continue;
+            __syncwarp();
             for (int n0 = 0; n0 < rows; n0 += kStepCols) {
                 float v[kStepCols];
 #pragma unroll

@@ -410,6 +410,7 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
                 bool ok = true;
                 if (lane == 0) ok = wait_count(&p.header->done[0], A * tiles0 * 4, &s_failed);
                 if (!__all_sync(0xffffffffu, ok)) s_failed = 1;
+                __syncwarp();  // (a vote orders no memory)
             }
             while (!warp_flag(&s_failed) && segs.next(sg)) {
                 int a, r;
@@ -541,8 +542,11 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
                             if (n0 + i < rows) __stcg(to + (n0 + i) * kTileRows, v[i]);
                     }
                     tc::fence_before_sync();
-                    __threadfence();
+                    // the warp's parts, then lane 0's fence and count; and the other way
+                    // round: what lane 0 finds counted, its fence, then the warp's reads
+                    // (a shuffle orders no memory)
                     __syncwarp();
+                    __threadfence();
                     int last = 0;
                     if (lane == 0) {
                         mbar_arrive(&acc_free[b]);
@@ -552,6 +556,7 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
                         __threadfence();
                     }
                     if (!__shfl_sync(0xffffffffu, last, 0)) continue;
+                    __syncwarp();
                 }
                 // channel of this lane, whether it is stored, its scale
                 int chan, limit;
@@ -604,8 +609,8 @@ __global__ void __launch_bounds__(Shape<FORMAT>::kThreads, 1)
                     }
                 }
                 if (whole) tc::fence_before_sync();
-                __threadfence();
                 __syncwarp();
+                __threadfence();
                 if (lane == 0) {
                     if (whole) mbar_arrive(&acc_free[b]);
                     atomicAdd(&p.header->done[phase], 1);
