@@ -435,6 +435,9 @@ def _empty(shape, dtype, device, stream, raw):
         return _torch.empty(shape, dtype=dtype, device=device)
 
 
+_INT32_MAX = 2 ** 31 - 1  # sizes go to the C entries in 32 bits, and ctypes would wrap them
+
+
 def _expect(t, dtype, shape, device, name):
     if t.dtype is not dtype or t.shape != shape:
         raise ValueError("%s: expected %s %s, got %s %s" % (name, dtype, tuple(shape), t.dtype,
@@ -457,6 +460,8 @@ def topk_gate(logits, top_k: int, scoring: int = MOE_SCORE_SOFTMAX, renormalize:
         if logits.dim() != 2 or logits.stride(1) != 1 or logits.stride(0) < E:
             raise ValueError("logits must be contiguous, or 2-D with dense rows")
         row_stride = logits.stride(0)
+    if E > _INT32_MAX or top_k > _INT32_MAX:
+        raise MoeA2AError(MOE_ERR_INVALID_ARG, "moe_topk_gate")
     shape = (*lead, top_k)
     raw = _raw_stream(stream, device)
     if out_ids is None:
@@ -497,6 +502,8 @@ def quantize_rows_int8(x, counts=None, out=None, scale=None, stream=None):
             raise ValueError("with counts x must be [groups, rows, hidden]")
         groups, rows = lead
         _expect(counts, _torch.int32, (groups,), device, "counts")
+    if rows > _INT32_MAX or groups > _INT32_MAX or H > _INT32_MAX:
+        raise MoeA2AError(MOE_ERR_INVALID_ARG, "moe_quantize_rows_int8")
     raw = _raw_stream(stream, device)
     if out is None:
         out = _empty(shape, _torch.int8, device, stream, raw)
@@ -557,6 +564,8 @@ class MoeGemmInt8(_Scratch):
 
     def __init__(self, groups: int, max_rows: int, N: int, hidden: int, device=None):
         self.groups, self.max_rows, self.N, self.hidden = groups, max_rows, N, hidden
+        if max(groups, max_rows, N, hidden) > _INT32_MAX:
+            raise MoeA2AError(MOE_ERR_INVALID_ARG, "moe_gemm_int8")
         super().__init__(moe_gemm_int8_scratch_bytes(max_rows), device,
                          "moe_gemm_int8_scratch_bytes")
 
@@ -601,7 +610,8 @@ class MoeLayerSmall(_Scratch):
         self.max_tokens, self.fmt = max_tokens, fmt
         self._wtypes = {MOE_FORMAT_BF16: (_torch.bfloat16,), MOE_FORMAT_INT8: (_torch.int8,),
                         MOE_FORMAT_FP8_E4M3: (_torch.float8_e4m3fn, _torch.uint8)}.get(fmt)
-        if self._wtypes is None:
+        if self._wtypes is None or max(num_experts, hidden, inter, top_k,
+                                       max_tokens) > _INT32_MAX:
             raise MoeA2AError(MOE_ERR_INVALID_ARG, "moe_layer_small")
         super().__init__(moe_layer_small_scratch_bytes(max_tokens, top_k, hidden, inter), device,
                          "moe_layer_small_scratch_bytes")

@@ -45,7 +45,7 @@ class Library:
     def __getattr__(self, name):
         def entry(*args):
             self.calls.append(name)
-            return 0
+            return b"" if name == "moe_a2a_status_string" else 0
         return entry
 
 
@@ -178,3 +178,31 @@ def test_scratch_is_tied_to_the_streams_it_is_used_on(api, monkeypatch):
     h.gemm(*args)                                       # another stream made current
     assert recorded() == [7, 11]
     assert api._lib.calls == ["moe_gemm_int8"] * 6
+
+
+def test_sizes_past_32_bits_are_refused(api, monkeypatch):
+    # 2^32 + 5 rows are not 5 rows
+    S = lambda shape, dtype: Stand(shape, dtype, 0)
+    f32, i32, i8 = torch.float32, torch.int32, torch.int8
+    monkeypatch.setattr(api._torch, "empty",
+                        lambda shape, dtype, device: Stand(
+                            shape if isinstance(shape, (tuple, list, torch.Size)) else (shape,),
+                            dtype, 0))
+    big = 2 ** 32
+    for call in (
+            lambda: api.quantize_rows_int8(S((big + 5, 8), f32)),
+            lambda: api.quantize_rows_int8(S((2, big + 5, 8), f32), S((2,), i32)),
+            lambda: api.quantize_rows_int8(S((big + 5, 2, 8), f32), S((big + 5,), i32)),
+            lambda: api.quantize_rows_int8(S((2, big + 64), f32)),
+            lambda: api.topk_gate(S((2, big + 64), f32), 2),
+            lambda: api.topk_gate(S((2, 64), f32), big + 2),
+            lambda: api.MoeGemmInt8(1, big + 4, 8, 16, "cuda:0"),
+            lambda: api.MoeGemmInt8(1, 4, big + 8, 16, "cuda:0"),
+            lambda: api.MoeGemmInt8(1, 4, 8, big + 16, "cuda:0"),
+            lambda: api.MoeLayerSmall(4, big + 16, 16, 2, 4, device="cuda:0"),
+            lambda: api.MoeLayerSmall(big + 4, 16, 16, 2, 4, device="cuda:0"),
+            lambda: api.MoeLayerSmall(4, 16, 16, 2, big + 4, device="cuda:0")):
+        with pytest.raises(api.MoeA2AError):
+            call()
+    # (only the text of the error was asked for)
+    assert set(api._lib.calls) <= {"moe_a2a_status_string"}
