@@ -30,8 +30,13 @@
 // rate of a bf16 product), bound by the tensor cores.  One CTA a tile took 593
 // us: it widens each token row twice as often.  16 tokens x 7168 x 4096: 15 us
 // for 29 MB (4.4 us); bound by the widening of a unit (about 650 cycles) and
-// the joining of cut tiles.  32 groups of up to 1024 rows, 4096 x 2048: 155 us;
-// the products are 77 us of it, the reading of accumulators between them 17 %.
+// the joining of cut tiles.  32 groups of up to 1024 rows, 4096 x 2048: 154 us,
+// where 98 us of products would do (the tensor pipe is active 52 % of the time).  A
+// tile of 256 columns has one accumulator, which is read between its products and the
+// next tile's (two shorter ones gained 1 % at most), and a group of few rows waits for
+// the widening of its weights; how the rest divides was not measured.  The ring is
+// sized for the planes' places, not for what they hold: 32 planes with 4 to 32 rows
+// each, 4096 x 2048, take 64 us in planes of 1024 places and 54 us in planes of 32.
 #include "kernels.h"
 #include "pair.cuh"
 #include "ring.h"

@@ -32,9 +32,9 @@
 //   warps 8-15, 8-bit formats: two groups of four in turn widen a stage's
 //     weight rows to bf16 into tensor memory (exact), which the products read
 //     as their A operand.
-// Bounds.  8 tokens, hidden 7168, inter 2048, 64 experts, top-8, int8: 288-296
-// us for 1.85 GB, 92-95 % of the copy rate; 64 tokens, hidden 2048, inter 1024,
-// bf16: 141 us for 0.81 GB (118 us).  One token, hidden 2048, inter 768: 23 us
+// Bounds.  8 tokens, hidden 7168, inter 2048, 64 experts, top-8, int8: 286-306
+// us for 1.85 GB, 89-95 % of the copy rate; 64 tokens, hidden 2048, inter 1024,
+// bf16: 142 us for 0.81 GB (118 us).  One token, hidden 2048, inter 768: 23 us
 // for 75 MB (11 us); 5 us are the launch, the lists and the last exchange, and
 // about 6 the way through the two phases (first weights, activations visible to
 // all CTAs, outputs visible to all).

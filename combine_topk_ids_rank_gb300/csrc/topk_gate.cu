@@ -20,10 +20,14 @@
 // lane sorts its values once (a network of 2-instruction exchanges) and a round
 // only shifts the winner's list.  Otherwise fp32 keys fill the word; the winner
 // lane clears the first value equal to the maximum and looks for its next.
-// Bound by instruction issue (66 % of the slots busy for bf16).  32768 tokens x
-// 256 logits, top-8: bf16 10.3 us (its 18.9 MB would take 2.8 us; scalar loads
-// and unsorted keys took 29 us, one token a warp 13.5 us), fp32 14.5 us (its
-// 35.7 MB would take 5.3 us; unsorted whole keys took 27.7 us).
+// 32768 tokens x 256 logits, top-8: bf16 10.4 us (its 18.9 MB would take 2.8 us;
+// scalar loads and unsorted keys took 29 us, one token a warp 13.5 us), fp32 15.4 us
+// from memory, 14.3 us from L2 (its 35.7 MB would take 5.3 us; unsorted whole keys
+// took 27.7 us).  fp32 logits that were bf16 before take 19.6 us: a token whose last
+// selected logit equals the next one is selected twice, and they have many such.
+// The bf16 kernel issues 241 instructions a token, 13 thousand cycles of a scheduler,
+// in 62 % of its slots.  The rest is latency: the rounds of a token are one chain of
+// dependent reductions, and a warp's tokens go through it one after another.
 #include "kernels.h"
 #include "layer.h"
 #include "ptx.cuh"
@@ -277,8 +281,7 @@ __global__ void __launch_bounds__(kThreads) topk_gate_kernel(const TopkGateParam
 // agree to 2^-15 in the wrong order.  So the selected logits are read again
 // (their weights need them) and compared; a token that has two of them in the
 // wrong order, or the last of them no further than 2^-15 from the next one, is
-// selected anew on whole keys.  About 160 instructions a bf16 token, which is the
-// bound beside 540 bytes of traffic.
+// selected anew on whole keys.
 constexpr int kTokens = 4;
 // Tokens an SM, up to which a warp takes one: 8 tokens of 256 fp32 logits take
 // 2.3 us with one a warp and 3.4 us with four, 2048 3.2 and 4.7 us, 4864 (32 an
