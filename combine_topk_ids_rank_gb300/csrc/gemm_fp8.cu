@@ -1,0 +1,27 @@
+// gemm_fp8.cu -- product of e4m3 codes with a scale for each block of 128
+// codes of a token and one for each 128 x 128 block of the weights, dense,
+// grouped over the experts' planes, or over rows that stand one group after
+// another (pair_product.cuh).
+//
+// Operation, group g, token row m, channel n:
+//   out[m][n] = bf16_rn( sum over blocks b of RN32(sx[m][b] * sw[g][n / 128][b]) * d_b ),
+//   d_b = sum over h in block b of xq[m][h] * wq[g][n][h],
+// the products of codes exact, the sums in fp32 (d_b as the tensor cores add,
+// the outer sum by fused multiply-adds in ascending b).
+#include "pair_product.cuh"
+
+namespace moe {
+
+cudaError_t launch_gemm_fp8(ProductParams p, const void *xq, const void *wq, int num_sms,
+                            cudaStream_t st) {
+    using namespace product;
+    CUtensorMap a, b, b8;
+    const long long rows = p.offsets != nullptr ? p.M : (long long)p.G * p.M;
+    if (!map_3d(&a, wq, p.G, p.lanes, p.depth, kAtom, kTileRows, true) ||
+        !map_2d(&b, xq, rows, p.depth, kAtom, kBigBox, true) ||
+        !map_2d(&b8, xq, rows, p.depth, kAtom, kSmallBox, true))
+        return cudaErrorInvalidValue;
+    return launch<kFp8>(p, a, b, b8, num_sms, st);
+}
+
+}  // namespace moe

@@ -1,5 +1,6 @@
 // moe_ops.cpp -- C entry points of the operators around dispatch and combine
 // (include/moe_a2a.h): argument checks on the host, then one launch.
+#include "entry.h"
 #include "layer.h"
 
 #include "moe_a2a.h"
@@ -9,31 +10,6 @@
 namespace {
 
 using namespace moe;
-
-bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-
-// A CUDA call failed: clear the runtime's last error, so that the caller's
-// next CUDA call does not report it again.
-int cuda_failed() {
-    (void)cudaGetLastError();
-    return MOE_ERR_CUDA;
-}
-
-bool sm_count(int *sms) {
-    int dev = 0;
-    return cudaGetDevice(&dev) == cudaSuccess &&
-           cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
-}
-
-// A launcher's result as a status; nothing is thrown through the C entries.
-template <typename Launch>
-int launched(Launch &&launch) {
-    try {
-        return launch() == cudaSuccess ? MOE_OK : cuda_failed();
-    } catch (...) {
-        return cuda_failed();
-    }
-}
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 

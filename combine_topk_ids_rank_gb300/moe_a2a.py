@@ -42,7 +42,9 @@ EXPORTS = ("moe_a2a_workspace_bytes", "moe_a2a_create", "moe_dispatch",
            "moe_expert_gemm_rank", "moe_expert_gemm_rank_fp8", "moe_topk_gate",
            "moe_quantize_rows_int8", "moe_gemm_int8_scratch_bytes", "moe_gemm_int8",
            "moe_layer_small_scratch_bytes", "moe_layer_small", "moe_scratch_init",
-           "moe_scratch_get_error")
+           "moe_scratch_get_error", "moe_quantize_blocks_fp8", "moe_gemm_fp8_scratch_bytes",
+           "moe_gemm_fp8", "moe_gemm_ragged_scratch_bytes", "moe_gemm_ragged",
+           "moe_gemm_ragged_input_grad", "moe_gemm_ragged_weight_grad")
 MOE_REDUCE_FP32_RANK_ORDER = 0
 MOE_REDUCE_BF16_TOPK_TREE = 1
 MOE_STATIC_SCRATCH_BYTES = 4 << 20
@@ -52,6 +54,7 @@ MOE_FORMAT_INT8 = 2
 MOE_SCORE_SOFTMAX = 0
 MOE_SCORE_SIGMOID = 1
 MOE_LAYER_MAX_TOKENS = 64
+MOE_SCALE_BLOCK = 128  # codes, and output channels, that share a scale of moe_gemm_fp8
 MOE_LAYOUT_RANK = 0
 MOE_LAYOUT_EXPERT = 1
 
@@ -150,6 +153,19 @@ def _load(path: str = LIBRARY):
     lib.moe_scratch_init.restype = ctypes.c_int
     lib.moe_scratch_get_error.argtypes = [p, p, ctypes.POINTER(ctypes.c_uint32)]
     lib.moe_scratch_get_error.restype = ctypes.c_int
+    lib.moe_quantize_blocks_fp8.argtypes = [p, i32, i32, i32, i32, i64, i32, p, p, p, p]
+    lib.moe_quantize_blocks_fp8.restype = ctypes.c_int
+    lib.moe_gemm_fp8_scratch_bytes.argtypes = [i32]
+    lib.moe_gemm_fp8_scratch_bytes.restype = sz
+    lib.moe_gemm_fp8.argtypes = [p] * 6 + [i32] * 4 + [p, p, sz, p]
+    lib.moe_gemm_fp8.restype = ctypes.c_int
+    lib.moe_gemm_ragged_scratch_bytes.argtypes = []
+    lib.moe_gemm_ragged_scratch_bytes.restype = sz
+    for f in (lib.moe_gemm_ragged, lib.moe_gemm_ragged_input_grad):
+        f.argtypes = [p] * 3 + [i32] * 4 + [p, p, sz, p]
+        f.restype = ctypes.c_int
+    lib.moe_gemm_ragged_weight_grad.argtypes = [p] * 3 + [i32] * 6 + [p, p, sz, p]
+    lib.moe_gemm_ragged_weight_grad.restype = ctypes.c_int
     lib.moe_a2a_status_string.argtypes = [ctypes.c_int]
     lib.moe_a2a_status_string.restype = ctypes.c_char_p
     return lib
@@ -391,6 +407,50 @@ def moe_scratch_get_error(d_scratch: int, stream: int = 0):
     return st, int(flags.value)
 
 
+def moe_quantize_blocks_fp8(d_x: int, bf16: bool, groups: int, rows: int, hidden: int,
+                            row_stride: int, block_rows: int, d_counts: int, d_q: int,
+                            d_scale: int, stream: int = 0) -> int:
+    return _lib.moe_quantize_blocks_fp8(d_x, int(bf16), groups, rows, hidden, row_stride,
+                                        block_rows, d_counts, d_q, d_scale, stream)
+
+
+def moe_gemm_fp8_scratch_bytes(rows: int) -> int:
+    return int(_lib.moe_gemm_fp8_scratch_bytes(rows))
+
+
+def moe_gemm_fp8(d_xq: int, d_x_scale: int, d_wq: int, d_w_scale: int, d_counts: int,
+                 d_offsets: int, groups: int, rows: int, N: int, hidden: int, d_out: int,
+                 d_scratch: int, scratch_bytes: int, stream: int = 0) -> int:
+    return _lib.moe_gemm_fp8(d_xq, d_x_scale, d_wq, d_w_scale, d_counts, d_offsets, groups, rows,
+                             N, hidden, d_out, d_scratch, scratch_bytes, stream)
+
+
+def moe_gemm_ragged_scratch_bytes() -> int:
+    return int(_lib.moe_gemm_ragged_scratch_bytes())
+
+
+def moe_gemm_ragged(d_x: int, d_w: int, d_offsets: int, groups: int, rows: int, N: int,
+                    hidden: int, d_out: int, d_scratch: int, scratch_bytes: int,
+                    stream: int = 0) -> int:
+    return _lib.moe_gemm_ragged(d_x, d_w, d_offsets, groups, rows, N, hidden, d_out, d_scratch,
+                                scratch_bytes, stream)
+
+
+def moe_gemm_ragged_input_grad(d_dy: int, d_w: int, d_offsets: int, groups: int, rows: int,
+                               N: int, hidden: int, d_dx: int, d_scratch: int,
+                               scratch_bytes: int, stream: int = 0) -> int:
+    return _lib.moe_gemm_ragged_input_grad(d_dy, d_w, d_offsets, groups, rows, N, hidden, d_dx,
+                                           d_scratch, scratch_bytes, stream)
+
+
+def moe_gemm_ragged_weight_grad(d_dy: int, d_x: int, d_offsets: int, groups: int, rows: int,
+                                N: int, hidden: int, fp32: bool, accumulate: bool, d_dw: int,
+                                d_scratch: int, scratch_bytes: int, stream: int = 0) -> int:
+    return _lib.moe_gemm_ragged_weight_grad(d_dy, d_x, d_offsets, groups, rows, N, hidden,
+                                            int(fp32), int(accumulate), d_dw, d_scratch,
+                                            scratch_bytes, stream)
+
+
 # ---- torch forms of the operators around dispatch and combine ------------------
 
 def _on_current(device):
@@ -595,6 +655,200 @@ class MoeGemmInt8(_Scratch):
                                 self._scratch_ptr, self._scratch_bytes, raw)
         if st != MOE_OK:
             raise MoeA2AError(st, "moe_gemm_int8")
+        return out
+
+
+def _e4m3(t, name):
+    """e4m3 codes as torch has them, or as bytes."""
+    if t.dtype is not _torch.float8_e4m3fn and t.dtype is not _torch.uint8:
+        raise ValueError("%s: expected e4m3 codes, got %s" % (name, t.dtype))
+    return t.dtype
+
+
+def _blocks(n: int) -> int:
+    return (n + MOE_SCALE_BLOCK - 1) // MOE_SCALE_BLOCK
+
+
+def quantize_blocks_fp8(x, block_rows: int = 1, counts=None, out=None, scale=None, stream=None):
+    """fp32 or bf16 [..., H] CUDA tensor -> (float8_e4m3fn [..., H], float32
+    scales [..., ceil(H / 128)]): one scale for 128 values of a row, or, with
+    block_rows = 128, for 128 values of 128 rows (x [..., rows, H], scales
+    [..., ceil(rows / 128), ceil(H / 128)]).  With counts (int32 [G] on the
+    device, block_rows = 1) x is [G, rows, H] and rows past a plane's count are
+    left alone.  2-D x may have any row stride that is a multiple of 16 bytes."""
+    dtype, device = x.dtype, x.device
+    bf16 = dtype is _torch.bfloat16
+    tiles = block_rows != 1
+    if not x.is_cuda or not (bf16 or dtype is _torch.float32) or x.dim() < 1 + tiles:
+        raise ValueError("x must be a float32 or bfloat16 CUDA tensor [..., H]")
+    if block_rows not in (1, MOE_SCALE_BLOCK):
+        raise ValueError("block_rows must be 1 or %d" % MOE_SCALE_BLOCK)
+    shape = x.shape
+    *lead, H = shape
+    row_stride = H
+    if not x.is_contiguous():
+        if x.dim() != 2 or x.stride(1) != 1 or x.stride(0) < H:
+            raise ValueError("x must be contiguous, or 2-D with dense rows")
+        row_stride = x.stride(0)
+    n = x.numel()
+    groups, rows = 1, n // H if H else 0
+    if tiles:
+        rows = lead[-1]
+        groups = n // (rows * H) if n else 0
+        lead = (*lead[:-1], _blocks(rows))
+    if counts is not None:
+        if x.dim() != 3 or tiles:
+            raise ValueError("with counts x must be [groups, rows, hidden], block_rows 1")
+        groups, rows = lead
+        _expect(counts, _torch.int32, (groups,), device, "counts")
+    if rows > _INT32_MAX or groups > _INT32_MAX or H > _INT32_MAX:
+        raise MoeA2AError(MOE_ERR_INVALID_ARG, "moe_quantize_blocks_fp8")
+    raw = _raw_stream(stream, device)
+    if out is None:
+        out = _empty(shape, _torch.float8_e4m3fn, device, stream, raw)
+    else:
+        _expect(out, _e4m3(out, "out"), shape, device, "out")
+    scales = (*lead, _blocks(H))
+    if scale is None:
+        scale = _empty(scales, _torch.float32, device, stream, raw)
+    else:
+        _expect(scale, _torch.float32, scales, device, "scale")
+    st = _lib.moe_quantize_blocks_fp8(x.data_ptr(), bf16, groups, rows, H, row_stride, block_rows,
+                                      0 if counts is None else counts.data_ptr(), out.data_ptr(),
+                                      scale.data_ptr(), raw)
+    if st != MOE_OK:
+        raise MoeA2AError(st, "moe_quantize_blocks_fp8")
+    return out, scale
+
+
+class MoeGemmFp8(_Scratch):
+    """The 8-bit floating-point product with block scales over `groups` weight
+    matrices, with the scratch memory it needs.  One call at a time: calls in
+    stream order."""
+
+    def __init__(self, groups: int, max_rows: int, N: int, hidden: int, device=None):
+        self.groups, self.max_rows, self.N, self.hidden = groups, max_rows, N, hidden
+        if max(groups, max_rows, N, hidden) > _INT32_MAX:
+            raise MoeA2AError(MOE_ERR_INVALID_ARG, "moe_gemm_fp8")
+        super().__init__(moe_gemm_fp8_scratch_bytes(max_rows), device,
+                         "moe_gemm_fp8_scratch_bytes")
+
+    def gemm(self, xq, x_scale, wq, w_scale, counts=None, offsets=None, out=None, stream=None):
+        """xq e4m3 [G, rows, H], x_scale float32 [G, rows, ceil(H / 128)], wq
+        e4m3 [G, N, H], w_scale float32 [G, ceil(N / 128), ceil(H / 128)],
+        counts int32 [G] on the device or None (all rows) -> out bf16 [G, rows,
+        N], rows past a count untouched (undefined in a new tensor).  With
+        offsets (int32 [G + 1] on the device) the rows stand one group after
+        another: xq [rows, H], x_scale [rows, ..], out [rows, N], rows of no
+        group untouched.  With one group the leading extent may be left out."""
+        G, N, H, dev = self.groups, self.N, self.hidden, self.device
+        wide = xq.dim()
+        lead = (G,) if wide == 3 or (G != 1 and offsets is None) else ()
+        wlead = (G,) if wq.dim() == 3 or G != 1 else ()
+        rows = xq.shape[-2] if wide >= 2 else 0
+        KB = _blocks(H)
+        if offsets is not None:
+            if counts is not None:
+                raise ValueError("counts or offsets, not both")
+            lead = ()
+            _expect(offsets, _torch.int32, (G + 1,), dev, "offsets")
+        elif counts is not None:
+            _expect(counts, _torch.int32, (G,), dev, "counts")
+        _expect(xq, _e4m3(xq, "xq"), (*lead, rows, H), dev, "xq")
+        _expect(x_scale, _torch.float32, (*lead, rows, KB), dev, "x_scale")
+        _expect(wq, _e4m3(wq, "wq"), (*wlead, N, H), dev, "wq")
+        _expect(w_scale, _torch.float32, (*wlead, _blocks(N), KB), dev, "w_scale")
+        if rows > self.max_rows:
+            raise MoeA2AError(MOE_ERR_CAPACITY, "moe_gemm_fp8")
+        raw = self._launch_stream(stream)
+        if out is None:
+            out = _empty((*lead, rows, N), _torch.bfloat16, dev, stream, raw)
+        else:
+            _expect(out, _torch.bfloat16, (*lead, rows, N), dev, "out")
+        st = _lib.moe_gemm_fp8(xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(),
+                               w_scale.data_ptr(), _ptr(counts), _ptr(offsets), G, rows, N, H,
+                               out.data_ptr(), self._scratch_ptr, self._scratch_bytes, raw)
+        if st != MOE_OK:
+            raise MoeA2AError(st, "moe_gemm_fp8")
+        return out
+
+
+class MoeGemmRagged(_Scratch):
+    """One linear map per expert (bf16 [G, N, H]) over rows that stand one
+    expert after another, and its gradients, with the scratch memory they need.
+    offsets: int32 [G + 1] on the device, expert e has rows offsets[e] to
+    offsets[e + 1]; rows of no expert are left alone (undefined in a new
+    tensor).  One call at a time: calls in stream order."""
+
+    def __init__(self, groups: int, max_rows: int, N: int, hidden: int, device=None):
+        self.groups, self.max_rows, self.N, self.hidden = groups, max_rows, N, hidden
+        if max(groups, max_rows, N, hidden) > _INT32_MAX or max_rows < 1:
+            raise MoeA2AError(MOE_ERR_INVALID_ARG, "moe_gemm_ragged")
+        super().__init__(moe_gemm_ragged_scratch_bytes(), device, "moe_gemm_ragged_scratch_bytes")
+
+    def _rows(self, t, cols, name, offsets, where):
+        rows = t.shape[0] if t.dim() == 2 else 0
+        _expect(t, _torch.bfloat16, (rows, cols), self.device, name)
+        _expect(offsets, _torch.int32, (self.groups + 1,), self.device, "offsets")
+        if rows > self.max_rows:
+            raise MoeA2AError(MOE_ERR_CAPACITY, where)
+        return rows
+
+    def _run(self, call, a, b, offsets, rows, cols, out, where, stream):
+        """A product whose output has a row for each row of `a`."""
+        raw = self._launch_stream(stream)
+        if out is None:
+            out = _empty((rows, cols), _torch.bfloat16, self.device, stream, raw)
+        else:
+            _expect(out, _torch.bfloat16, (rows, cols), self.device, "out")
+        st = call(a.data_ptr(), b.data_ptr(), offsets.data_ptr(), self.groups, rows, self.N,
+                  self.hidden, out.data_ptr(), self._scratch_ptr, self._scratch_bytes, raw)
+        if st != MOE_OK:
+            raise MoeA2AError(st, where)
+        return out
+
+    def forward(self, x, w, offsets, out=None, stream=None):
+        """x bf16 [rows, H], w bf16 [G, N, H] -> out bf16 [rows, N]."""
+        G, N, H = self.groups, self.N, self.hidden
+        rows = self._rows(x, H, "x", offsets, "moe_gemm_ragged")
+        _expect(w, _torch.bfloat16, (G, N, H), self.device, "w")
+        return self._run(_lib.moe_gemm_ragged, x, w, offsets, rows, N, out, "moe_gemm_ragged",
+                         stream)
+
+    def input_grad(self, dy, w, offsets, out=None, stream=None):
+        """dy bf16 [rows, N], w bf16 [G, N, H] -> dx bf16 [rows, H].  N a
+        multiple of 8."""
+        G, N, H = self.groups, self.N, self.hidden
+        rows = self._rows(dy, N, "dy", offsets, "moe_gemm_ragged_input_grad")
+        _expect(w, _torch.bfloat16, (G, N, H), self.device, "w")
+        return self._run(_lib.moe_gemm_ragged_input_grad, dy, w, offsets, rows, H, out,
+                         "moe_gemm_ragged_input_grad", stream)
+
+    def weight_grad(self, dy, x, offsets, out=None, dtype=None, accumulate=False, stream=None):
+        """dy bf16 [rows, N], x bf16 [rows, H] -> dw [G, N, H], bf16 (or
+        dtype = float32; with `out` its type), zero for an expert without rows.
+        accumulate: added to a float32 `out`.  N a multiple of 8."""
+        G, N, H, dev = self.groups, self.N, self.hidden, self.device
+        where = "moe_gemm_ragged_weight_grad"
+        rows = self._rows(dy, N, "dy", offsets, where)
+        _expect(x, _torch.bfloat16, (rows, H), dev, "x")
+        if dtype is None:
+            dtype = _torch.bfloat16 if out is None else out.dtype
+        if dtype is not _torch.bfloat16 and dtype is not _torch.float32:
+            raise ValueError("the weights' gradient is bfloat16 or float32, not %s" % dtype)
+        if accumulate and (out is None or dtype is not _torch.float32):
+            raise ValueError("accumulate needs a float32 out")
+        raw = self._launch_stream(stream)
+        if out is None:
+            out = _empty((G, N, H), dtype, dev, stream, raw)
+        else:
+            _expect(out, dtype, (G, N, H), dev, "out")
+        st = _lib.moe_gemm_ragged_weight_grad(
+            dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), G, rows, N, H,
+            dtype is _torch.float32, bool(accumulate), out.data_ptr(), self._scratch_ptr,
+            self._scratch_bytes, raw)
+        if st != MOE_OK:
+            raise MoeA2AError(st, where)
         return out
 
 

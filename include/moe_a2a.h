@@ -572,7 +572,89 @@ int moe_layer_small(const void *d_x, const int32_t *d_topk_ids, const float *d_t
                     int32_t format, void *d_out, void *d_scratch, size_t scratch_bytes,
                     void *stream);
 
-/* Prepare a scratch buffer of moe_gemm_int8 or moe_layer_small for its first
+/* ---- 8-bit floating-point product with block scales ---------------------------
+ * Rows to e4m3 codes with one scale for each block of block_rows x 128 values
+ * (1 x 128: activations; 128 x 128: weights; the last blocks are what is left):
+ *   scale = max(amax |x| / 448, 2^-126) in binary32 (1 for an all-zero block),
+ *   q     = e4m3(x / scale), binary32 quotient, to nearest, ties to even,
+ *           saturating at 448.  A block with a NaN or an infinity gets scale
+ *           NaN and zero codes.
+ *   d_x     fp32 or bf16, `groups` planes of `rows` rows, row r of plane g at
+ *           (g * rows + r) * row_stride; 16-byte aligned, row_stride a
+ *           multiple of 16 bytes
+ *   hidden  a multiple of 16
+ *   d_counts int32 [groups] or NULL (block_rows = 1 only): rows j >= d_counts[g]
+ *           of plane g are neither read nor written
+ *   d_q     e4m3 [groups][rows][hidden], 16-byte aligned
+ *   d_scale fp32 [groups][ceil(rows / block_rows)][ceil(hidden / 128)]
+ * Queues one kernel on `stream`; no handle. */
+int moe_quantize_blocks_fp8(const void *d_x, int32_t bf16, int32_t groups, int32_t rows,
+                            int32_t hidden, int64_t row_stride, int32_t block_rows,
+                            const int32_t *d_counts, void *d_q, float *d_scale, void *stream);
+
+/* Product of such codes, for group g, token row m and channel n:
+ *   out[m][n] = bf16_rn( sum over blocks b of RN32(sx[m][b] * sw[g][n / 128][b]) * d_b ),
+ *   d_b = sum over h in block b of xq[m][h] * wq[g][n][h],
+ * fp32 sums (d_b as the tensor cores add, the outer sum by fused multiply-adds
+ * in ascending b).
+ * Token rows: planes, d_offsets NULL: [groups][rows], rows m >= d_counts[g]
+ * of plane g are not written (d_counts NULL: all rows are used; counts are
+ * clamped to 0..rows); or one group after another, d_offsets int32
+ * [groups + 1], ascending: group g has rows d_offsets[g] <= m < d_offsets[g+1]
+ * of `rows`, and rows of no group are not written (offsets are clamped to
+ * 0..rows; those of a group that would begin past its end are none).  Not both.
+ *   d_xq e4m3 [..rows][hidden], d_x_scale fp32 [..rows][ceil(hidden / 128)]
+ *   d_wq e4m3 [groups][N][hidden],
+ *   d_w_scale fp32 [groups][ceil(N / 128)][ceil(hidden / 128)]
+ *   hidden  a multiple of 16; N and rows any; groups <= 1024; hidden, all rows,
+ *           groups * N, groups * hidden < 2^31 - 2^24
+ *   d_out   bf16 [..rows][N]
+ *   d_scratch at least moe_gemm_fp8_scratch_bytes(rows) bytes, as for
+ *           moe_gemm_int8
+ * d_xq and d_wq 16-byte aligned.  Queues one kernel on `stream`. */
+size_t moe_gemm_fp8_scratch_bytes(int32_t rows);
+
+int moe_gemm_fp8(const void *d_xq, const float *d_x_scale, const void *d_wq,
+                 const float *d_w_scale, const int32_t *d_counts, const int32_t *d_offsets,
+                 int32_t groups, int32_t rows, int32_t N, int32_t hidden, void *d_out,
+                 void *d_scratch, size_t scratch_bytes, void *stream);
+
+/* ---- One linear map per expert over ragged rows, and its gradients ------------
+ * Rows stand one expert after another: expert e has rows d_offsets[e] <= m <
+ * d_offsets[e + 1] of `rows` (int32 [groups + 1] as for moe_gemm_fp8), maps
+ * W_e are [N][hidden]:
+ *   moe_gemm_ragged:             y[m][n]    = bf16_rn( sum_h x[m][h] * W_e[n][h] )
+ *   moe_gemm_ragged_input_grad:  dx[m][h]   = bf16_rn( sum_n dy[m][n] * W_e[n][h] )
+ *   moe_gemm_ragged_weight_grad: dW_e[n][h] = sum_m dy[m][n] * x[m][h],
+ *                                bf16 (fp32 = 0) or fp32, or (accumulate, fp32
+ *                                only) added to what d_dw holds
+ * bf16 operands, fp32 sums.  Rows of no expert are not written (and take no
+ * part in dW); the dW of an expert without rows is zero.
+ *   hidden  a multiple of 8; N any, a multiple of 8 for the gradients;
+ *           groups <= 1024; limits as for moe_gemm_fp8 (weight gradient:
+ *           groups * hidden and the tiles of 256 x 256 of all maps < 2^30)
+ *   d_x bf16 [rows][hidden], d_dy bf16 [rows][N], d_w bf16 [groups][N][hidden]:
+ *           16-byte aligned; d_out, d_dx bf16; d_dw 16-byte aligned.  Outputs
+ *           overlap no input.
+ *   d_scratch at least moe_gemm_ragged_scratch_bytes() bytes, as for
+ *           moe_gemm_int8
+ * Each queues one kernel on `stream` (the weight gradient of no rows a memset). */
+size_t moe_gemm_ragged_scratch_bytes(void);
+
+int moe_gemm_ragged(const void *d_x, const void *d_w, const int32_t *d_offsets, int32_t groups,
+                    int32_t rows, int32_t N, int32_t hidden, void *d_out, void *d_scratch,
+                    size_t scratch_bytes, void *stream);
+
+int moe_gemm_ragged_input_grad(const void *d_dy, const void *d_w, const int32_t *d_offsets,
+                               int32_t groups, int32_t rows, int32_t N, int32_t hidden,
+                               void *d_dx, void *d_scratch, size_t scratch_bytes, void *stream);
+
+int moe_gemm_ragged_weight_grad(const void *d_dy, const void *d_x, const int32_t *d_offsets,
+                                int32_t groups, int32_t rows, int32_t N, int32_t hidden,
+                                int32_t fp32, int32_t accumulate, void *d_dw, void *d_scratch,
+                                size_t scratch_bytes, void *stream);
+
+/* Prepare a scratch buffer of a product above or of moe_layer_small for its first
  * call (queues one memset); every call leaves it prepared for the next. */
 int moe_scratch_init(void *d_scratch, size_t scratch_bytes, void *stream);
 
