@@ -59,9 +59,9 @@ enum Op { kFp8, kForward, kInputGrad, kWeightGrad };
 
 constexpr int kEpiWarps = 8, kProducerWarp = 8, kMmaWarp = 9, kHelpWarp = 10;
 constexpr int kThreads = 12 * 32;
-// Registers: 384 threads start with 168 each (64512); the epilogue's 256 go to 216, the
-// other 128 to 72, which is 64512 again.
-constexpr int kStartRegs = 168, kEpiRegs = 216, kOtherRegs = 72;
+// Registers: 384 threads start with 168 each (64512); the epilogue's 256 go to 208, the
+// other 128 to 88, which is 64512 again.
+constexpr int kStartRegs = 168, kEpiRegs = 208, kOtherRegs = 88;
 static_assert(kEpiWarps * 32 * kEpiRegs + (kThreads - kEpiWarps * 32) * kOtherRegs <=
                   kThreads * kStartRegs, "more registers than the block starts with");
 constexpr int kPairLanes = 2 * kTileRows;
@@ -89,11 +89,17 @@ __device__ __forceinline__ int width_of(int cols) {
 // `parts` pairs from p0 on; pair c keeps its part in slot 0 unless it is p0.
 struct Seg {
     int g, l, c0, cols, k0, k1;
+    bool turned;  // tokens are the lanes
     int p0, parts, slot0;
     __device__ bool whole() const { return parts == 1; }
     __device__ int slot(int c) const { return c == p0 ? slot0 : 0; }
 };
 
+// Turned tiles (kFp8).  A group with many tokens has them as the lanes and 256
+// channels as the columns: a lane then has one scale for a block and 128 columns,
+// in a register, where tokens as columns need one read of shared memory for four
+// products.  (There are as many tiles either way.)
+//
 // The work of a call, in shared memory (the roles keep few registers of it).
 // Tiles: groups in `order`; in a group, blocks of kRowGroup lane tiles, column
 // tile outer and lane tile inner.  `waves` tiles of each pair are whole; the
@@ -104,8 +110,12 @@ struct Plan {
     int start[kProductMaxGroups];       // its first row
     uint16_t order[kProductMaxGroups];
     int hist[kClasses];
+    int turn_from;                      // tokens that make a group's tiles turned
     int waves, rest, share, blocks;     // share: pairs for each of the rest (kWeightGrad)
     int parts, grain, q, more;          // the cut of the rest (tokens as columns)
+
+    // Columns of the tiles of a group of `c` tokens.
+    __device__ int width(int c) const { return c >= turn_from ? kMaxCols : width_of(c); }
 
     template <bool KRAGGED>
     __device__ void tile(int t, const ProductParams &p, Seg &s) const {
@@ -117,7 +127,8 @@ struct Plan {
         s.g = order[lo];
         const int ltiles = (p.lanes + kPairLanes - 1) / kPairLanes;
         const int c = KRAGGED ? p.cols : count[s.g], k = tiles_of(c), u = t - first[lo];
-        const int w = width_of(c), block = u / (kRowGroup * k);
+        const int w = KRAGGED ? width_of(c) : width(c), block = u / (kRowGroup * k);
+        s.turned = !KRAGGED && c >= turn_from;
         const int in = min(kRowGroup, ltiles - block * kRowGroup);
         const int v = u - block * kRowGroup * k;
         const int m = v / in;
@@ -249,6 +260,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!B_MN) tc::prefetch_map(&map_b8);
     }
     if (tid < kClasses) plan.hist[tid] = 0;
+    // (a turned tile's rows are stored 8 channels at a time)
+    if (tid == 0)
+        plan.turn_from = OP == kFp8 && p.lanes % 8 == 0 &&
+                                 reinterpret_cast<uintptr_t>(p.out) % 16 == 0
+                             ? kProductTurnFrom : INT32_MAX;
     ptx::grid_dependency_wait();  // nothing of the caller's memory is touched before
     for (int g = tid; g < p.G; g += kThreads) {
         int at = 0, c = p.M;
@@ -271,7 +287,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // groups by the work of a tile, stable: its columns, or (to a half power of two)
     // its blocks of k
     const auto class_of = [&](int g) {
-        if (!KRAGGED) return width_of(plan.count[g]) / 16;
+        if (!KRAGGED) return plan.width(plan.count[g]) / 16;
         const int b = (plan.count[g] + 63) / 64;
         if (b < 2) return b;
         const int e = 31 - __clz(b);
@@ -318,7 +334,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (KRAGGED) {
         widest = width_of(p.cols);
     } else if (p.G == 1) {
-        widest = max(16, width_of(plan.count[0]));
+        widest = max(16, plan.width(plan.count[0]));
     } else {
         for (int w = 2; w <= kMaxCols / 16; ++w)
             if (plan.hist[w] != 0) widest = 16 * w;
@@ -368,7 +384,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const int half = (sg.cols + 15) / 16 * 8;  // columns of this CTA
                     const int a0 = sg.l * kPairLanes + rank * kTileRows, b0 = sg.c0 + rank * half;
                     const int at = plan.start[sg.g];
-                    const uint32_t bytes = kLaneBytes + half_bytes_of<OP>(2 * half);
+                    // bytes of this CTA and of the pair; turned: boxes of 64 tokens
+                    uint32_t bytes = kLaneBytes + half_bytes_of<OP>(2 * half);
+                    uint32_t both = 2 * bytes;
+                    if (OP == kFp8 && sg.turned)
+                        both = 2 * kLaneBytes + (sg.cols + 63) / 64 * kPanelBytes;
                     for (int kb = sg.k0; kb < sg.k1; ++kb, st.next()) {
                         const int s = (int)st.at;
                         if (!ptx::mbar_park(&empty[s], st.parity ^ 1u, kWaitNs)) {
@@ -385,12 +405,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             tails |= 1u << s;
                             bar = ptx::cluster_smem(&tail[s], rank);
                         } else if (rank == 0) {
-                            ptx::mbar_arrive_expect_tx(&full[s], 2 * bytes);
+                            ptx::mbar_arrive_expect_tx(&full[s], both);
                             issued |= 1u << s;
                         } else if (KRAGGED) {
                             ptx::mbar_arrive_pair(bar);
                         }
                         uint8_t *a = a_of(s), *b = b_of(s);
+                        if (OP == kFp8 && sg.turned) {
+                            for (int c = rank * kTileRows; c < sg.cols && c < (rank + 1) * kTileRows;
+                                 c += kBigBox)
+                                tc::tma_load_2d_pair(a + c % kTileRows * kAtom, &map_b, kb * kBlock,
+                                                     at + sg.c0 + c, bar);
+                            tc::tma_load_3d_pair(b, &map_a, kb * kBlock, a0, sg.g, bar);
+                            continue;
+                        }
                         if constexpr (OP == kFp8 || OP == kForward) {
                             tc::tma_load_3d_pair(a, &map_a, kb * kBlock, a0, sg.g, bar);
                         } else if constexpr (OP == kInputGrad) {
@@ -433,7 +461,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // a step along k: 32 bytes, or 16 rows, in descriptor units of 16 bytes
                 constexpr uint64_t kStepA = A_MN ? 128 : 2, kStepB = B_MN ? 128 : 2;
                 while (!s_failed && work.next(p, sg)) {
-                    const int n = (sg.cols + 15) / 16 * 16;
+                    const int n = sg.turned ? kMaxCols : (sg.cols + 15) / 16 * 16;
                     const uint32_t idesc = (OP == kFp8 ? tc::idesc_e4m3_f32(kPairLanes, n)
                                                        : tc::idesc_bf16_f32(kPairLanes, n)) |
                                            kMajor;
@@ -476,37 +504,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         } else if (warp == kHelpWarp) {
             if constexpr (OP == kFp8) {
-                // Scales of a run of blocks: those of the tokens times the one of the CTA's
-                // 128 channels.
+                // Products of the tokens' scales and the channels', four blocks of k
+                // (a run) at a time: for each column, or, turned, for each lane and each
+                // half of the columns.
                 Turn sc(kScaleSlots);
                 const int KB = blocks, NB = (p.lanes + kScaleBlock - 1) / kScaleBlock;
+                const bool vec = KB % 4 == 0 && reinterpret_cast<uintptr_t>(p.x_scale) % 16 == 0;
                 bool ok = true;
                 while (ok && !warp_flag(&s_failed) && work.next(p, sg)) {
-                    const int nb = min(2 * sg.l + rank, NB - 1);
-                    const float *sw = p.w_scale + ((size_t)sg.g * NB + nb) * KB;
-                    const float *sx = p.x_scale + ((size_t)plan.start[sg.g] + sg.c0) * KB;
-                    const int n = (sg.cols + 15) / 16 * 16;
-                    for (int kb = sg.k0; kb < sg.k1; kb += kScaleRun, sc.next()) {
+                    const int nb = 2 * sg.l + (sg.turned ? 0 : rank);
+                    const float *sw = p.w_scale + ((size_t)sg.g * NB + min(nb, NB - 1)) * KB;
+                    const float *sw1 = nb + 1 < NB ? sw + KB : sw;
+                    const int first = sg.turned ? rank * kTileRows : 0;
+                    const float *sx = p.x_scale +
+                                      ((size_t)plan.start[sg.g] + sg.c0 + first + lane) * KB;
+                    // tokens from this lane's first one on
+                    const int left = min(sg.cols - first, sg.turned ? kTileRows : kMaxCols) - lane;
+                    for (int kb = sg.k0 & ~3; kb < sg.k1; kb += kScaleRun, sc.next()) {
+                        float x[kMaxCols / 32][kScaleRun], w[kScaleRun], w1[kScaleRun];
+#pragma unroll
+                        for (int j = 0; j < kMaxCols / 32; ++j) {
+                            const float *from = sx + (size_t)(32 * j) * KB + kb;
+#pragma unroll
+                            for (int i = 0; i < kScaleRun; ++i) x[j][i] = 0.0f;
+                            if (32 * j >= left) continue;
+                            if (vec) {
+                                const float4 f = __ldg(reinterpret_cast<const float4 *>(from));
+                                x[j][0] = f.x, x[j][1] = f.y, x[j][2] = f.z, x[j][3] = f.w;
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < kScaleRun; ++i)
+                                    if (kb + i < KB) x[j][i] = __ldg(from + i);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < kScaleRun; ++i) {
+                            w[i] = kb + i < KB ? __ldg(sw + kb + i) : 0.0f;
+                            w1[i] = sg.turned && kb + i < KB ? __ldg(sw1 + kb + i) : 0.0f;
+                        }
                         ok = __all_sync(0xffffffffu,
                                         ptx::mbar_park(&sc_free[sc.at], sc.parity ^ 1u, kWaitNs));
                         if (!ok) {
                             s_failed = 1;
                             break;
                         }
-                        float *to = s_scale + sc.at * kScaleRun * kMaxCols;
-                        float w[kScaleRun];
+                        float *to = s_scale + sc.at * kScaleRun * kMaxCols + lane;
 #pragma unroll
-                        for (int i = 0; i < kScaleRun; ++i)
-                            w[i] = kb + i < sg.k1 ? __ldg(sw + kb + i) : 0.0f;
-                        for (int c = lane; c < n; c += 32) {
-                            float x[kScaleRun];
+                        for (int j = 0; j < kMaxCols / 32; ++j) {
+                            if (j < kTileRows / 32 || !sg.turned) {
 #pragma unroll
-                            for (int i = 0; i < kScaleRun; ++i)
-                                x[i] = c < sg.cols && kb + i < sg.k1
-                                           ? __ldg(sx + (size_t)c * KB + kb + i) : 0.0f;
+                                for (int i = 0; i < kScaleRun; ++i)
+                                    to[i * kMaxCols + 32 * j] = __fmul_rn(x[j][i], w[i]);
+                            } else {
 #pragma unroll
-                            for (int i = 0; i < kScaleRun; ++i)
-                                to[i * kMaxCols + c] = __fmul_rn(x[i], w[i]);
+                                for (int i = 0; i < kScaleRun; ++i)
+                                    to[i * kMaxCols + 32 * j] =
+                                        __fmul_rn(x[j - kTileRows / 32][i], w1[i]);
+                            }
                         }
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&sc_full[sc.at]);
@@ -549,9 +603,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         Turn acc(2), sc(kScaleSlots);
         bool ok = true;
         while (ok && work.next(p, sg)) {
-            const int all = (sg.cols + kStep - 1) / kStep;
-            const int s0 = hf ? (all + 1) / 2 : 0, steps = hf ? all / 2 : (all + 1) / 2;
-            const int n0 = s0 * kStep;  // this warp's first column of the tile
+            int s0, steps;  // this warp's steps of kStep columns of the tile
+            if (OP == kFp8 && sg.turned) {  // channels that exist, if a token of the warp does
+                s0 = hf * kSteps;
+                const int chans = p.lanes - sg.l * kPairLanes - s0 * kStep;
+                steps = rank * kTileRows + q * 32 < sg.cols
+                            ? min(max((chans + kStep - 1) / kStep, 0), kSteps) : 0;
+            } else {
+                const int all = (sg.cols + kStep - 1) / kStep;
+                s0 = hf ? (all + 1) / 2 : 0;
+                steps = hf ? all / 2 : (all + 1) / 2;
+            }
+            const int n0 = s0 * kStep;
             x2::f2 sum[kSteps][kStep / 2];
 #pragma unroll
             for (int i = 0; i < kSteps; ++i)
@@ -559,44 +622,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < kStep / 2; ++j) sum[i][j] = 0ull;
             for (int kb = sg.k0; kb < sg.k1; acc.next()) {
                 ok = ptx::mbar_park(&acc_full[acc.at], acc.parity, kWaitNs);
-                const int run = (kb - sg.k0) % kScaleRun;
-                if (OP == kFp8 && run == 0)
+                const int run = kb % kScaleRun;
+                if (OP == kFp8 && (run == 0 || kb == sg.k0))
                     ok = ok && ptx::mbar_park(&sc_full[sc.at], sc.parity, kWaitNs);
-                ok = __all_sync(0xffffffffu, ok && !s_failed);
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) {
                     s_failed = 1;
                     break;
                 }
                 tc::fence_after_sync();
                 const uint32_t from = taddr + acc.at * kMaxCols + n0 + ((uint32_t)(q * 32) << 16);
-                const float *scale = s_scale + (sc.at * kScaleRun + run) * kMaxCols + n0;
+                const float *scale = s_scale + (sc.at * kScaleRun + run) * kMaxCols;
                 uint32_t u[2][kStep];
-                if (steps > 0) tc::ld_32x16(from, u[0]);
+                const auto pair_of = [](const uint32_t *v) {
+                    return x2::pack(__uint_as_float(v[0]), __uint_as_float(v[1]));
+                };
+                // (the loads of the next step are in flight)
+                const auto read = [&](auto &&take) {
+                    if (steps > 0) tc::ld_32x16(from, u[0]);
 #pragma unroll
-                for (int i = 0; i < kSteps; ++i) {
-                    if (i >= steps) break;
-                    tc::wait_ld(u[i & 1]);
-                    if (i + 1 < steps && i + 1 < kSteps)
-                        tc::ld_32x16(from + (i + 1) * kStep, u[(i + 1) & 1]);
-                    if constexpr (OP == kFp8) {
+                    for (int i = 0; i < kSteps; ++i) {
+                        if (i >= steps) break;
+                        tc::wait_ld(u[i & 1]);
+                        if (i + 1 < steps && i + 1 < kSteps)
+                            tc::ld_32x16(from + (i + 1) * kStep, u[(i + 1) & 1]);
+                        take(i, u[i & 1], sum[i]);
+                    }
+                };
+                if constexpr (OP == kFp8) {
+                    if (sg.turned) {
+                        const float f = scale[hf * kTileRows + row];
+                        const x2::f2 ff = x2::pack(f, f);
+                        read([&](int, const uint32_t (&v)[kStep], x2::f2 (&t)[kStep / 2]) {
 #pragma unroll
-                        for (int j = 0; j < kStep / 4; ++j) {
-                            const float4 f = *reinterpret_cast<const float4 *>(scale + i * kStep + 4 * j);
-                            const uint32_t *v = &u[i & 1][4 * j];
-                            sum[i][2 * j] =
-                                x2::fma(x2::pack(__uint_as_float(v[0]), __uint_as_float(v[1])),
-                                        x2::pack(f.x, f.y), sum[i][2 * j]);
-                            sum[i][2 * j + 1] =
-                                x2::fma(x2::pack(__uint_as_float(v[2]), __uint_as_float(v[3])),
-                                        x2::pack(f.z, f.w), sum[i][2 * j + 1]);
-                        }
+                            for (int j = 0; j < kStep / 2; ++j)
+                                t[j] = x2::fma(pair_of(&v[2 * j]), ff, t[j]);
+                        });
                     } else {
+                        read([&](int i, const uint32_t (&v)[kStep], x2::f2 (&t)[kStep / 2]) {
+                            const float4 *f = reinterpret_cast<const float4 *>(scale + n0 + i * kStep);
+#pragma unroll
+                            for (int j = 0; j < kStep / 4; ++j) {
+                                const float4 f4 = f[j];
+                                t[2 * j] = x2::fma(pair_of(&v[4 * j]), x2::pack(f4.x, f4.y), t[2 * j]);
+                                t[2 * j + 1] = x2::fma(pair_of(&v[4 * j + 2]), x2::pack(f4.z, f4.w),
+                                                       t[2 * j + 1]);
+                            }
+                        });
+                    }
+                } else {
+                    read([&](int, const uint32_t (&v)[kStep], x2::f2 (&t)[kStep / 2]) {
 #pragma unroll
                         for (int j = 0; j < kStep / 2; ++j)
-                            sum[i][j] = x2::add(sum[i][j],
-                                                x2::pack(__uint_as_float(u[i & 1][2 * j]),
-                                                         __uint_as_float(u[i & 1][2 * j + 1])));
-                    }
+                            t[j] = x2::add(t[j], pair_of(&v[2 * j]));
+                    });
                 }
                 tc::fence_before_sync();
                 __syncwarp();
@@ -628,7 +707,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 return *reinterpret_cast<const uint32_t *>(&o);
             };
             auto store = [&](int n, const x2::f2 (&v)[kStep / 2]) {
-                if constexpr (!KRAGGED) {
+                if (OP == kFp8 && sg.turned) {  // a token's row, 8 channels at a time
+                    const int tok = rank * kTileRows + row, at = sg.l * kPairLanes + n;
+                    if (tok >= sg.cols) return;
+                    uint16_t *o = out16 + (tok0 + tok) * p.lanes + at;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (at + 8 * h < p.lanes)
+                            reinterpret_cast<uint4 *>(o)[h] =
+                                make_uint4(pack_bf16(v[4 * h]), pack_bf16(v[4 * h + 1]),
+                                           pack_bf16(v[4 * h + 2]), pack_bf16(v[4 * h + 3]));
+                } else if constexpr (!KRAGGED) {
                     uint16_t *at = out + (size_t)(n + (lane & 1)) * p.lanes;
                     const int left = sg.cols - n - (lane & 1);
 #pragma unroll

@@ -50,11 +50,13 @@ struct ProductParams {
     int f32, accumulate;     // gradient of the maps: type, added to what is there
 };
 
-// Columns a part needs for M rows of tokens.
+// Columns a part needs for M rows of tokens (a group of kProductTurnFrom tokens may
+// have tiles of 256 channels).
+constexpr int kProductTurnFrom = 81;
 inline int product_nmax(int M) {
     int n = 16;
     while (n < M && n < kProductMaxCols) n *= 2;
-    return n;
+    return M >= kProductTurnFrom ? kProductMaxCols : n;
 }
 
 inline size_t product_part_bytes(int nmax) {

@@ -109,6 +109,22 @@ def test_quantize_extremes(api, dtype, b):
     check_quant(x, b, *api.quantize_blocks_fp8(x, b))
 
 
+def test_quantize_every_pair_of_bf16_significands(api):
+    """A block's largest value against every value below it down to 2^-23 of it (smaller
+    ones have code 0), maxima of 128 significands, with and without scaled quotients."""
+    small = torch.arange(128, 256, device=DEV).float()
+    below = (small * torch.exp2(-torch.arange(24, device=DEV).float())[:, None]).reshape(-1)
+    for power in (0, -100, 110):
+        for m in range(128, 256):
+            v = below[below <= m]
+            v = torch.nn.functional.pad(v, (0, -len(v) % 127)).view(-1, 127)
+            v = torch.cat([v, torch.full((len(v), 1), float(m), device=DEV)], 1)
+            v[:, ::2] *= -1
+            x = (v * 2.0 ** power).to(BF)
+            assert torch.equal(x.float(), v * 2.0 ** power)
+            check_quant(x, 1, *api.quantize_blocks_fp8(x))
+
+
 def test_quantize_planes_strides_and_buffers(api):
     g = gen(2)
     x = torch.randn((4, 37, 272), generator=g, device=DEV).to(BF)
@@ -159,7 +175,7 @@ def fp8_ref(xq, sx, wq, sw):
 
 
 SIZES = [(1, 1, 16), (1, 256, 128), (3, 130, 144), (16, 1000, 1040), (17, 129, 384), (64, 512, 512),
-         (100, 264, 2048), (255, 70, 640), (256, 256, 128), (257, 513, 272), (700, 300, 1024)]
+         (100, 264, 2048), (255, 70, 640), (80, 144, 256), (81, 144, 256), (256, 256, 128), (257, 513, 272), (700, 300, 1024)]
 
 
 @pytest.mark.parametrize("rows,N,H", SIZES)
