@@ -1,0 +1,1026 @@
+// expert_product.cuh -- the persistent product of the experts' maps that
+// gemm_fp8.cu and gemm_ragged.cu instantiate:
+//   D[lane][column] = sum_k A[lane][k] * B[column][k],
+// per group g, on the tensor cores (A is 128 tensor-memory lanes a CTA).
+//
+//   op          lanes              columns        k
+//   kFp8        output channels    tokens         hidden size, 8-bit codes with block scales
+//   kForward    output channels    tokens         hidden size
+//   kInputGrad  hidden size        tokens         output channels
+//   kWeightGrad output channels    hidden size    tokens
+//
+// Groups are ragged along the tokens: the columns of the first three (a tile is
+// as wide as its group needs, a multiple of 16, so that a group of few tokens
+// costs its weights and little else), k of the last one.
+//
+// bf16: pairs of CTAs (cta_group::2), 256 lanes by up to 256 columns a tile.
+// 8-bit: one CTA a tile, 128 lanes by up to 256 columns: its accumulators are
+// read after every block of k, and two CTAs' meeting takes longer than that (a
+// block of 256 x 256 x 128 took 1060 cycles on a pair, 512 of them products).
+//
+// Both operands come by TMA with the 128-byte swizzle, 128 bytes of k (or 64
+// rows of k where k is not the innermost extent: MN-major tiles) a stage.
+// Warps of a CTA:
+//   0-7  epilogue: tensor-memory lanes 32 (w mod 4), half of the tile's columns;
+//   8    producer;
+//   9    (of CTA 0 of a pair) issues the products;
+//   10   kFp8: fetches the scales; kWeightGrad: clears what a last block of k
+//        holds of the next group's rows;
+//   11   lists the CTA's tiles for the others, a few ahead (finding the next tile
+//        takes 1500 to 2000 cycles).
+// Sums.  The tensor cores add in fp32 with truncation (measured on bf16 normal
+// values against 64 bits: 4.7e-7 of the result's norm after 512 products, 2.1e-6
+// after 2048, 9.1e-6 after 8192), so what is kept in 32 bits (kWeightGrad) leaves
+// tensor memory every 512 rows of k and is summed to nearest in registers.  The
+// 8-bit product leaves it every 128 codes, where its scales change.  Two
+// accumulators of 256 columns take turns meanwhile.
+//
+// Split.  Whole waves of tiles go round robin, those with the most work first.
+// What is left over is cut by k: into equal ranges of the line of all blocks
+// (tokens as columns), or each tile into equal parts (kWeightGrad).  The parts
+// go through memory; the CTA that finishes last adds them in ascending k, so the
+// order of the additions does not depend on timing.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "kernels.h"
+#include "pair.cuh"
+#include "product.h"
+#include "smem_limit_once.h"
+#include "stream.cuh"
+#include "tcgen05.cuh"
+#include "tensor_map.h"
+
+#include "moe_a2a.h"
+
+namespace moe {
+namespace product {
+
+using namespace stream;
+
+enum Op { kFp8, kForward, kInputGrad, kWeightGrad };
+
+constexpr int kEpiWarps = 8, kProducerWarp = 8, kMmaWarp = 9, kHelpWarp = 10, kListWarp = 11;
+constexpr int kThreads = 12 * 32;
+// Registers: 384 threads start with 168 each (64512); the epilogue's 256 go to 208, the
+// other 128 to 88, which is 64512 again.
+constexpr int kStartRegs = 168, kEpiRegs = 208, kOtherRegs = 88;
+static_assert(kEpiWarps * 32 * kEpiRegs + (kThreads - kEpiWarps * 32) * kOtherRegs <=
+                  kThreads * kStartRegs, "more registers than the block starts with");
+constexpr int kMaxCols = kProductMaxCols;
+constexpr int kAccs = 2;                                  // accumulators of kMaxCols columns
+constexpr int kStep = 16, kSteps = kMaxCols / 2 / kStep;  // columns an epilogue warp stores at once
+constexpr int kLaneBytes = kTileRows * kAtom;             // A of a stage
+constexpr int kPanelBytes = 64 * kAtom;                   // 64 lanes or columns by 64 rows of k
+constexpr int kMaxStages = 12;
+constexpr int kRowGroup = 8;                              // lane tiles of a raster group
+constexpr int kBigBox = 64, kSmallBox = 8;                // rows of the token boxes
+constexpr int kScaleSlots = 4, kScaleRun = 4;             // runs of 4 blocks' scales
+constexpr int kSegs = 4;                                  // listed tiles
+constexpr int kDynamic = 193 * 1024;                      // 227 KB less the static tables
+constexpr int kClasses = 64;
+constexpr int kGradRun = 8;       // blocks of 64 rows of k that stay in tensor memory
+constexpr int kMinPart = 4;       // blocks of k that make a part worth its way through memory
+constexpr int kFp8Cols = 128;     // columns of an 8-bit tile that is not turned, at most
+
+constexpr int ctas_of(Op op) { return op == kFp8 ? 1 : 2; }
+
+// Columns of the `k` tiles of `cols` columns: evened out, a multiple of 16.
+__device__ __forceinline__ int width_of(int cols, int k) {
+    return k <= 1 ? (cols + 15) / 16 * 16 : ((cols + k - 1) / k + 15) / 16 * 16;
+}
+
+// Blocks [k0, k1) of k of a tile of a pair's (a CTA's) work: lane tile l, columns
+// from c0 on.  The tile is summed over `parts` pairs from p0 on; pair c keeps its
+// part in slot 0 unless it is p0.
+struct Seg {
+    int g, l, c0, cols, k0, k1;   // (g < 0: no more)
+    int turned;                   // tokens are the lanes
+    int p0, parts, slot0;
+    __device__ int slot(int c) const { return c == p0 ? slot0 : 0; }
+};
+
+// Turned tiles (kFp8).  A group with many tokens has them as the lanes, 128 a
+// tile, and 256 channels as the columns: a lane then has one scale for a block and
+// 128 columns, in a register, where tokens as columns need one read of shared
+// memory for four products.
+//
+// The work of a call, in shared memory.  Tiles: groups in `order`; in a group,
+// blocks of kRowGroup tiles along the channels (l), tile along the tokens (or the
+// maps' columns) outer and l inner.  `waves` tiles of each pair are whole; the
+// `rest` tiles behind them are cut.
+template <Op OP>
+struct Plan {
+    static constexpr bool KRAGGED = OP == kWeightGrad;
+    static constexpr int kLanes = ctas_of(OP) * kTileRows;
+
+    int first[kProductMaxGroups + 1];   // tiles of the groups before, in this order
+    int count[kProductMaxGroups];       // tokens of a group
+    int start[kProductMaxGroups];       // its first row
+    uint16_t order[kProductMaxGroups];
+    int hist[kClasses];
+    int turn_from;                      // tokens that make a group's tiles turned
+    int waves, rest, share, blocks;     // share: pairs for each of the rest (kWeightGrad)
+    int parts, grain, q, more;          // the cut of the rest (tokens as columns)
+
+    __device__ bool turned(int c) const { return OP == kFp8 && c >= turn_from; }
+    // Tiles along the channels, and along `c` tokens (or the maps' columns).
+    __device__ int ltiles(int c, int lanes) const {
+        const int l = turned(c) ? kMaxCols : kLanes;
+        return (lanes + l - 1) / l;
+    }
+    __device__ int mtiles(int c) const {
+        const int most = OP == kFp8 ? (turned(c) ? kTileRows : kFp8Cols) : kMaxCols;
+        return (c + most - 1) / most;
+    }
+    // Columns of a tile, and the tokens (or columns) from one tile to the next.
+    __device__ int width(int c) const { return turned(c) ? kMaxCols : width_of(c, mtiles(c)); }
+    __device__ int stride(int c) const { return turned(c) ? kTileRows : width(c); }
+
+    __device__ void tile(int t, const ProductParams &p, Seg &s) const {
+        int lo = 0, hi = p.G - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (first[mid] <= t) lo = mid; else hi = mid - 1;
+        }
+        s.g = order[lo];
+        const int c = KRAGGED ? p.cols : count[s.g], k = mtiles(c), u = t - first[lo];
+        const int w = stride(c), block = u / (kRowGroup * k);
+        const int in = min(kRowGroup, ltiles(c, p.lanes) - block * kRowGroup);
+        const int v = u - block * kRowGroup * k;
+        const int m = v / in;
+        s.l = block * kRowGroup + v - m * in;
+        s.c0 = m * w;
+        s.cols = min(w, c - s.c0);
+        s.turned = turned(c);
+    }
+    __device__ Cut cut() const {
+        Cut c(0, 0, grain);
+        c.parts = parts;
+        c.q = q;
+        c.more = more;
+        return c;
+    }
+};
+
+// A pair's way through it: its parts of the cut tiles, which are the last ones,
+// then a tile of each whole wave, to and fro.
+template <Op OP>
+struct Work {
+    static constexpr bool KRAGGED = OP == kWeightGrad;
+    const Plan<OP> &plan;
+    int u, end;  // blocks of the cut tiles' line (kWeightGrad: end 0 once they are done)
+    int wave;
+    __device__ explicit Work(const Plan<OP> &plan_) : plan(plan_), u(0), end(1), wave(0) {
+        if constexpr (!KRAGGED) {
+            const Segments sg(plan.cut(), blockIdx.x / ctas_of(OP), plan.blocks);
+            u = sg.u;
+            end = sg.end;
+        }
+    }
+    __device__ int blocks_of(int g) const {
+        return KRAGGED ? (plan.count[g] + 63) / 64 : plan.blocks;
+    }
+    __device__ bool next(const ProductParams &p, Seg &s) {
+        const int pair = blockIdx.x / ctas_of(OP), pairs = gridDim.x / ctas_of(OP);
+        s.p0 = pair;
+        s.parts = 1;
+        s.slot0 = 0;
+        if constexpr (KRAGGED) {
+            if (end != 0) {
+                end = 0;
+                const int share = plan.share, t = pair / share, part = pair - t * share;
+                if (t < plan.rest) {
+                    plan.tile(plan.waves * pairs + t, p, s);
+                    const int b = blocks_of(s.g), n = min(share, max(1, b / kMinPart));
+                    if (part < n) {
+                        s.k0 = (int)((long long)b * part / n);
+                        s.k1 = (int)((long long)b * (part + 1) / n);
+                        s.p0 = t * share;
+                        s.parts = n;
+                        return true;
+                    }
+                }
+            }
+        } else if (u < end) {
+            const int blocks = plan.blocks, t = u / blocks;
+            plan.tile(plan.waves * pairs + t, p, s);
+            s.k0 = u - t * blocks;
+            s.k1 = min(s.k0 + end - u, blocks);
+            u += s.k1 - s.k0;
+            if (s.k0 != 0 || s.k1 != blocks) {
+                const Parts pt(plan.cut(), t, blocks);
+                s.p0 = pt.c0;
+                s.parts = pt.count();
+                s.slot0 = pt.slot0;
+            }
+            return true;
+        }
+        if (wave >= plan.waves) {
+            s.g = -1;
+            return false;
+        }
+        plan.tile(wave * pairs + (wave & 1 ? pairs - 1 - pair : pair), p, s);
+        ++wave;
+        s.k0 = 0;
+        s.k1 = blocks_of(s.g);
+        return true;
+    }
+};
+
+// Bytes that `cols` columns of a tile take of a CTA's stage.
+template <Op OP>
+__device__ __forceinline__ int col_bytes(int cols) {
+    const int mine = cols / ctas_of(OP);
+    return OP == kWeightGrad ? (mine + 63) / 64 * kPanelBytes : mine * kAtom;
+}
+
+// 32 bytes of 16 neighbouring bf16 values or 8 fp32 values, 32-byte aligned.
+__device__ __forceinline__ void store_256(void *p, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+template <Op OP>
+__global__ void __launch_bounds__(kThreads, 1)
+    product_kernel(const __grid_constant__ CUtensorMap map_a,
+                   const __grid_constant__ CUtensorMap map_b,
+                   const __grid_constant__ CUtensorMap map_b8, const ProductParams p) {
+    constexpr bool KRAGGED = OP == kWeightGrad;
+    constexpr int kCtas = ctas_of(OP), kLanes = kCtas * kTileRows;
+    constexpr bool PAIR = kCtas == 2;
+    constexpr bool A_MN = OP == kInputGrad || OP == kWeightGrad, B_MN = OP == kWeightGrad;
+    constexpr bool HELP = OP == kFp8 || KRAGGED;
+    constexpr int kBlock = OP == kFp8 ? kAtom : kAtom / 2;  // extent of k in a stage
+    constexpr int kScaleFloats = OP == kFp8 ? kScaleSlots * kScaleRun * kMaxCols : 4;
+    // blocks of k whose products one accumulator takes
+    constexpr int kRun = OP == kFp8 ? 1 : (OP == kWeightGrad ? kGradRun : INT32_MAX);
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(16) float s_scale[kScaleFloats];
+    // (pairs.  full, acc_free: CTA 0's, both CTAs arrive; empty, acc_full: either's own)
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tail[kMaxStages];
+    __shared__ uint64_t acc_full[kAccs], acc_free[kAccs], sc_full[kScaleSlots], sc_free[kScaleSlots];
+    __shared__ uint64_t seg_full[kSegs], seg_free[kSegs], drained;
+    __shared__ Seg segs[kSegs];
+    __shared__ Plan<OP> plan;
+    __shared__ uint32_t s_taddr;
+    __shared__ volatile int s_failed;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = PAIR ? (int)ptx::cluster_rank() : 0;
+    const uint32_t base = ptx::smem_u32(smem_raw);
+    uint8_t *smem = smem_raw + ((1024u - (base & 1023u)) & 1023u);
+
+    if (warp == kMmaWarp) {
+        if (PAIR) tc::tmem_alloc_pair(&s_taddr, kAccs * kMaxCols);
+        else tc::tmem_alloc(&s_taddr, kAccs * kMaxCols);
+    }
+    if (tid < kMaxStages) {
+        ptx::mbar_init(&full[tid], KRAGGED ? kCtas : 1);
+        ptx::mbar_init(&empty[tid], 1);
+        ptx::mbar_init(&tail[tid], 1);
+        if (tid < kScaleSlots) {
+            ptx::mbar_init(&sc_full[tid], 1);
+            ptx::mbar_init(&sc_free[tid], kEpiWarps);
+        }
+        if (tid < kSegs) {  // read by the epilogue, the producer, the helper, the issuer
+            ptx::mbar_init(&seg_full[tid], 1);
+            ptx::mbar_init(&seg_free[tid], kEpiWarps + 1 + HELP + (rank == 0));
+        }
+        if (tid < kAccs) {
+            ptx::mbar_init(&acc_full[tid], 1);
+            ptx::mbar_init(&acc_free[tid], kCtas * kEpiWarps);
+        }
+        if (tid == 0) {
+            ptx::mbar_init(&drained, 1);
+            s_failed = 0;
+            // (a turned tile's rows are stored 8 channels at a time)
+            plan.turn_from = OP == kFp8 && p.lanes % 8 == 0 &&
+                                     reinterpret_cast<uintptr_t>(p.out) % 16 == 0
+                                 ? kProductTurnFrom : INT32_MAX;
+        }
+        ptx::fence_mbar_init();
+    }
+    if (warp == kProducerWarp && lane == 0) {
+        tc::prefetch_map(&map_a);
+        tc::prefetch_map(&map_b);
+        if (!B_MN) tc::prefetch_map(&map_b8);
+    }
+    if (tid < kClasses) plan.hist[tid] = 0;
+    ptx::grid_dependency_wait();  // nothing of the caller's memory is touched before
+    for (int g = tid; g < p.G; g += kThreads) {
+        int at = 0, c = p.M;
+        if (p.offsets != nullptr) {  // in bounds whatever they hold
+            at = min(max(__ldg(p.offsets + g), 0), p.M);
+            c = min(max(__ldg(p.offsets + g + 1), at), p.M) - at;
+        } else {
+            at = g * p.M;
+            if (p.counts != nullptr) c = min(max(__ldg(p.counts + g), 0), p.M);
+        }
+        plan.start[g] = at;
+        plan.count[g] = c;
+        if (p.G == 1) plan.order[g] = 0;
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    // the pair's barriers are set up before either arrives on the other's
+    if (PAIR) ptx::cluster_arrive();
+    // groups by the work of a tile, stable: its columns, or (to a half power of two)
+    // its blocks of k
+    const auto class_of = [&](int g) {
+        if (!KRAGGED) return plan.width(plan.count[g]) / 16;
+        const int b = (plan.count[g] + 63) / 64;
+        if (b < 2) return b;
+        const int e = 31 - __clz(b);
+        return min(kClasses - 1, 2 * e + (b >> (e - 1) & 1));
+    };
+    if (p.G > 1) {
+        for (int g = tid; g < p.G; g += kThreads) atomicAdd(&plan.hist[class_of(g)], 1);
+        __syncthreads();
+        for (int mine = warp; mine < kClasses; mine += kThreads / 32) {
+            if (plan.hist[mine] == 0) continue;
+            int at = 0;
+            for (int w = mine + 1; w < kClasses; ++w) at += plan.hist[w];
+            for (int g0 = 0; g0 < p.G; g0 += 32) {
+                const bool hit = g0 + lane < p.G && class_of(g0 + lane) == mine;
+                const unsigned m = __ballot_sync(0xffffffffu, hit);
+                if (hit) plan.order[at + __popc(m & ((1u << lane) - 1u))] = (uint16_t)(g0 + lane);
+                at += __popc(m);
+            }
+        }
+        __syncthreads();
+    }
+    if (warp == 0) {  // exclusive prefix of the groups' tiles
+        int sum = 0;
+        for (int g0 = 0; g0 < p.G; g0 += 32) {
+            const int g = g0 + lane;
+            int n = 0;
+            if (g < p.G) {
+                const int c = KRAGGED ? p.cols : plan.count[plan.order[g]];
+                n = plan.mtiles(c) * plan.ltiles(c, p.lanes);
+            }
+            int s = n;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += v;
+            }
+            if (g < p.G) plan.first[g] = sum + s - n;
+            sum += __shfl_sync(0xffffffffu, s, 31);
+        }
+        if (lane == 0) plan.first[p.G] = sum;
+    }
+    __syncthreads();
+
+    const uint32_t taddr = s_taddr;
+    const int blocks = KRAGGED ? 0 : (p.depth + kBlock - 1) / kBlock;
+    // the widest tile decides how many stages the ring has
+    int widest = 16;
+    if (KRAGGED) {
+        widest = plan.width(p.cols);
+    } else if (p.G == 1) {
+        widest = max(16, plan.width(plan.count[0]));
+    } else {
+        for (int w = 2; w <= kMaxCols / 16; ++w)
+            if (plan.hist[w] != 0) widest = 16 * w;
+    }
+    const int stage_bytes = kLaneBytes + col_bytes<OP>(widest);
+    const int stages = min(kMaxStages, (kDynamic - 1024) / stage_bytes);
+    auto a_of = [&](uint32_t s) { return smem + s * stage_bytes; };
+    auto b_of = [&](uint32_t s) { return smem + s * stage_bytes + kLaneBytes; };
+    if (tid == 0) {
+        // Whole waves are dealt out as they are; the rest (and one wave more where the
+        // rest is under a quarter of a wave) is cut.
+        const int tiles = plan.first[p.G], pairs = gridDim.x / kCtas;
+        int waves = tiles / pairs, rest = tiles - waves * pairs;
+        if (!KRAGGED && waves > 0 && rest != 0 && rest * 4 < pairs) --waves;
+        rest = tiles - waves * pairs;
+        plan.waves = waves;
+        plan.rest = rest;
+        plan.share = rest ? max(1, pairs / rest) : 1;
+        plan.blocks = blocks;
+        if constexpr (!KRAGGED) {
+            const Cut ct = widest <= 32 ? cut<true>(rest, blocks, pairs, 4 + widest / 16)
+                                        : cut<false>(rest, blocks, pairs, 4 + widest / 16);
+            plan.parts = ct.parts;
+            plan.grain = ct.grain;
+            plan.q = ct.q;
+            plan.more = ct.more;
+        }
+    }
+    __syncthreads();
+    if (PAIR) ptx::cluster_wait();
+    tc::fence_after_sync();
+    // rows of k of a block (kWeightGrad: fewer than 64 in a group's last one)
+    auto rows_of = [&](int g, int kb) { return KRAGGED ? min(64, plan.count[g] - kb * 64) : 64; };
+    // the listed tiles in turn: waits for the next one, null behind the last (or on failure)
+    const auto listed = [&](const Turn &sq) -> const Seg * {
+        if (!ptx::mbar_park(&seg_full[sq.at], sq.parity, kWaitNs)) {
+            s_failed = 1;
+            return nullptr;
+        }
+        const Seg *s = &segs[sq.at];
+        return s->g < 0 ? nullptr : s;
+    };
+    const auto arrive_first = [](uint64_t *bar) {  // on CTA 0's barrier
+        if (PAIR) ptx::mbar_arrive_pair(ptx::cluster_smem(bar, 0));
+        else mbar_arrive(bar);
+    };
+
+    // (setmaxnreg in the branch of its own roles: where two paths meet, the smaller
+    // number holds)
+    if (warp >= kEpiWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        Turn sq(kSegs);
+        if (warp == kListWarp) {
+            if (ptx::elect_one()) {
+                Work<OP> work(plan);
+                for (bool more = true; more && !s_failed; sq.next()) {
+                    Seg s;
+                    more = work.next(p, s);
+                    if (!ptx::mbar_park(&seg_free[sq.at], sq.parity ^ 1u, kWaitNs)) {
+                        s_failed = 1;
+                        break;
+                    }
+                    segs[sq.at] = s;
+                    mbar_arrive(&seg_full[sq.at]);
+                }
+            }
+        } else if (warp == kProducerWarp) {
+            if (ptx::elect_one()) {
+                Turn st(stages);
+                uint32_t issued = 0, tails = 0, tail_parity = 0;
+                while (const Seg *sp = s_failed ? nullptr : listed(sq)) {
+                    const Seg sg = *sp;
+                    mbar_arrive(&seg_free[sq.at]);
+                    sq.next();
+                    // columns of this CTA; its first lane and column; the group's first row
+                    const int half = (sg.cols + 15) / 16 * (16 / kCtas);
+                    const int a0 = sg.l * (OP == kFp8 && sg.turned ? kMaxCols : kLanes) +
+                                   rank * kTileRows;
+                    const int b0 = sg.c0 + rank * half, at = plan.start[sg.g];
+                    uint32_t bytes = kLaneBytes + col_bytes<OP>(kCtas * half);
+                    if (OP == kFp8 && sg.turned)  // boxes of 64 tokens, 256 channels
+                        bytes = (sg.cols + 63) / 64 * kPanelBytes + 2 * kLaneBytes;
+                    for (int kb = sg.k0; kb < sg.k1; ++kb, st.next()) {
+                        const int s = (int)st.at;
+                        if (!ptx::mbar_park(&empty[s], st.parity ^ 1u, kWaitNs)) {
+                            s_failed = 1;
+                            break;
+                        }
+                        // A last block with rows of the next group lands on a barrier of this
+                        // CTA; the helper clears those rows and arrives in the producer's place.
+                        const bool last = KRAGGED && rows_of(sg.g, kb) < 64;
+                        uint64_t *bar = &full[s];
+                        uint32_t bar0 = PAIR ? ptx::cluster_smem(bar, 0) : 0;
+                        if (last) {
+                            bar = &tail[s];
+                            ptx::mbar_arrive_expect_tx(bar, bytes);
+                            if (tails >> s & 1u) tail_parity ^= 1u << s;
+                            tails |= 1u << s;
+                            bar0 = ptx::cluster_smem(bar, rank);
+                        } else if (rank == 0) {
+                            ptx::mbar_arrive_expect_tx(bar, kCtas * bytes);
+                            issued |= 1u << s;
+                        } else if (KRAGGED) {
+                            ptx::mbar_arrive_pair(bar0);
+                        }
+                        const auto load_2d = [&](uint8_t *to, const CUtensorMap *m, int x, int y) {
+                            if (PAIR) tc::tma_load_2d_pair(to, m, x, y, bar0);
+                            else tc::tma_load_2d(to, m, x, y, bar);
+                        };
+                        const auto load_3d = [&](uint8_t *to, const CUtensorMap *m, int x, int y) {
+                            if (PAIR) tc::tma_load_3d_pair(to, m, x, y, sg.g, bar0);
+                            else tc::tma_load_3d(to, m, x, y, sg.g, bar);
+                        };
+                        uint8_t *a = a_of(s), *b = b_of(s);
+                        const int k = kb * kBlock;
+                        if (OP == kFp8 && sg.turned) {
+                            for (int c = 0; c < sg.cols; c += kBigBox)
+                                load_2d(a + c * kAtom, &map_b, k, at + sg.c0 + c);
+                            load_3d(b, &map_a, k, a0);
+                            load_3d(b + kLaneBytes, &map_a, k, a0 + kTileRows);
+                            continue;
+                        }
+                        if constexpr (OP == kFp8 || OP == kForward) {
+                            load_3d(a, &map_a, k, a0);
+                        } else if constexpr (OP == kInputGrad) {
+                            load_3d(a, &map_a, a0, k);
+                            load_3d(a + kPanelBytes, &map_a, a0 + 64, k);
+                        } else {
+                            load_2d(a, &map_a, a0, at + k);
+                            load_2d(a + kPanelBytes, &map_a, a0 + 64, at + k);
+                        }
+                        if constexpr (B_MN) {
+                            for (int c = 0; c < half; c += 64)
+                                load_2d(b + c / 64 * kPanelBytes, &map_b, b0 + c, at + k);
+                        } else {
+                            int c = 0;
+                            for (; c + kBigBox <= half; c += kBigBox)
+                                load_2d(b + c * kAtom, &map_b, k, at + b0 + c);
+                            for (; c < half; c += kSmallBox)
+                                load_2d(b + c * kAtom, &map_b8, k, at + b0 + c);
+                        }
+                    }
+                }
+                // copies still in flight land before shared memory goes away (CTA 1's
+                // complete on CTA 0's barriers, and the pair ends together)
+                for (int i = 0; i < stages; ++i, st.next()) {
+                    const uint32_t s = st.at, over = st.parity ^ 1u;
+                    if (issued >> s & 1u) ptx::mbar_park(&full[s], over, kWaitNs);
+                    if (tails >> s & 1u) ptx::mbar_park(&tail[s], tail_parity >> s & 1u, kWaitNs);
+                }
+            }
+        } else if (warp == kMmaWarp) {
+            if (rank == 0 && ptx::elect_one()) {
+                Turn st(stages), acc(kAccs);
+                constexpr uint32_t kMajor =
+                    (A_MN ? tc::kIdescMnA : 0u) | (B_MN ? tc::kIdescMnB : 0u);
+                // a step along k: 32 bytes, or 16 rows, in descriptor units of 16 bytes
+                constexpr uint64_t kStepA = A_MN ? 128 : 2, kStepB = B_MN ? 128 : 2;
+                const uint32_t as = ptx::smem_u32(a_of(0)), bs = ptx::smem_u32(b_of(0));
+                const uint64_t ad0 = A_MN ? tc::smem_desc_mn_sw128(as, kPanelBytes)
+                                          : tc::smem_desc_sw128(as);
+                const uint64_t bd0 = B_MN ? tc::smem_desc_mn_sw128(bs, kPanelBytes)
+                                          : tc::smem_desc_sw128(bs);
+                const auto wait_for = [&](uint64_t *bar, uint32_t parity) {
+                    const bool ok = ptx::mbar_park(bar, parity, kWaitNs);
+                    if (!ok) s_failed = 1;
+                    tc::fence_after_sync();
+                    return ok;
+                };
+                const auto commit = [](uint64_t *bar) {
+                    if (PAIR) tc::commit_pair(bar);
+                    else tc::commit(bar);
+                };
+                while (const Seg *sp = s_failed ? nullptr : listed(sq)) {
+                    const Seg sg = *sp;
+                    mbar_arrive(&seg_free[sq.at]);
+                    sq.next();
+                    const int n = sg.turned ? kMaxCols : (sg.cols + 15) / 16 * 16;
+                    const uint32_t idesc = (OP == kFp8 ? tc::idesc_e4m3_f32(kLanes, n)
+                                                       : tc::idesc_bf16_f32(kLanes, n)) |
+                                           kMajor;
+                    for (int kb = sg.k0; kb < sg.k1 && !s_failed; acc.next()) {
+                        const int from = kb, to = kRun < sg.k1 - kb ? kb + kRun : sg.k1;
+                        const uint32_t d = taddr + acc.at * kMaxCols;
+                        if (!wait_for(&acc_free[acc.at], acc.parity ^ 1u)) break;
+                        for (; kb < to; ++kb, st.next()) {
+                            if (!wait_for(&full[st.at], st.parity)) break;
+                            const uint32_t at = st.at * (uint32_t)(stage_bytes / 16);
+                            const int steps = (rows_of(sg.g, kb) + 15) / 16;
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk) {
+                                if (KRAGGED && kk >= steps) break;
+                                const bool add = kb != from || kk != 0;
+                                const uint64_t ad = ad0 + at + kk * kStepA, bd = bd0 + at + kk * kStepB;
+                                if (OP == kFp8) tc::mma_f8(d, ad, bd, idesc, add);
+                                else tc::mma_bf16_pair(d, ad, bd, idesc, add);
+                            }
+                            commit(&empty[st.at]);
+                        }
+                        commit(&acc_full[acc.at]);
+                    }
+                }
+                commit(&drained);  // before tensor memory is freed
+                ptx::mbar_park(&drained, 0, kWaitNs);
+            }
+        } else if (HELP && warp == kHelpWarp) {
+            bool ok = true;
+            Turn st(stages);          // (kWeightGrad)
+            uint32_t parity = 0;
+            Turn sc(kScaleSlots);     // (kFp8)
+            while (ok) {
+                const Seg *sp = listed(sq);
+                if (__any_sync(0xffffffffu, sp == nullptr)) break;
+                const Seg sg = *sp;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&seg_free[sq.at]);
+                sq.next();
+                if constexpr (OP == kFp8) {
+                    // Products of the tokens' scales and the channels', four blocks of k
+                    // (a run) at a time: for each column, or, turned, for each lane and each
+                    // half of the columns.
+                    const int KB = blocks, NB = (p.lanes + kScaleBlock - 1) / kScaleBlock;
+                    const bool vec = KB % 4 == 0 && reinterpret_cast<uintptr_t>(p.x_scale) % 16 == 0;
+                    const int nb = sg.turned ? 2 * sg.l : sg.l;
+                    const float *sw = p.w_scale + ((size_t)sg.g * NB + nb) * KB;
+                    const float *sw1 = nb + 1 < NB ? sw + KB : sw;
+                    const float *sx = p.x_scale + ((size_t)plan.start[sg.g] + sg.c0 + lane) * KB;
+                    const int left = sg.cols - lane;  // tokens from this lane's first one on
+                    for (int kb = sg.k0 & ~3; kb < sg.k1; kb += kScaleRun, sc.next()) {
+                        float x[kTileRows / 32][kScaleRun], w[kScaleRun], w1[kScaleRun];
+#pragma unroll
+                        for (int j = 0; j < kTileRows / 32; ++j) {
+                            const float *from = sx + (size_t)(32 * j) * KB + kb;
+#pragma unroll
+                            for (int i = 0; i < kScaleRun; ++i) x[j][i] = 0.0f;
+                            if (32 * j >= left) continue;
+                            if (vec) {
+                                const float4 f = __ldg(reinterpret_cast<const float4 *>(from));
+                                x[j][0] = f.x, x[j][1] = f.y, x[j][2] = f.z, x[j][3] = f.w;
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < kScaleRun; ++i)
+                                    if (kb + i < KB) x[j][i] = __ldg(from + i);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < kScaleRun; ++i) {
+                            w[i] = kb + i < KB ? __ldg(sw + kb + i) : 0.0f;
+                            w1[i] = sg.turned && kb + i < KB ? __ldg(sw1 + kb + i) : 0.0f;
+                        }
+                        ok = __all_sync(0xffffffffu,
+                                        ptx::mbar_park(&sc_free[sc.at], sc.parity ^ 1u, kWaitNs));
+                        if (!ok) {
+                            s_failed = 1;
+                            break;
+                        }
+                        float *to = s_scale + sc.at * kScaleRun * kMaxCols + lane;
+#pragma unroll
+                        for (int j = 0; j < kTileRows / 32; ++j)
+#pragma unroll
+                            for (int i = 0; i < kScaleRun; ++i) {
+                                to[i * kMaxCols + 32 * j] = __fmul_rn(x[j][i], w[i]);
+                                if (sg.turned)
+                                    to[i * kMaxCols + kTileRows + 32 * j] = __fmul_rn(x[j][i], w1[i]);
+                            }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sc_full[sc.at]);
+                    }
+                } else {
+                    const int half = (sg.cols + 15) / 16 * 8, panels = 2 + (half + 63) / 64;
+                    for (int kb = sg.k0; kb < sg.k1; ++kb, st.next()) {
+                        const int rows = rows_of(sg.g, kb);
+                        if (rows == 64) continue;
+                        ok = __all_sync(0xffffffffu, ptx::mbar_park(&tail[st.at],
+                                                                    parity >> st.at & 1u, kWaitNs));
+                        if (!ok) {
+                            s_failed = 1;
+                            break;
+                        }
+                        parity ^= 1u << st.at;
+                        // up to the end of the last step of 16 rows (B's panels follow A's)
+                        const int chunks = ((rows + 15) / 16 * 16 - rows) * (kAtom / 16);
+                        for (int i = lane; i < panels * chunks; i += 32) {
+                            const int panel = i / chunks, c = i - panel * chunks;
+                            *reinterpret_cast<uint4 *>(a_of(st.at) + panel * kPanelBytes +
+                                                       rows * kAtom + c * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        ptx::fence_proxy_async_smem();  // read next by the tensor cores
+                        __syncwarp();
+                        if (lane == 0) arrive_first(&full[st.at]);
+                    }
+                }
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+        // Each warp finishes 32 lanes by half of the tile's columns by itself.
+        const int q = warp & 3, hf = warp >> 2, row = q * 32 + lane;
+        Turn sq(kSegs), acc(kAccs), sc(kScaleSlots);
+        const uint32_t mine = taddr + ((uint32_t)(q * 32) << 16);
+        const uint32_t free0 = PAIR ? ptx::cluster_smem(acc_free, 0) : 0;
+        bool ok = true;
+        const auto wait_for = [&](uint64_t *bar, uint32_t parity) {
+            ok = __all_sync(0xffffffffu, ptx::mbar_park(bar, parity, kWaitNs));
+            if (!ok) s_failed = 1;
+            return ok;
+        };
+        const auto release = [&] {  // the accumulator has been read
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                if (PAIR) ptx::mbar_arrive_pair(free0 + 8 * acc.at);
+                else mbar_arrive(&acc_free[acc.at]);
+            }
+            acc.next();
+        };
+        for (;;) {
+            const Seg *const sp = listed(sq);
+            if (__any_sync(0xffffffffu, sp == nullptr)) break;
+            const Seg &sg = *sp;  // (stays there until the tile is stored)
+            int s0, steps;        // this warp's steps of kStep columns of the tile
+            if (OP == kFp8 && sg.turned) {  // channels that exist, if a token of the warp does
+                s0 = hf * kSteps;
+                const int chans = p.lanes - sg.l * kMaxCols - s0 * kStep;
+                steps = q * 32 < sg.cols ? min(max((chans + kStep - 1) / kStep, 0), kSteps) : 0;
+            } else {
+                const int all = (sg.cols + kStep - 1) / kStep;
+                s0 = hf ? (all + 1) / 2 : 0;
+                steps = hf ? all / 2 : (all + 1) / 2;
+            }
+            const int n0 = s0 * kStep, k0 = sg.k0, k1 = sg.k1;
+            float sum[kSteps][kStep];
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+                for (int j = 0; j < kStep; ++j) sum[i][j] = 0.0f;
+            if constexpr (OP == kFp8) {
+                const auto scales = [&](int kb) {  // of block kb; (a new run's: once they are there)
+                    if (kb % kScaleRun == 0 || kb == k0) wait_for(&sc_full[sc.at], sc.parity);
+                    return s_scale + (sc.at * kScaleRun + kb % kScaleRun) * kMaxCols;
+                };
+                const auto scales_read = [&](int kb) {
+                    if (kb % kScaleRun == kScaleRun - 1 || kb + 1 == k1) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sc_free[sc.at]);
+                        sc.next();
+                    }
+                };
+                if (sg.turned) {
+                    // Four loads of 32 columns a block; while one is under way the one
+                    // before is added.
+                    constexpr int kHeld = 32;
+                    uint32_t u[2][kHeld];
+                    const auto add = [&](const uint32_t (&v)[kHeld], int at, float f) {
+#pragma unroll
+                        for (int j = 0; j < kHeld; ++j) {
+                            float &t = sum[(at + j) / kStep][(at + j) % kStep];
+                            t = __fmaf_rn(__uint_as_float(v[j]), f, t);
+                        }
+                    };
+#pragma unroll
+                    for (int j = 0; j < kHeld; ++j) u[1][j] = 0;
+                    float before = 0.0f;
+                    for (int kb = k0; kb < k1; ++kb) {
+                        const float f = scales(kb)[hf * kTileRows + row];
+                        scales_read(kb);
+                        if (!ok || !wait_for(&acc_full[acc.at], acc.parity)) break;
+                        tc::fence_after_sync();
+                        const uint32_t from = mine + acc.at * kMaxCols + hf * (kMaxCols / 2);
+                        tc::ld_32x32(from, u[0]);
+                        add(u[1], 96, before);
+                        tc::wait_ld(u[0]);
+                        tc::ld_32x32(from + 32, u[1]);
+                        add(u[0], 0, f);
+                        tc::wait_ld(u[1]);
+                        tc::ld_32x32(from + 64, u[0]);
+                        add(u[1], 32, f);
+                        tc::wait_ld(u[0]);
+                        tc::ld_32x32(from + 96, u[1]);
+                        add(u[0], 64, f);
+                        tc::wait_ld(u[1]);
+                        release();
+                        before = f;
+                    }
+                    add(u[1], 96, before);
+                } else {
+                    for (int kb = k0; kb < k1; ++kb) {
+                        const float4 *fs = reinterpret_cast<const float4 *>(scales(kb) + n0);
+                        if (!ok || !wait_for(&acc_full[acc.at], acc.parity)) break;
+                        tc::fence_after_sync();
+                        const uint32_t from = mine + acc.at * kMaxCols + n0;
+                        uint32_t u[2][kStep];  // (the loads of the next step are in flight)
+                        if (steps > 0) tc::ld_32x16(from, u[0]);
+#pragma unroll
+                        for (int i = 0; i < kFp8Cols / 2 / kStep; ++i) {
+                            if (i >= steps) break;
+                            tc::wait_ld(u[i & 1]);
+                            if (i + 1 < steps)
+                                tc::ld_32x16(from + (i + 1) * kStep, u[(i + 1) & 1]);
+                            float(&t)[kStep] = sum[i];
+#pragma unroll
+                            for (int j = 0; j < kStep / 4; ++j) {
+                                const float4 f4 = fs[i * (kStep / 4) + j];
+                                const uint32_t *v = &u[i & 1][4 * j];
+                                t[4 * j] = __fmaf_rn(__uint_as_float(v[0]), f4.x, t[4 * j]);
+                                t[4 * j + 1] = __fmaf_rn(__uint_as_float(v[1]), f4.y, t[4 * j + 1]);
+                                t[4 * j + 2] = __fmaf_rn(__uint_as_float(v[2]), f4.z, t[4 * j + 2]);
+                                t[4 * j + 3] = __fmaf_rn(__uint_as_float(v[3]), f4.w, t[4 * j + 3]);
+                            }
+                        }
+                        release();
+                        scales_read(kb);
+                    }
+                }
+            } else {
+                for (int kb = k0; kb < k1; kb = kRun < k1 - kb ? kb + kRun : k1) {
+                    if (!wait_for(&acc_full[acc.at], acc.parity)) break;
+                    tc::fence_after_sync();
+                    const uint32_t from = mine + acc.at * kMaxCols + n0;
+                    uint32_t u[2][kStep];  // (the loads of the next step are in flight)
+                    if (steps > 0) tc::ld_32x16(from, u[0]);
+#pragma unroll
+                    for (int i = 0; i < kSteps; ++i) {
+                        if (i >= steps) break;
+                        tc::wait_ld(u[i & 1]);
+                        if (i + 1 < steps && i + 1 < kSteps)
+                            tc::ld_32x16(from + (i + 1) * kStep, u[(i + 1) & 1]);
+#pragma unroll
+                        for (int j = 0; j < kStep; ++j)
+                            sum[i][j] = __fadd_rn(sum[i][j], __uint_as_float(u[i & 1][j]));
+                    }
+                    release();
+                }
+            }
+            if (!ok) break;
+
+            // the lane's channel (not turned)
+            const int chan = sg.l * kLanes + rank * kTileRows + row;
+            const bool live = chan < p.lanes;
+            uint16_t *const out16 = static_cast<uint16_t *>(p.out);
+            // values 2 j and 2 j + 1
+            const auto pack_bf16 = [](const float (&v)[kStep], int j) {
+                const __nv_bfloat162 o = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+                return *reinterpret_cast<const uint32_t *>(&o);
+            };
+            // 16 neighbouring values of a row of `left` more, `left` a multiple of 8
+            const bool whole32 = (KRAGGED ? p.cols : p.lanes) % 16 == 0 &&
+                                 reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
+            const auto store_row = [&](uint16_t *o, const float (&v)[kStep], int left) {
+                if (left <= 0) return;
+                uint32_t w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = pack_bf16(v, j);
+                if (whole32) {
+                    store_256(o, w);
+                } else {
+                    reinterpret_cast<uint4 *>(o)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                    if (left > 8)
+                        reinterpret_cast<uint4 *>(o)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                }
+            };
+            // Columns n .. n + 15 (of the tile) of this lane.
+            const auto store = [&](int n, const float (&v)[kStep]) {
+                if (OP == kFp8 && sg.turned) {  // a token's row
+                    const int at = sg.l * kMaxCols + n;
+                    if (row < sg.cols)
+                        store_row(out16 + ((size_t)plan.start[sg.g] + sg.c0 + row) * p.lanes + at, v,
+                                  p.lanes - at);
+                } else if constexpr (!KRAGGED) {
+                    // Tokens as columns: two a word; neighbouring lanes exchange, so that the
+                    // even lane stores both lanes' values of the first column and the odd
+                    // lane those of the second.
+                    const bool words =
+                        p.lanes % 2 == 0 && reinterpret_cast<uintptr_t>(p.out) % 4 == 0;
+                    const uint32_t pick = lane & 1 ? 0x3276u : 0x5410u;
+                    uint16_t *at = out16 + (chan & ~1) +
+                                   ((size_t)plan.start[sg.g] + sg.c0 + n + (lane & 1)) * p.lanes;
+                    const int left = sg.cols - n - (lane & 1);
+#pragma unroll
+                    for (int j = 0; j < kStep / 2; ++j, at += 2 * (size_t)p.lanes) {
+                        const uint32_t mine2 = pack_bf16(v, j);
+                        const uint32_t both =
+                            __byte_perm(mine2, __shfl_xor_sync(0xffffffffu, mine2, 1), pick);
+                        if (words) {
+                            if (live && 2 * j < left) *reinterpret_cast<uint32_t *>(at) = both;
+                        } else if (2 * j < left) {  // odd extent or address: rows start off a word
+                            if ((chan & ~1) < p.lanes) at[0] = (uint16_t)both;
+                            if ((chan | 1) < p.lanes) at[1] = (uint16_t)(both >> 16);
+                        }
+                    }
+                } else if (live) {  // a row of the map's gradient
+                    const size_t at = ((size_t)sg.g * p.lanes + chan) * p.cols + sg.c0 + n;
+                    const int left = p.cols - sg.c0 - n;
+                    if (!p.f32) {
+                        store_row(out16 + at, v, left);
+                        return;
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (8 * h >= left) break;
+                        float *o = static_cast<float *>(p.out) + at + 8 * h;
+                        float f[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) f[j] = v[8 * h + j];
+                        if (p.accumulate) {
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const float4 old = reinterpret_cast<const float4 *>(o)[j];
+                                f[4 * j] = old.x + f[4 * j];
+                                f[4 * j + 1] = old.y + f[4 * j + 1];
+                                f[4 * j + 2] = old.z + f[4 * j + 2];
+                                f[4 * j + 3] = old.w + f[4 * j + 3];
+                            }
+                        }
+                        if (reinterpret_cast<uintptr_t>(p.out) % 32 == 0) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(f[j]);
+                            store_256(o, w);
+                        } else {
+                            reinterpret_cast<float4 *>(o)[0] = make_float4(f[0], f[1], f[2], f[3]);
+                            reinterpret_cast<float4 *>(o)[1] = make_float4(f[4], f[5], f[6], f[7]);
+                        }
+                    }
+                }
+            };
+            if (sg.parts == 1) {
+                // (adding nothing to what is there: left alone)
+                if (!(KRAGGED && p.accumulate && k0 == k1)) {
+#pragma unroll
+                    for (int i = 0; i < kSteps; ++i) {
+                        if (i >= steps) break;
+                        store(n0 + i * kStep, sum[i]);
+                    }
+                }
+            } else if (steps > 0) {
+                const int pair = blockIdx.x / kCtas;
+                auto part_of = [&](int c) {
+                    return p.part +
+                           (size_t)(2 * (kCtas * c + rank) + sg.slot(c)) * p.nmax * kTileRows + row;
+                };
+                float *to = part_of(pair) + n0 * kTileRows;
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    if (i >= steps) break;
+#pragma unroll
+                    for (int j = 0; j < kStep; ++j)
+                        __stcg(to + (i * kStep + j) * kTileRows, sum[i][j]);
+                }
+                // the warp's parts, then lane 0's fence and count; and the other way round: what
+                // lane 0 finds counted, its fence, then the warp's reads (a shuffle orders no
+                // memory)
+                __syncwarp();
+                __threadfence();
+                int last = 0;
+                if (lane == 0) {
+                    int *m = &p.header->merged[hf][kCtas * sg.p0 + rank][q];
+                    last = atomicAdd(m, 1) == sg.parts - 1;
+                    if (last) *m = 0;  // for the next call
+                    __threadfence();
+                }
+                last = __shfl_sync(0xffffffffu, last, 0);
+                __syncwarp();
+                for (int i = 0; last && i < steps; ++i) {
+                    const int n = n0 + i * kStep;
+                    float v[kStep];
+#pragma unroll
+                    for (int j = 0; j < kStep; ++j) v[j] = 0.0f;
+                    for (int c = sg.p0; c < sg.p0 + sg.parts; ++c) {
+                        const float *f = part_of(c) + (size_t)n * kTileRows;
+#pragma unroll
+                        for (int j = 0; j < kStep; ++j) v[j] += __ldcg(f + j * kTileRows);
+                    }
+                    store(n, v);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&seg_free[sq.at]);
+            sq.next();
+        }
+    }
+
+    __syncwarp();
+    if (warp == kMmaWarp && rank != 0)  // CTA 0's products read this CTA's memory too
+        ptx::mbar_park(&drained, 0, kWaitNs);
+    __syncwarp();
+    tc::fence_before_sync();
+    if (PAIR) ptx::cluster_sync();
+    else __syncthreads();
+    tc::fence_after_sync();
+    // the output may be an input that the next kernel reads before it waits for this
+    // one: the CTA's stores (all of them are before the barrier) are visible first
+    if (tid == 0) __threadfence();
+    if (tid == 0 && s_failed) atomicOr(&p.header->flags, MOE_DEVICE_FLAG_WAIT_TIMEOUT);
+    if (warp == kMmaWarp) {
+        if (PAIR) tc::tmem_dealloc_pair(taddr, kAccs * kMaxCols);
+        else tc::tmem_dealloc(taddr, kAccs * kMaxCols);
+    }
+}
+
+// Matrix of `rows` rows of `cols` values, boxes of box_cols x box_rows.
+inline bool map_2d(CUtensorMap *m, const void *base, long long rows, long long cols, int box_cols,
+                   int box_rows, bool bytes) {
+    const long long ext[2] = {cols, rows}, str[2] = {1, cols};
+    const int box[2] = {box_cols, box_rows};
+    return make_map_nd(m, base, 2, ext, str, box, bytes);
+}
+
+// `groups` matrices one after another.
+inline bool map_3d(CUtensorMap *m, const void *base, long long groups, long long rows,
+                   long long cols, int box_cols, int box_rows, bool bytes) {
+    const long long ext[3] = {cols, rows, groups}, str[3] = {1, cols, rows * cols};
+    const int box[3] = {box_cols, box_rows, 1};
+    return make_map_nd(m, base, 3, ext, str, box, bytes);
+}
+
+template <Op OP>
+cudaError_t launch(const ProductParams &p, const CUtensorMap &a, const CUtensorMap &b,
+                   const CUtensorMap &b8, int num_sms, cudaStream_t st) {
+    constexpr int kCtas = ctas_of(OP);
+    int grid = num_sms < kStreamMaxCtas ? num_sms : kStreamMaxCtas;
+    grid -= grid % kCtas;
+    if (grid < kCtas) return cudaErrorInvalidValue;
+    static std::atomic<unsigned long long> raised{0};
+    const cudaError_t err = raise_smem_limit_once(product_kernel<OP>, (size_t)kDynamic, raised);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kDynamic;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kCtas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = kCtas > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, product_kernel<OP>, a, b, b8, p);
+}
+
+}  // namespace product
+}  // namespace moe

@@ -1,14 +1,14 @@
 // gemm_fp8.cu -- product of e4m3 codes with a scale for each block of 128
 // codes of a token and one for each 128 x 128 block of the weights, dense,
 // grouped over the experts' planes, or over rows that stand one group after
-// another (pair_product.cuh).
+// another (expert_product.cuh).
 //
 // Operation, group g, token row m, channel n:
 //   out[m][n] = bf16_rn( sum over blocks b of RN32(sx[m][b] * sw[g][n / 128][b]) * d_b ),
 //   d_b = sum over h in block b of xq[m][h] * wq[g][n][h],
 // the products of codes exact, the sums in fp32 (d_b as the tensor cores add,
 // the outer sum by fused multiply-adds in ascending b).
-#include "pair_product.cuh"
+#include "expert_product.cuh"
 
 namespace moe {
 

@@ -1,5 +1,5 @@
 // gemm_ragged.cu -- one linear map per expert over rows that stand one
-// expert after another, and its gradients (pair_product.cuh).
+// expert after another, and its gradients (expert_product.cuh).
 //
 // With rows offsets[e] <= m < offsets[e + 1] of expert e and maps W_e (N x H):
 //   y[m][n]    = bf16_rn( sum_h x[m][h] * W_e[n][h] )
@@ -7,7 +7,7 @@
 //   dW_e[n][h] = sum_m dy[m][n] * x[m][h]            (bf16 or fp32, or added to fp32)
 // products of bf16 values summed in fp32.  Rows of no expert are not written;
 // the dW_e of an expert without rows is zero.
-#include "pair_product.cuh"
+#include "expert_product.cuh"
 
 namespace moe {
 

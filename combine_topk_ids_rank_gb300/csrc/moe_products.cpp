@@ -17,7 +17,7 @@ bool extents_ok(int64_t groups, int64_t rows, int64_t lanes, int64_t wide, int64
         groups * depth > kProductMaxExtent)
         return false;
     // (a group may end with a tile that is not full)
-    return (lanes + 255) / 256 * (wide / 256 + groups) <= INT32_MAX / 2;
+    return (lanes + 255) / 256 * (wide / 128 + groups) <= INT32_MAX / 2;
 }
 
 ProductParams params(const int32_t *counts, const int32_t *offsets, void *out, void *scratch,
