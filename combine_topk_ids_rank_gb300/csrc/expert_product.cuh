@@ -15,19 +15,20 @@
 //
 // bf16: pairs of CTAs (cta_group::2), 256 lanes by up to 256 columns a tile.
 // 8-bit: one CTA a tile, 128 lanes by up to 256 columns: its accumulators are
-// read after every block of k, and two CTAs' meeting takes longer than that (a
-// block of 256 x 256 x 128 took 1060 cycles on a pair, 512 of them products).
+// read after every block of k, and two CTAs' meeting takes longer than that.  An
+// accumulator's two halves of 128 columns are filled by an issuing warp each and
+// given back by themselves.
 //
 // Both operands come by TMA with the 128-byte swizzle, 128 bytes of k (or 64
 // rows of k where k is not the innermost extent: MN-major tiles) a stage.
 // Warps of a CTA:
 //   0-7  epilogue: tensor-memory lanes 32 (w mod 4), half of the tile's columns;
-//   8    producer;
-//   9    (of CTA 0 of a pair) issues the products;
-//   10   kFp8: fetches the scales; kWeightGrad: clears what a last block of k
-//        holds of the next group's rows;
-//   11   lists the CTA's tiles for the others, a few ahead (finding the next tile
-//        takes 1500 to 2000 cycles).
+//   8    producer; kFp8: lists the CTA's tiles for the others as it goes;
+//   9    (of CTA 0 of a pair) issues the products; kFp8: of columns 0 to 127;
+//   10   kFp8: fetches the scales of tiles that are not turned; kWeightGrad:
+//        clears what a last block of k holds of the next group's rows;
+//   11   lists the pair's tiles, a few ahead (finding the next tile takes 1500 to
+//        2000 cycles); kFp8: issues the products of columns 128 to 255.
 // Sums.  The tensor cores add in fp32 with truncation (measured on bf16 normal
 // values against 64 bits: 4.7e-7 of the result's norm after 512 products, 2.1e-6
 // after 2048, 9.1e-6 after 8192), so what is kept in 32 bits (kWeightGrad) leaves
@@ -44,6 +45,7 @@
 
 #include <cuda_bf16.h>
 
+#include "f32x2.cuh"
 #include "kernels.h"
 #include "pair.cuh"
 #include "product.h"
@@ -63,9 +65,9 @@ enum Op { kFp8, kForward, kInputGrad, kWeightGrad };
 
 constexpr int kEpiWarps = 8, kProducerWarp = 8, kMmaWarp = 9, kHelpWarp = 10, kListWarp = 11;
 constexpr int kThreads = 12 * 32;
-// Registers: 384 threads start with 168 each (64512); the epilogue's 256 go to 208, the
-// other 128 to 88, which is 64512 again.
-constexpr int kStartRegs = 168, kEpiRegs = 208, kOtherRegs = 88;
+// Registers: 384 threads start with 168 each (64512); the epilogue's 256 go to 224, the
+// other 128 to 56, which is 64512 again.
+constexpr int kStartRegs = 168, kEpiRegs = 224, kOtherRegs = 56;
 static_assert(kEpiWarps * 32 * kEpiRegs + (kThreads - kEpiWarps * 32) * kOtherRegs <=
                   kThreads * kStartRegs, "more registers than the block starts with");
 constexpr int kMaxCols = kProductMaxCols;
@@ -254,14 +256,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr bool A_MN = OP == kInputGrad || OP == kWeightGrad, B_MN = OP == kWeightGrad;
     constexpr bool HELP = OP == kFp8 || KRAGGED;
     constexpr int kBlock = OP == kFp8 ? kAtom : kAtom / 2;  // extent of k in a stage
-    constexpr int kScaleFloats = OP == kFp8 ? kScaleSlots * kScaleRun * kMaxCols : 4;
+    constexpr int kScaleFloats = OP == kFp8 ? kScaleSlots * kScaleRun * kFp8Cols : 4;
     // blocks of k whose products one accumulator takes
     constexpr int kRun = OP == kFp8 ? 1 : (OP == kWeightGrad ? kGradRun : INT32_MAX);
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(16) float s_scale[kScaleFloats];
     // (pairs.  full, acc_free: CTA 0's, both CTAs arrive; empty, acc_full: either's own)
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tail[kMaxStages];
-    __shared__ uint64_t acc_full[kAccs], acc_free[kAccs], sc_full[kScaleSlots], sc_free[kScaleSlots];
+    __shared__ uint64_t acc_full[kAccs][2], acc_free[kAccs][2], sc_full[kScaleSlots], sc_free[kScaleSlots];
     __shared__ uint64_t seg_full[kSegs], seg_free[kSegs], drained;
     __shared__ Seg segs[kSegs];
     __shared__ Plan<OP> plan;
@@ -278,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (tid < kMaxStages) {
         ptx::mbar_init(&full[tid], KRAGGED ? kCtas : 1);
-        ptx::mbar_init(&empty[tid], 1);
+        ptx::mbar_init(&empty[tid], OP == kFp8 ? 2 : 1);
         ptx::mbar_init(&tail[tid], 1);
         if (tid < kScaleSlots) {
             ptx::mbar_init(&sc_full[tid], 1);
@@ -289,11 +291,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(&seg_free[tid], kEpiWarps + 1 + HELP + (rank == 0));
         }
         if (tid < kAccs) {
-            ptx::mbar_init(&acc_full[tid], 1);
-            ptx::mbar_init(&acc_free[tid], kCtas * kEpiWarps);
+            for (int h = 0; h < 2; ++h) {
+                ptx::mbar_init(&acc_full[tid][h], 1);
+                ptx::mbar_init(&acc_free[tid][h], OP == kFp8 ? kEpiWarps / 2 : kCtas * kEpiWarps);
+            }
         }
         if (tid == 0) {
-            ptx::mbar_init(&drained, 1);
+            ptx::mbar_init(&drained, OP == kFp8 ? 2 : 1);
             s_failed = 0;
             // (a turned tile's rows are stored 8 channels at a time)
             plan.turn_from = OP == kFp8 && p.lanes % 8 == 0 &&
@@ -432,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp >= kEpiWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         Turn sq(kSegs);
-        if (warp == kListWarp) {
+        if (OP != kFp8 && warp == kListWarp) {
             if (ptx::elect_one()) {
                 Work<OP> work(plan);
                 for (bool more = true; more && !s_failed; sq.next()) {
@@ -450,10 +454,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ptx::elect_one()) {
                 Turn st(stages);
                 uint32_t issued = 0, tails = 0, tail_parity = 0;
-                while (const Seg *sp = s_failed ? nullptr : listed(sq)) {
-                    const Seg sg = *sp;
-                    mbar_arrive(&seg_free[sq.at]);
-                    sq.next();
+                Work<OP> work(plan);
+                for (;;) {
+                    Seg sg;
+                    if (OP == kFp8) {  // lists the tiles itself
+                        const bool more = !s_failed && work.next(p, sg);
+                        if (!ptx::mbar_park(&seg_free[sq.at], sq.parity ^ 1u, kWaitNs)) {
+                            s_failed = 1;
+                            break;
+                        }
+                        segs[sq.at] = sg;
+                        mbar_arrive(&seg_full[sq.at]);
+                        sq.next();
+                        if (!more) break;
+                    } else {
+                        const Seg *sp = s_failed ? nullptr : listed(sq);
+                        if (sp == nullptr) break;
+                        sg = *sp;
+                        mbar_arrive(&seg_free[sq.at]);
+                        sq.next();
+                    }
                     // columns of this CTA; its first lane and column; the group's first row
                     const int half = (sg.cols + 15) / 16 * (16 / kCtas);
                     const int a0 = sg.l * (OP == kFp8 && sg.turned ? kMaxCols : kLanes) +
@@ -531,8 +551,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (tails >> s & 1u) ptx::mbar_park(&tail[s], tail_parity >> s & 1u, kWaitNs);
                 }
             }
-        } else if (warp == kMmaWarp) {
+        } else if (warp == kMmaWarp || (OP == kFp8 && warp == kListWarp)) {
             if (rank == 0 && ptx::elect_one()) {
+                const int h = warp == kMmaWarp ? 0 : 1;
                 Turn st(stages), acc(kAccs);
                 constexpr uint32_t kMajor =
                     (A_MN ? tc::kIdescMnA : 0u) | (B_MN ? tc::kIdescMnB : 0u);
@@ -557,29 +578,49 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const Seg sg = *sp;
                     mbar_arrive(&seg_free[sq.at]);
                     sq.next();
-                    const int n = sg.turned ? kMaxCols : (sg.cols + 15) / 16 * 16;
+                    // 8-bit: an accumulator's halves are filled and given back by themselves
+                    const int n = sg.turned ? kMaxCols / 2 : (sg.cols + 15) / 16 * 16;
                     const uint32_t idesc = (OP == kFp8 ? tc::idesc_e4m3_f32(kLanes, n)
                                                        : tc::idesc_bf16_f32(kLanes, n)) |
                                            kMajor;
                     for (int kb = sg.k0; kb < sg.k1 && !s_failed; acc.next()) {
                         const int from = kb, to = kRun < sg.k1 - kb ? kb + kRun : sg.k1;
                         const uint32_t d = taddr + acc.at * kMaxCols;
-                        if (!wait_for(&acc_free[acc.at], acc.parity ^ 1u)) break;
+                        if (!wait_for(&full[st.at], st.parity)) break;
+                        if (OP == kFp8) {
+                            const uint32_t at = st.at * (uint32_t)(stage_bytes / 16);
+                            // (not turned: all warps read what the first issuer's products left)
+                            if (!wait_for(&acc_free[acc.at][h], acc.parity ^ 1u) ||
+                                (h == 0 && !sg.turned &&
+                                 !wait_for(&acc_free[acc.at][1], acc.parity ^ 1u)))
+                                break;
+                            if (h == 0 || sg.turned) {
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    tc::mma_f8(d + h * (kMaxCols / 2), ad0 + at + kk * kStepA,
+                                               bd0 + at + h * (kLaneBytes / 16) + kk * kStepB, idesc,
+                                               kk != 0);
+                            }
+                            commit(&acc_full[acc.at][h]);
+                            commit(&empty[st.at]);
+                            ++kb;
+                            st.next();
+                            continue;
+                        }
+                        if (!wait_for(&acc_free[acc.at][0], acc.parity ^ 1u)) break;
                         for (; kb < to; ++kb, st.next()) {
-                            if (!wait_for(&full[st.at], st.parity)) break;
+                            if (kb != from && !wait_for(&full[st.at], st.parity)) break;
                             const uint32_t at = st.at * (uint32_t)(stage_bytes / 16);
                             const int steps = (rows_of(sg.g, kb) + 15) / 16;
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk) {
                                 if (KRAGGED && kk >= steps) break;
-                                const bool add = kb != from || kk != 0;
-                                const uint64_t ad = ad0 + at + kk * kStepA, bd = bd0 + at + kk * kStepB;
-                                if (OP == kFp8) tc::mma_f8(d, ad, bd, idesc, add);
-                                else tc::mma_bf16_pair(d, ad, bd, idesc, add);
+                                tc::mma_bf16_pair(d, ad0 + at + kk * kStepA, bd0 + at + kk * kStepB,
+                                                  idesc, kb != from || kk != 0);
                             }
                             commit(&empty[st.at]);
                         }
-                        commit(&acc_full[acc.at]);
+                        commit(&acc_full[acc.at][0]);
                     }
                 }
                 commit(&drained);  // before tensor memory is freed
@@ -598,20 +639,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(&seg_free[sq.at]);
                 sq.next();
                 if constexpr (OP == kFp8) {
-                    // Products of the tokens' scales and the channels', four blocks of k
-                    // (a run) at a time: for each column, or, turned, for each lane and each
-                    // half of the columns.
+                    // Products of the tokens' scales and the channels' of tiles that are not
+                    // turned, four blocks of k (a run) at a time, for each column.
+                    if (sg.turned) continue;
                     const int KB = blocks, NB = (p.lanes + kScaleBlock - 1) / kScaleBlock;
                     const bool vec = KB % 4 == 0 && reinterpret_cast<uintptr_t>(p.x_scale) % 16 == 0;
-                    const int nb = sg.turned ? 2 * sg.l : sg.l;
-                    const float *sw = p.w_scale + ((size_t)sg.g * NB + nb) * KB;
-                    const float *sw1 = nb + 1 < NB ? sw + KB : sw;
+                    const float *sw = p.w_scale + ((size_t)sg.g * NB + sg.l) * KB;
                     const float *sx = p.x_scale + ((size_t)plan.start[sg.g] + sg.c0 + lane) * KB;
                     const int left = sg.cols - lane;  // tokens from this lane's first one on
                     for (int kb = sg.k0 & ~3; kb < sg.k1; kb += kScaleRun, sc.next()) {
-                        float x[kTileRows / 32][kScaleRun], w[kScaleRun], w1[kScaleRun];
+                        float x[kFp8Cols / 32][kScaleRun], w[kScaleRun];
 #pragma unroll
-                        for (int j = 0; j < kTileRows / 32; ++j) {
+                        for (int j = 0; j < kFp8Cols / 32; ++j) {
                             const float *from = sx + (size_t)(32 * j) * KB + kb;
 #pragma unroll
                             for (int i = 0; i < kScaleRun; ++i) x[j][i] = 0.0f;
@@ -626,25 +665,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
 #pragma unroll
-                        for (int i = 0; i < kScaleRun; ++i) {
+                        for (int i = 0; i < kScaleRun; ++i)
                             w[i] = kb + i < KB ? __ldg(sw + kb + i) : 0.0f;
-                            w1[i] = sg.turned && kb + i < KB ? __ldg(sw1 + kb + i) : 0.0f;
-                        }
                         ok = __all_sync(0xffffffffu,
                                         ptx::mbar_park(&sc_free[sc.at], sc.parity ^ 1u, kWaitNs));
                         if (!ok) {
                             s_failed = 1;
                             break;
                         }
-                        float *to = s_scale + sc.at * kScaleRun * kMaxCols + lane;
+                        float *to = s_scale + sc.at * kScaleRun * kFp8Cols + lane;
 #pragma unroll
-                        for (int j = 0; j < kTileRows / 32; ++j)
+                        for (int j = 0; j < kFp8Cols / 32; ++j)
 #pragma unroll
-                            for (int i = 0; i < kScaleRun; ++i) {
-                                to[i * kMaxCols + 32 * j] = __fmul_rn(x[j][i], w[i]);
-                                if (sg.turned)
-                                    to[i * kMaxCols + kTileRows + 32 * j] = __fmul_rn(x[j][i], w1[i]);
-                            }
+                            for (int i = 0; i < kScaleRun; ++i)
+                                to[i * kFp8Cols + 32 * j] = __fmul_rn(x[j][i], w[i]);
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&sc_full[sc.at]);
                     }
@@ -680,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int q = warp & 3, hf = warp >> 2, row = q * 32 + lane;
         Turn sq(kSegs), acc(kAccs), sc(kScaleSlots);
         const uint32_t mine = taddr + ((uint32_t)(q * 32) << 16);
-        const uint32_t free0 = PAIR ? ptx::cluster_smem(acc_free, 0) : 0;
+        const uint32_t free0 = PAIR ? ptx::cluster_smem(&acc_free[0][0], 0) : 0;
         bool ok = true;
         const auto wait_for = [&](uint64_t *bar, uint32_t parity) {
             ok = __all_sync(0xffffffffu, ptx::mbar_park(bar, parity, kWaitNs));
@@ -691,8 +725,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) {
-                if (PAIR) ptx::mbar_arrive_pair(free0 + 8 * acc.at);
-                else mbar_arrive(&acc_free[acc.at]);
+                if (PAIR) ptx::mbar_arrive_pair(free0 + 16 * acc.at);
+                else mbar_arrive(&acc_free[acc.at][hf]);
             }
             acc.next();
         };
@@ -719,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (OP == kFp8) {
                 const auto scales = [&](int kb) {  // of block kb; (a new run's: once they are there)
                     if (kb % kScaleRun == 0 || kb == k0) wait_for(&sc_full[sc.at], sc.parity);
-                    return s_scale + (sc.at * kScaleRun + kb % kScaleRun) * kMaxCols;
+                    return s_scale + (sc.at * kScaleRun + kb % kScaleRun) * kFp8Cols;
                 };
                 const auto scales_read = [&](int kb) {
                     if (kb % kScaleRun == kScaleRun - 1 || kb + 1 == k1) {
@@ -729,46 +763,72 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 };
                 if (sg.turned) {
-                    // Four loads of 32 columns a block; while one is under way the one
-                    // before is added.
+                    // Four loads of 32 columns a block; the last two are added when the
+                    // accumulator's half has been given back.
                     constexpr int kHeld = 32;
                     uint32_t u[2][kHeld];
                     const auto add = [&](const uint32_t (&v)[kHeld], int at, float f) {
 #pragma unroll
-                        for (int j = 0; j < kHeld; ++j) {
-                            float &t = sum[(at + j) / kStep][(at + j) % kStep];
-                            t = __fmaf_rn(__uint_as_float(v[j]), f, t);
+                        for (int j = 0; j < kHeld; j += 2) {
+                            float *t = &sum[(at + j) / kStep][(at + j) % kStep];
+                            const x2::f2 o = x2::fma(
+                                x2::pack(__uint_as_float(v[j]), __uint_as_float(v[j + 1])),
+                                x2::pack(f, f), x2::pack(t[0], t[1]));
+                            x2::unpack(o, t[0], t[1]);
                         }
                     };
-#pragma unroll
-                    for (int j = 0; j < kHeld; ++j) u[1][j] = 0;
-                    float before = 0.0f;
+                    // Scales of this lane's token, four blocks (a run) at a time, a run ahead.
+                    const int KB = plan.blocks, NB = (p.lanes + kScaleBlock - 1) / kScaleBlock;
+                    const bool there = row < sg.cols;
+                    const bool vec = KB % 4 == 0 && reinterpret_cast<uintptr_t>(p.x_scale) % 16 == 0;
+                    const float *sx = p.x_scale + ((size_t)plan.start[sg.g] + sg.c0 + row) * KB;
+                    const float *sw =
+                        p.w_scale + ((size_t)sg.g * NB + min(2 * sg.l + hf, NB - 1)) * KB;
+                    float4 x4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), f4 = x4;
+                    const auto fetch = [&](int kb) {
+                        if (!there) return;
+                        if (vec) {
+                            x4 = __ldg(reinterpret_cast<const float4 *>(sx + kb));
+                        } else {
+                            x4.x = __ldg(sx + kb);
+                            if (kb + 1 < KB) x4.y = __ldg(sx + kb + 1);
+                            if (kb + 2 < KB) x4.z = __ldg(sx + kb + 2);
+                            if (kb + 3 < KB) x4.w = __ldg(sx + kb + 3);
+                        }
+                    };
+                    fetch(k0 & ~3);
                     for (int kb = k0; kb < k1; ++kb) {
-                        const float f = scales(kb)[hf * kTileRows + row];
-                        scales_read(kb);
-                        if (!ok || !wait_for(&acc_full[acc.at], acc.parity)) break;
+                        const int r = kb % kScaleRun;
+                        if (r == 0 || kb == k0) {
+                            const int b = kb - r;
+                            f4.x = __fmul_rn(x4.x, __ldg(sw + b));
+                            f4.y = __fmul_rn(x4.y, __ldg(sw + min(b + 1, KB - 1)));
+                            f4.z = __fmul_rn(x4.z, __ldg(sw + min(b + 2, KB - 1)));
+                            f4.w = __fmul_rn(x4.w, __ldg(sw + min(b + 3, KB - 1)));
+                            if (b + kScaleRun < k1) fetch(b + kScaleRun);
+                        }
+                        const float f = r < 2 ? (r == 0 ? f4.x : f4.y) : (r == 2 ? f4.z : f4.w);
+                        if (!wait_for(&acc_full[acc.at][hf], acc.parity)) break;
                         tc::fence_after_sync();
                         const uint32_t from = mine + acc.at * kMaxCols + hf * (kMaxCols / 2);
                         tc::ld_32x32(from, u[0]);
-                        add(u[1], 96, before);
-                        tc::wait_ld(u[0]);
                         tc::ld_32x32(from + 32, u[1]);
-                        add(u[0], 0, f);
+                        tc::wait_ld(u[0]);
                         tc::wait_ld(u[1]);
+                        add(u[0], 0, f);
                         tc::ld_32x32(from + 64, u[0]);
                         add(u[1], 32, f);
-                        tc::wait_ld(u[0]);
                         tc::ld_32x32(from + 96, u[1]);
-                        add(u[0], 64, f);
+                        tc::wait_ld(u[0]);
                         tc::wait_ld(u[1]);
                         release();
-                        before = f;
+                        add(u[0], 64, f);
+                        add(u[1], 96, f);
                     }
-                    add(u[1], 96, before);
                 } else {
                     for (int kb = k0; kb < k1; ++kb) {
                         const float4 *fs = reinterpret_cast<const float4 *>(scales(kb) + n0);
-                        if (!ok || !wait_for(&acc_full[acc.at], acc.parity)) break;
+                        if (!ok || !wait_for(&acc_full[acc.at][0], acc.parity)) break;
                         tc::fence_after_sync();
                         const uint32_t from = mine + acc.at * kMaxCols + n0;
                         uint32_t u[2][kStep];  // (the loads of the next step are in flight)
@@ -796,7 +856,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             } else {
                 for (int kb = k0; kb < k1; kb = kRun < k1 - kb ? kb + kRun : k1) {
-                    if (!wait_for(&acc_full[acc.at], acc.parity)) break;
+                    if (!wait_for(&acc_full[acc.at][0], acc.parity)) break;
                     tc::fence_after_sync();
                     const uint32_t from = mine + acc.at * kMaxCols + n0;
                     uint32_t u[2][kStep];  // (the loads of the next step are in flight)
@@ -841,23 +901,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                         reinterpret_cast<uint4 *>(o)[1] = make_uint4(w[4], w[5], w[6], w[7]);
                 }
             };
+            // Where columns n of this lane go (n = 0: the tile's first), and how many are left.
+            const size_t first = KRAGGED ? 0 : (size_t)plan.start[sg.g] + sg.c0;
+            const int turned = OP == kFp8 && sg.turned, at0 = sg.l * kMaxCols;
+            uint16_t *to16 = out16;
+            size_t to = 0;
+            int room = 0;
+            if (turned) {  // a token's row
+                to16 += (first + row) * p.lanes + at0;
+                room = row < sg.cols ? p.lanes - at0 : 0;
+            } else if (KRAGGED) {  // a row of the map's gradient
+                to = ((size_t)sg.g * p.lanes + chan) * p.cols + sg.c0;
+                room = live ? p.cols - sg.c0 : 0;
+            } else {
+                to16 += (first + (lane & 1)) * p.lanes + (chan & ~1);
+                room = sg.cols - (lane & 1);
+            }
+            const bool words = p.lanes % 2 == 0 && reinterpret_cast<uintptr_t>(p.out) % 4 == 0;
             // Columns n .. n + 15 (of the tile) of this lane.
             const auto store = [&](int n, const float (&v)[kStep]) {
-                if (OP == kFp8 && sg.turned) {  // a token's row
-                    const int at = sg.l * kMaxCols + n;
-                    if (row < sg.cols)
-                        store_row(out16 + ((size_t)plan.start[sg.g] + sg.c0 + row) * p.lanes + at, v,
-                                  p.lanes - at);
+                const int left = room - n;
+                if (turned) {
+                    store_row(to16 + n, v, left);
                 } else if constexpr (!KRAGGED) {
                     // Tokens as columns: two a word; neighbouring lanes exchange, so that the
                     // even lane stores both lanes' values of the first column and the odd
                     // lane those of the second.
-                    const bool words =
-                        p.lanes % 2 == 0 && reinterpret_cast<uintptr_t>(p.out) % 4 == 0;
                     const uint32_t pick = lane & 1 ? 0x3276u : 0x5410u;
-                    uint16_t *at = out16 + (chan & ~1) +
-                                   ((size_t)plan.start[sg.g] + sg.c0 + n + (lane & 1)) * p.lanes;
-                    const int left = sg.cols - n - (lane & 1);
+                    uint16_t *at = to16 + (size_t)n * p.lanes;
 #pragma unroll
                     for (int j = 0; j < kStep / 2; ++j, at += 2 * (size_t)p.lanes) {
                         const uint32_t mine2 = pack_bf16(v, j);
@@ -870,17 +941,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if ((chan | 1) < p.lanes) at[1] = (uint16_t)(both >> 16);
                         }
                     }
-                } else if (live) {  // a row of the map's gradient
-                    const size_t at = ((size_t)sg.g * p.lanes + chan) * p.cols + sg.c0 + n;
-                    const int left = p.cols - sg.c0 - n;
-                    if (!p.f32) {
-                        store_row(out16 + at, v, left);
-                        return;
-                    }
+                } else if (!p.f32) {
+                    store_row(out16 + to + n, v, left);
+                } else {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         if (8 * h >= left) break;
-                        float *o = static_cast<float *>(p.out) + at + 8 * h;
+                        float *o = static_cast<float *>(p.out) + to + n + 8 * h;
                         float f[8];
 #pragma unroll
                         for (int j = 0; j < 8; ++j) f[j] = v[8 * h + j];
@@ -921,13 +988,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return p.part +
                            (size_t)(2 * (kCtas * c + rank) + sg.slot(c)) * p.nmax * kTileRows + row;
                 };
-                float *to = part_of(pair) + n0 * kTileRows;
+                float *part = part_of(pair) + n0 * kTileRows;
 #pragma unroll
                 for (int i = 0; i < kSteps; ++i) {
                     if (i >= steps) break;
 #pragma unroll
                     for (int j = 0; j < kStep; ++j)
-                        __stcg(to + (i * kStep + j) * kTileRows, sum[i][j]);
+                        __stcg(part + (i * kStep + j) * kTileRows, sum[i][j]);
                 }
                 // the warp's parts, then lane 0's fence and count; and the other way round: what
                 // lane 0 finds counted, its fence, then the warp's reads (a shuffle orders no

@@ -50,13 +50,14 @@ struct ProductParams {
     int f32, accumulate;     // gradient of the maps: type, added to what is there
 };
 
-// Columns a part needs for M rows of tokens (a group of kProductTurnFrom tokens may
-// have tiles of 256 channels).
+// Columns a part needs for M rows of tokens (an 8-bit group of kProductTurnFrom
+// tokens or more may have tiles of 128 channels).
 constexpr int kProductTurnFrom = 81;
+static_assert(kProductTurnFrom > 64, "parts of 128 columns");
 inline int product_nmax(int M) {
     int n = 16;
     while (n < M && n < kProductMaxCols) n *= 2;
-    return M >= kProductTurnFrom ? kProductMaxCols : n;
+    return n;
 }
 
 inline size_t product_part_bytes(int nmax) {
