@@ -93,14 +93,34 @@ __device__ __forceinline__ int width_of(int cols, int k) {
     return k <= 1 ? (cols + 15) / 16 * 16 : ((cols + k - 1) / k + 15) / 16 * 16;
 }
 
-// Blocks [k0, k1) of k of a tile of a pair's (a CTA's) work: lane tile l, columns
-// from c0 on.  The tile is summed over `parts` pairs from p0 on; pair c keeps its
-// part in slot 0 unless it is p0.
+// Blocks [k0, k1) of k of a tile of a pair's (a CTA's) work: channel tile l, tokens
+// (or the maps' columns) from c0 on.
 struct Seg {
     int g, l, c0, cols, k0, k1;   // (g < 0: no more)
     int turned;                   // tokens are the lanes
-    int p0, parts, slot0;
-    __device__ int slot(int c) const { return c == p0 ? slot0 : 0; }
+    int whole, t;                 // the sum is whole; else t: the tile among the cut ones
+    int p0, parts;                // (kWeightGrad)
+};
+
+// How groups are divided into tiles.
+template <Op OP>
+struct Shape {
+    static constexpr int kLanes = ctas_of(OP) * kTileRows;
+    int turn_from;  // tokens that make a group's tiles turned
+    int shift;      // columns of a tile that is not, at most: 1 << shift
+
+    __device__ bool turned(int c) const { return OP == kFp8 && c >= turn_from; }
+    // Tiles along the channels, and along `c` tokens (or the maps' columns).
+    __device__ int ltiles(int c, int lanes) const {
+        return turned(c) ? (lanes + kMaxCols - 1) / kMaxCols : (lanes + kLanes - 1) / kLanes;
+    }
+    __device__ int mtiles(int c) const {
+        return turned(c) ? (c + kTileRows - 1) / kTileRows : (c + (1 << shift) - 1) >> shift;
+    }
+    // Columns of a tile, and the tokens (or columns) from one tile to the next.
+    __device__ int width(int c) const { return turned(c) ? kMaxCols : width_of(c, mtiles(c)); }
+    __device__ int stride(int c) const { return turned(c) ? kTileRows : width(c); }
+    __device__ int tiles(int c, int lanes) const { return mtiles(c) * ltiles(c, lanes); }
 };
 
 // Turned tiles (kFp8).  A group with many tokens has them as the lanes, 128 a
@@ -115,30 +135,19 @@ struct Seg {
 template <Op OP>
 struct Plan {
     static constexpr bool KRAGGED = OP == kWeightGrad;
-    static constexpr int kLanes = ctas_of(OP) * kTileRows;
+    using Shape = product::Shape<OP>;
 
     int first[kProductMaxGroups + 1];   // tiles of the groups before, in this order
     int count[kProductMaxGroups];       // tokens of a group
     int start[kProductMaxGroups];       // its first row
     uint16_t order[kProductMaxGroups];
-    int hist[kClasses];
-    int turn_from;                      // tokens that make a group's tiles turned
+    uint16_t tally[kProductMaxGroups / 32][kClasses];  // groups of a class among 32 groups
+    int base[kClasses];                 // groups of the classes above
+    int sums[4], most_tokens;           // tiles by their widest form; the largest group
+    int scan[kThreads / 32];
+    Shape shape;
     int waves, rest, share, blocks;     // share: pairs for each of the rest (kWeightGrad)
     int parts, grain, q, more;          // the cut of the rest (tokens as columns)
-
-    __device__ bool turned(int c) const { return OP == kFp8 && c >= turn_from; }
-    // Tiles along the channels, and along `c` tokens (or the maps' columns).
-    __device__ int ltiles(int c, int lanes) const {
-        const int l = turned(c) ? kMaxCols : kLanes;
-        return (lanes + l - 1) / l;
-    }
-    __device__ int mtiles(int c) const {
-        const int most = OP == kFp8 ? (turned(c) ? kTileRows : kFp8Cols) : kMaxCols;
-        return (c + most - 1) / most;
-    }
-    // Columns of a tile, and the tokens (or columns) from one tile to the next.
-    __device__ int width(int c) const { return turned(c) ? kMaxCols : width_of(c, mtiles(c)); }
-    __device__ int stride(int c) const { return turned(c) ? kTileRows : width(c); }
 
     __device__ void tile(int t, const ProductParams &p, Seg &s) const {
         int lo = 0, hi = p.G - 1;
@@ -147,15 +156,20 @@ struct Plan {
             if (first[mid] <= t) lo = mid; else hi = mid - 1;
         }
         s.g = order[lo];
-        const int c = KRAGGED ? p.cols : count[s.g], k = mtiles(c), u = t - first[lo];
-        const int w = stride(c), block = u / (kRowGroup * k);
-        const int in = min(kRowGroup, ltiles(c, p.lanes) - block * kRowGroup);
-        const int v = u - block * kRowGroup * k;
-        const int m = v / in;
-        s.l = block * kRowGroup + v - m * in;
-        s.c0 = m * w;
-        s.cols = min(w, c - s.c0);
-        s.turned = turned(c);
+        const int c = KRAGGED ? p.cols : count[s.g], k = shape.mtiles(c), u = t - first[lo];
+        s.turned = shape.turned(c);
+        s.l = u;
+        s.c0 = 0;
+        s.cols = c;
+        if (k > 1) {
+            const int w = shape.stride(c), block = u / (kRowGroup * k);
+            const int in = min(kRowGroup, shape.ltiles(c, p.lanes) - block * kRowGroup);
+            const int v = u - block * kRowGroup * k;
+            const int m = v / in;
+            s.l = block * kRowGroup + v - m * in;
+            s.c0 = m * w;
+            s.cols = min(w, c - s.c0);
+        }
     }
     __device__ Cut cut() const {
         Cut c(0, 0, grain);
@@ -186,9 +200,7 @@ struct Work {
     }
     __device__ bool next(const ProductParams &p, Seg &s) {
         const int pair = blockIdx.x / ctas_of(OP), pairs = gridDim.x / ctas_of(OP);
-        s.p0 = pair;
-        s.parts = 1;
-        s.slot0 = 0;
+        s.whole = 1;
         if constexpr (KRAGGED) {
             if (end != 0) {
                 end = 0;
@@ -196,13 +208,16 @@ struct Work {
                 if (t < plan.rest) {
                     plan.tile(plan.waves * pairs + t, p, s);
                     const int b = blocks_of(s.g), n = min(share, max(1, b / kMinPart));
-                    if (part < n) {
+                    s.k0 = 0;
+                    s.k1 = b;
+                    if (n > 1 && part < n) {
                         s.k0 = (int)((long long)b * part / n);
                         s.k1 = (int)((long long)b * (part + 1) / n);
+                        s.whole = 0;
                         s.p0 = t * share;
                         s.parts = n;
-                        return true;
                     }
+                    if (part < n) return true;
                 }
             }
         } else if (u < end) {
@@ -211,12 +226,8 @@ struct Work {
             s.k0 = u - t * blocks;
             s.k1 = min(s.k0 + end - u, blocks);
             u += s.k1 - s.k0;
-            if (s.k0 != 0 || s.k1 != blocks) {
-                const Parts pt(plan.cut(), t, blocks);
-                s.p0 = pt.c0;
-                s.parts = pt.count();
-                s.slot0 = pt.slot0;
-            }
+            s.whole = s.k0 == 0 && s.k1 == blocks;
+            s.t = t;
             return true;
         }
         if (wave >= plan.waves) {
@@ -230,6 +241,24 @@ struct Work {
         return true;
     }
 };
+
+// The steps of kStep columns of a tile that one half of the epilogue's warps (and,
+// in 8 bits, of an accumulator) takes.
+constexpr int kHalfCols = kMaxCols / 2;
+struct Half {
+    int first, steps;
+    __device__ Half(bool turned, int cols, int h) {
+        const int all = (cols + kStep - 1) / kStep;
+        first = turned ? h * kSteps : (h ? (all + 1) / 2 : 0);
+        steps = turned ? kSteps : (h ? all / 2 : (all + 1) / 2);
+    }
+};
+
+// 8-bit: blocks of k that half an accumulator holds side by side.  (A meeting of
+// the issuer and the epilogue takes about 1000 cycles, whatever it is about.)
+__device__ __forceinline__ int blocks_each(bool turned, int cols) {
+    return turned ? 1 : (cols <= kMaxCols / 4 ? 4 : 2);
+}
 
 // Bytes that `cols` columns of a tile take of a CTA's stage.
 template <Op OP>
@@ -299,10 +328,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tid == 0) {
             ptx::mbar_init(&drained, OP == kFp8 ? 2 : 1);
             s_failed = 0;
-            // (a turned tile's rows are stored 8 channels at a time)
-            plan.turn_from = OP == kFp8 && p.lanes % 8 == 0 &&
-                                     reinterpret_cast<uintptr_t>(p.out) % 16 == 0
-                                 ? kProductTurnFrom : INT32_MAX;
+            plan.most_tokens = 0;
+            for (int i = 0; i < 4; ++i) plan.sums[i] = 0;
         }
         ptx::fence_mbar_init();
     }
@@ -311,8 +338,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::prefetch_map(&map_b);
         if (!B_MN) tc::prefetch_map(&map_b8);
     }
-    if (tid < kClasses) plan.hist[tid] = 0;
+    const int pairs = gridDim.x / kCtas, chunks = (p.G + 31) / 32;
+    for (int i = tid; i < chunks * kClasses / 2; i += kThreads)
+        reinterpret_cast<uint32_t *>(&plan.tally[0][0])[i] = 0;
+    // (a turned tile's rows are stored 8 channels at a time)
+    Shape<OP> shape;
+    shape.turn_from = OP == kFp8 && p.lanes % 8 == 0 &&
+                              reinterpret_cast<uintptr_t>(p.out) % 16 == 0
+                          ? kProductTurnFrom : INT32_MAX;
+    constexpr int kShift = OP == kFp8 ? 7 : 8;
+    static_assert(1 << kShift == (OP == kFp8 ? kFp8Cols : kMaxCols), "columns of a tile");
+    shape.shift = kShift;
+    __syncthreads();
     ptx::grid_dependency_wait();  // nothing of the caller's memory is touched before
+    int sums[4] = {0, 0, 0, 0}, most = 0;
     for (int g = tid; g < p.G; g += kThreads) {
         int at = 0, c = p.M;
         if (p.offsets != nullptr) {  // in bounds whatever they hold
@@ -324,86 +363,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         plan.start[g] = at;
         plan.count[g] = c;
-        if (p.G == 1) plan.order[g] = 0;
+        plan.order[g] = (uint16_t)g;
+        most = max(most, c);
+        sums[0] += shape.tiles(KRAGGED ? p.cols : c, p.lanes);
+        for (int i = 1; i < 4; ++i) sums[i] += (c + (128 >> (i - 1)) - 1) >> (8 - i);
+    }
+    // (groups that this warp has none of leave the sums as they are)
+    if (warp * 32 < p.G) {
+        for (int i = 0; i < 4; ++i) {
+            const int n = __reduce_add_sync(0xffffffffu, sums[i]);
+            if (lane == 0) atomicAdd(&plan.sums[i], n);
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) atomicMax(&plan.most_tokens, most);
     }
     tc::fence_before_sync();
     __syncthreads();
     // the pair's barriers are set up before either arrives on the other's
     if (PAIR) ptx::cluster_arrive();
-    // groups by the work of a tile, stable: its columns, or (to a half power of two)
-    // its blocks of k
-    const auto class_of = [&](int g) {
-        if (!KRAGGED) return plan.width(plan.count[g]) / 16;
-        const int b = (plan.count[g] + 63) / 64;
-        if (b < 2) return b;
-        const int e = 31 - __clz(b);
-        return min(kClasses - 1, 2 * e + (b >> (e - 1) & 1));
-    };
-    if (p.G > 1) {
-        for (int g = tid; g < p.G; g += kThreads) atomicAdd(&plan.hist[class_of(g)], 1);
-        __syncthreads();
-        for (int mine = warp; mine < kClasses; mine += kThreads / 32) {
-            if (plan.hist[mine] == 0) continue;
-            int at = 0;
-            for (int w = mine + 1; w < kClasses; ++w) at += plan.hist[w];
-            for (int g0 = 0; g0 < p.G; g0 += 32) {
-                const bool hit = g0 + lane < p.G && class_of(g0 + lane) == mine;
-                const unsigned m = __ballot_sync(0xffffffffu, hit);
-                if (hit) plan.order[at + __popc(m & ((1u << lane) - 1u))] = (uint16_t)(g0 + lane);
-                at += __popc(m);
+    // Few tiles: narrower ones while each still finds an idle pair (333 x 1000 x 1040 in
+    // 8 bits: 12 turned tiles of nine blocks, or 56 of 48 columns).
+    int tiles = plan.sums[0];
+    if (!KRAGGED && tiles * 2 <= pairs) {
+        const int l = (p.lanes + kLanes - 1) / kLanes;
+        for (int i = 1; i < 4; ++i)
+            if (plan.sums[i] * l <= pairs) {
+                shape.turn_from = INT32_MAX;
+                shape.shift = 8 - i;
+                tiles = plan.sums[i] * l;
             }
-        }
-        __syncthreads();
     }
-    if (warp == 0) {  // exclusive prefix of the groups' tiles
-        int sum = 0;
-        for (int g0 = 0; g0 < p.G; g0 += 32) {
-            const int g = g0 + lane;
-            int n = 0;
-            if (g < p.G) {
-                const int c = KRAGGED ? p.cols : plan.count[plan.order[g]];
-                n = plan.mtiles(c) * plan.ltiles(c, p.lanes);
-            }
-            int s = n;
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, s, o);
-                if (lane >= o) s += v;
-            }
-            if (g < p.G) plan.first[g] = sum + s - n;
-            sum += __shfl_sync(0xffffffffu, s, 31);
-        }
-        if (lane == 0) plan.first[p.G] = sum;
-    }
-    __syncthreads();
-
-    const uint32_t taddr = s_taddr;
-    const int blocks = KRAGGED ? 0 : (p.depth + kBlock - 1) / kBlock;
     // the widest tile decides how many stages the ring has
-    int widest = 16;
-    if (KRAGGED) {
-        widest = plan.width(p.cols);
-    } else if (p.G == 1) {
-        widest = max(16, plan.width(plan.count[0]));
-    } else {
-        for (int w = 2; w <= kMaxCols / 16; ++w)
-            if (plan.hist[w] != 0) widest = 16 * w;
-    }
-    const int stage_bytes = kLaneBytes + col_bytes<OP>(widest);
-    const int stages = min(kMaxStages, (kDynamic - 1024) / stage_bytes);
-    auto a_of = [&](uint32_t s) { return smem + s * stage_bytes; };
-    auto b_of = [&](uint32_t s) { return smem + s * stage_bytes + kLaneBytes; };
-    if (tid == 0) {
+    const int blocks = KRAGGED ? 0 : (p.depth + kBlock - 1) / kBlock;
+    int widest = max(16, KRAGGED ? shape.width(p.cols)
+                                 : min(1 << shape.shift, (plan.most_tokens + 15) / 16 * 16));
+    if (shape.turned(plan.most_tokens)) widest = kMaxCols;
+    if (tid == kThreads - 1) {
         // Whole waves are dealt out as they are; the rest (and one wave more where the
         // rest is under a quarter of a wave) is cut.
-        const int tiles = plan.first[p.G], pairs = gridDim.x / kCtas;
         int waves = tiles / pairs, rest = tiles - waves * pairs;
         if (!KRAGGED && waves > 0 && rest != 0 && rest * 4 < pairs) --waves;
         rest = tiles - waves * pairs;
+        plan.shape = shape;
         plan.waves = waves;
         plan.rest = rest;
-        plan.share = rest ? max(1, pairs / rest) : 1;
         plan.blocks = blocks;
-        if constexpr (!KRAGGED) {
+        if constexpr (KRAGGED) {
+            plan.share = rest ? max(1, pairs / rest) : 1;
+        } else {
             const Cut ct = widest <= 32 ? cut<true>(rest, blocks, pairs, 4 + widest / 16)
                                         : cut<false>(rest, blocks, pairs, 4 + widest / 16);
             plan.parts = ct.parts;
@@ -412,6 +419,86 @@ __global__ void __launch_bounds__(kThreads, 1)
             plan.more = ct.more;
         }
     }
+    // Groups by the work of a tile, stable: its columns, or (to a half power of two)
+    // its blocks of k.  Where every pair has one tile at most the order is nothing.
+    if (p.G > 1 && tiles > pairs) {
+        const auto class_of = [&](int g) {
+            if (!KRAGGED) return shape.width(plan.count[g]) / 16;
+            const int b = (plan.count[g] + 63) / 64;
+            if (b < 2) return b;
+            const int e = 31 - __clz(b);
+            return min(kClasses - 1, 2 * e + (b >> (e - 1) & 1));
+        };
+        // of 32 groups at a time (a warp's): those of a class, and the place among them
+        constexpr int kTurns = (kProductMaxGroups / 32 + kThreads / 32 - 1) / (kThreads / 32);
+        int cls[kTurns], place[kTurns];
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) {
+            const int chunk = warp + i * (kThreads / 32), g = chunk * 32 + lane;
+            if (chunk >= chunks) break;
+            cls[i] = g < p.G ? class_of(g) : kClasses;
+            const unsigned same = __match_any_sync(0xffffffffu, cls[i]);
+            place[i] = __popc(same & ((1u << lane) - 1u));
+            if (place[i] == 0 && g < p.G) plan.tally[chunk][cls[i]] = (uint16_t)__popc(same);
+        }
+        __syncthreads();
+        if (tid < kClasses) {
+            int n = 0;
+            for (int k = 0; k < chunks; ++k) {
+                const int here = plan.tally[k][tid];
+                plan.tally[k][tid] = (uint16_t)n;
+                n += here;
+            }
+            plan.base[tid] = n;
+        }
+        __syncthreads();
+        if (warp == 0) {  // the classes above: classes 63 - 2 lane and the next lower one
+            const int hi = kClasses - 1 - 2 * lane, a = plan.base[hi], b = plan.base[hi - 1];
+            int n = a + b;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, n, o);
+                if (lane >= o) n += v;
+            }
+            plan.base[hi] = n - a - b;
+            plan.base[hi - 1] = n - b;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) {
+            const int chunk = warp + i * (kThreads / 32), g = chunk * 32 + lane;
+            if (chunk < chunks && g < p.G)
+                plan.order[plan.base[cls[i]] + plan.tally[chunk][cls[i]] + place[i]] = (uint16_t)g;
+        }
+        __syncthreads();
+    }
+    {  // exclusive prefix of the groups' tiles in this order
+        const int each = (p.G + kThreads - 1) / kThreads, g0 = tid * each;
+        const auto tiles_at = [&](int i) {
+            return shape.tiles(KRAGGED ? p.cols : plan.count[plan.order[i]], p.lanes);
+        };
+        int n = 0;
+        for (int i = g0; i < min(g0 + each, p.G); ++i) n += tiles_at(i);
+        int sum = n;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += v;
+        }
+        if (lane == 31) plan.scan[warp] = sum;
+        sum -= n;
+        if (p.G > 32 * each) {  // (else the first warp has all of them)
+            __syncthreads();
+            for (int w = 0; w < warp; ++w) sum += plan.scan[w];
+        }
+        for (int i = g0; i < min(g0 + each, p.G); ++i) {
+            plan.first[i] = sum;
+            sum += tiles_at(i);
+        }
+    }
+    const uint32_t taddr = s_taddr;
+    const int stage_bytes = kLaneBytes + col_bytes<OP>(widest);
+    const int stages = min(kMaxStages, (kDynamic - 1024) / stage_bytes);
+    auto a_of = [&](uint32_t s) { return smem + s * stage_bytes; };
+    auto b_of = [&](uint32_t s) { return smem + s * stage_bytes + kLaneBytes; };
     __syncthreads();
     if (PAIR) ptx::cluster_wait();
     tc::fence_after_sync();
@@ -458,6 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (;;) {
                     Seg sg;
                     if (OP == kFp8) {  // lists the tiles itself
+                        sg.g = -1;
                         const bool more = !s_failed && work.next(p, sg);
                         if (!ptx::mbar_park(&seg_free[sq.at], sq.parity ^ 1u, kWaitNs)) {
                             s_failed = 1;
@@ -578,33 +666,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const Seg sg = *sp;
                     mbar_arrive(&seg_free[sq.at]);
                     sq.next();
-                    // 8-bit: an accumulator's halves are filled and given back by themselves
-                    const int n = sg.turned ? kMaxCols / 2 : (sg.cols + 15) / 16 * 16;
+                    // 8-bit: an accumulator's halves are filled and given back by themselves,
+                    // this issuer's from column b0 of the tile on
+                    const int each = blocks_each(sg.turned, sg.cols);
+                    int n = (sg.cols + 15) / 16 * 16, b0 = 0;
+                    if (OP == kFp8) {
+                        const Half half(sg.turned, sg.cols, h);
+                        n = half.steps * kStep;
+                        b0 = half.first * kStep;
+                    }
                     const uint32_t idesc = (OP == kFp8 ? tc::idesc_e4m3_f32(kLanes, n)
                                                        : tc::idesc_bf16_f32(kLanes, n)) |
                                            kMajor;
-                    for (int kb = sg.k0; kb < sg.k1 && !s_failed; acc.next()) {
+                    for (int kb = sg.k0; kb < sg.k1 && !s_failed;) {
                         const int from = kb, to = kRun < sg.k1 - kb ? kb + kRun : sg.k1;
                         const uint32_t d = taddr + acc.at * kMaxCols;
                         if (!wait_for(&full[st.at], st.parity)) break;
                         if (OP == kFp8) {
                             const uint32_t at = st.at * (uint32_t)(stage_bytes / 16);
-                            // (not turned: all warps read what the first issuer's products left)
-                            if (!wait_for(&acc_free[acc.at][h], acc.parity ^ 1u) ||
-                                (h == 0 && !sg.turned &&
-                                 !wait_for(&acc_free[acc.at][1], acc.parity ^ 1u)))
+                            if ((kb == sg.k0 || kb % each == 0) &&
+                                !wait_for(&acc_free[acc.at][h], acc.parity ^ 1u))
                                 break;
-                            if (h == 0 || sg.turned) {
+                            if (n > 0) {
+                                const uint32_t col = h * kHalfCols + kb % each * (kHalfCols / each);
 #pragma unroll
                                 for (int kk = 0; kk < 4; ++kk)
-                                    tc::mma_f8(d + h * (kMaxCols / 2), ad0 + at + kk * kStepA,
-                                               bd0 + at + h * (kLaneBytes / 16) + kk * kStepB, idesc,
+                                    tc::mma_f8(d + col, ad0 + at + kk * kStepA,
+                                               bd0 + at + b0 * (kAtom / 16) + kk * kStepB, idesc,
                                                kk != 0);
                             }
-                            commit(&acc_full[acc.at][h]);
                             commit(&empty[st.at]);
                             ++kb;
                             st.next();
+                            if (kb == sg.k1 || kb % each == 0) {
+                                commit(&acc_full[acc.at][h]);
+                                acc.next();
+                            }
                             continue;
                         }
                         if (!wait_for(&acc_free[acc.at][0], acc.parity ^ 1u)) break;
@@ -621,6 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             commit(&empty[st.at]);
                         }
                         commit(&acc_full[acc.at][0]);
+                        acc.next();
                     }
                 }
                 commit(&drained);  // before tensor memory is freed
@@ -721,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) s_failed = 1;
             return ok;
         };
-        const auto release = [&] {  // the accumulator has been read
+        const auto release = [&] {  // the accumulator (8-bit: this half) has been read
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) {
@@ -734,22 +832,214 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Seg *const sp = listed(sq);
             if (__any_sync(0xffffffffu, sp == nullptr)) break;
             const Seg &sg = *sp;  // (stays there until the tile is stored)
-            int s0, steps;        // this warp's steps of kStep columns of the tile
+            const Half half(OP == kFp8 && sg.turned, sg.cols, hf);
+            int steps = half.steps;
             if (OP == kFp8 && sg.turned) {  // channels that exist, if a token of the warp does
-                s0 = hf * kSteps;
-                const int chans = p.lanes - sg.l * kMaxCols - s0 * kStep;
+                const int chans = p.lanes - sg.l * kMaxCols - half.first * kStep;
                 steps = q * 32 < sg.cols ? min(max((chans + kStep - 1) / kStep, 0), kSteps) : 0;
-            } else {
-                const int all = (sg.cols + kStep - 1) / kStep;
-                s0 = hf ? (all + 1) / 2 : 0;
-                steps = hf ? all / 2 : (all + 1) / 2;
             }
-            const int n0 = s0 * kStep, k0 = sg.k0, k1 = sg.k1;
-            float sum[kSteps][kStep];
+            const int n0 = half.first * kStep, k0 = sg.k0, k1 = sg.k1;
+            // Sums to the columns from `to` on (16 a step).
+            const auto keep = [&](uint32_t to, const auto &sum) {
+                constexpr int S = sizeof sum / sizeof sum[0];
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i)
+                for (int i = 0; i < S; ++i) {
+                    uint32_t v[kStep];
 #pragma unroll
-                for (int j = 0; j < kStep; ++j) sum[i][j] = 0.0f;
+                    for (int j = 0; j < kStep; ++j) v[j] = __float_as_uint(sum[i][j]);
+                    if (i < steps) tc::st_32x16(to + i * kStep, v);  // (no column more)
+                }
+                tc::wait_st();
+            };
+            const auto clear = [](auto &sum) {
+#pragma unroll
+                for (auto &step : sum)
+#pragma unroll
+                    for (float &v : step) v = 0.0f;
+            };
+            // What the sums (columns n0 + 16 i .. of this lane), kept in tensor memory, come
+            // to.  (Held in registers here they do not leave enough for the rest.)
+            const auto finish = [&](uint32_t from, bool none) {
+                const auto get = [&](int i, float (&v)[2][kStep]) {  // steps i and i + 1
+                    uint32_t u[2][kStep];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int j = 0; j < kStep; ++j) u[h][j] = 0;
+                    if (!none) {
+                        tc::ld_32x16(from + i * kStep, u[0]);
+                        if (i + 1 < steps) tc::ld_32x16(from + (i + 1) * kStep, u[1]);
+                        tc::wait_ld(u[0]);
+                        tc::after_wait(u[1]);
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int j = 0; j < kStep; ++j) v[h][j] = __uint_as_float(u[h][j]);
+                };
+                // the lane's channel (not turned)
+                const int chan = sg.l * kLanes + rank * kTileRows + row;
+                const bool live = chan < p.lanes;
+                uint16_t *const out16 = static_cast<uint16_t *>(p.out);
+                // values 2 j and 2 j + 1
+                const auto pack_bf16 = [](const float (&v)[kStep], int j) {
+                    const __nv_bfloat162 o = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+                    return *reinterpret_cast<const uint32_t *>(&o);
+                };
+                // 16 neighbouring values of a row of `left` more, `left` a multiple of 8
+                const bool whole32 = (KRAGGED ? p.cols : p.lanes) % 16 == 0 &&
+                                     reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
+                const auto store_row = [&](uint16_t *o, const float (&v)[kStep], int left) {
+                    if (left <= 0) return;
+                    uint32_t w[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) w[j] = pack_bf16(v, j);
+                    if (whole32) {
+                        store_256(o, w);
+                    } else {
+                        reinterpret_cast<uint4 *>(o)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                        if (left > 8)
+                            reinterpret_cast<uint4 *>(o)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                    }
+                };
+                // Where columns n of this lane go (n = 0: the tile's first), and how many are left.
+                const size_t first = KRAGGED ? 0 : (size_t)plan.start[sg.g] + sg.c0;
+                const int turned = OP == kFp8 && sg.turned, at0 = sg.l * kMaxCols;
+                uint16_t *to16 = out16;
+                size_t to = 0;
+                int room = 0;
+                if (turned) {  // a token's row
+                    to16 += (first + row) * p.lanes + at0;
+                    room = row < sg.cols ? p.lanes - at0 : 0;
+                } else if (KRAGGED) {  // a row of the map's gradient
+                    to = ((size_t)sg.g * p.lanes + chan) * p.cols + sg.c0;
+                    room = live ? p.cols - sg.c0 : 0;
+                } else {
+                    to16 += (first + (lane & 1)) * p.lanes + (chan & ~1);
+                    room = sg.cols - (lane & 1);
+                }
+                const bool words = p.lanes % 2 == 0 && reinterpret_cast<uintptr_t>(p.out) % 4 == 0;
+                // Columns n .. n + 15 (of the tile) of this lane.
+                const auto store = [&](int n, const float (&v)[kStep]) {
+                    const int left = room - n;
+                    if (turned) {
+                        store_row(to16 + n, v, left);
+                    } else if constexpr (!KRAGGED) {
+                        // Tokens as columns: two a word; neighbouring lanes exchange, so that the
+                        // even lane stores both lanes' values of the first column and the odd
+                        // lane those of the second.
+                        const uint32_t pick = lane & 1 ? 0x3276u : 0x5410u;
+                        uint16_t *at = to16 + (size_t)n * p.lanes;
+#pragma unroll
+                        for (int j = 0; j < kStep / 2; ++j, at += 2 * (size_t)p.lanes) {
+                            const uint32_t mine2 = pack_bf16(v, j);
+                            const uint32_t both =
+                                __byte_perm(mine2, __shfl_xor_sync(0xffffffffu, mine2, 1), pick);
+                            if (words) {
+                                if (live && 2 * j < left) *reinterpret_cast<uint32_t *>(at) = both;
+                            } else if (2 * j < left) {  // odd extent or address: rows start off a word
+                                if ((chan & ~1) < p.lanes) at[0] = (uint16_t)both;
+                                if ((chan | 1) < p.lanes) at[1] = (uint16_t)(both >> 16);
+                            }
+                        }
+                    } else if (!p.f32) {
+                        store_row(out16 + to + n, v, left);
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (8 * h >= left) break;
+                            float *o = static_cast<float *>(p.out) + to + n + 8 * h;
+                            float f[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) f[j] = v[8 * h + j];
+                            if (p.accumulate) {
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    const float4 old = reinterpret_cast<const float4 *>(o)[j];
+                                    f[4 * j] = old.x + f[4 * j];
+                                    f[4 * j + 1] = old.y + f[4 * j + 1];
+                                    f[4 * j + 2] = old.z + f[4 * j + 2];
+                                    f[4 * j + 3] = old.w + f[4 * j + 3];
+                                }
+                            }
+                            if (reinterpret_cast<uintptr_t>(p.out) % 32 == 0) {
+                                uint32_t w[8];
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(f[j]);
+                                store_256(o, w);
+                            } else {
+                                reinterpret_cast<float4 *>(o)[0] = make_float4(f[0], f[1], f[2], f[3]);
+                                reinterpret_cast<float4 *>(o)[1] = make_float4(f[4], f[5], f[6], f[7]);
+                            }
+                        }
+                    }
+                };
+                if (sg.whole) {
+                    // (adding nothing to what is there: left alone)
+                    if (KRAGGED && p.accumulate && none) return;
+#pragma unroll 1
+                    for (int i = 0; i < steps; i += 2) {
+                        float v[2][kStep];
+                        get(i, v);
+                        store(n0 + i * kStep, v[0]);
+                        if (i + 1 < steps) store(n0 + (i + 1) * kStep, v[1]);
+                    }
+                } else if (steps > 0) {
+                    const int pair = blockIdx.x / kCtas;
+                    // summed over `parts` pairs from p0 on; pair c keeps its part in slot 0
+                    // unless it is p0
+                    int p0 = sg.p0, parts = sg.parts, slot0 = 0;
+                    if (!KRAGGED) {
+                        const Parts pt(plan.cut(), sg.t, plan.blocks);
+                        p0 = pt.c0;
+                        parts = pt.count();
+                        slot0 = pt.slot0;
+                    }
+                    auto part_of = [&](int c) {
+                        const int slot = c == p0 ? slot0 : 0;
+                        return p.part + (size_t)(2 * (kCtas * c + rank) + slot) * p.nmax * kTileRows +
+                               row;
+                    };
+                    float *part = part_of(pair) + n0 * kTileRows;
+#pragma unroll 1
+                    for (int i = 0; i < steps; i += 2) {
+                        float v[2][kStep];
+                        get(i, v);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            if (i + h < steps)
+#pragma unroll
+                                for (int j = 0; j < kStep; ++j)
+                                    __stcg(part + ((i + h) * kStep + j) * kTileRows, v[h][j]);
+                    }
+                    // the warp's parts, then lane 0's fence and count; and the other way round: what
+                    // lane 0 finds counted, its fence, then the warp's reads (a shuffle orders no
+                    // memory)
+                    __syncwarp();
+                    __threadfence();
+                    int last = 0;
+                    if (lane == 0) {
+                        int *m = &p.header->merged[hf][kCtas * p0 + rank][q];
+                        last = atomicAdd(m, 1) == parts - 1;
+                        if (last) *m = 0;  // for the next call
+                        __threadfence();
+                    }
+                    last = __shfl_sync(0xffffffffu, last, 0);
+                    __syncwarp();
+                    for (int i = 0; last && i < steps; ++i) {
+                        const int n = n0 + i * kStep;
+                        float v[kStep];
+#pragma unroll
+                        for (int j = 0; j < kStep; ++j) v[j] = 0.0f;
+                        for (int c = p0; c < p0 + parts; ++c) {
+                            const float *f = part_of(c) + (size_t)n * kTileRows;
+#pragma unroll
+                            for (int j = 0; j < kStep; ++j) v[j] += __ldcg(f + j * kTileRows);
+                        }
+                        store(n, v);
+                    }
+                }
+            };
             if constexpr (OP == kFp8) {
                 const auto scales = [&](int kb) {  // of block kb; (a new run's: once they are there)
                     if (kb % kScaleRun == 0 || kb == k0) wait_for(&sc_full[sc.at], sc.parity);
@@ -767,6 +1057,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // accumulator's half has been given back.
                     constexpr int kHeld = 32;
                     uint32_t u[2][kHeld];
+                    float sum[kSteps][kStep];
+                    clear(sum);
                     const auto add = [&](const uint32_t (&v)[kHeld], int at, float f) {
 #pragma unroll
                         for (int j = 0; j < kHeld; j += 2) {
@@ -810,7 +1102,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float f = r < 2 ? (r == 0 ? f4.x : f4.y) : (r == 2 ? f4.z : f4.w);
                         if (!wait_for(&acc_full[acc.at][hf], acc.parity)) break;
                         tc::fence_after_sync();
-                        const uint32_t from = mine + acc.at * kMaxCols + hf * (kMaxCols / 2);
+                        const uint32_t from = mine + acc.at * kMaxCols + hf * kHalfCols;
                         tc::ld_32x32(from, u[0]);
                         tc::ld_32x32(from + 32, u[1]);
                         tc::wait_ld(u[0]);
@@ -821,208 +1113,113 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc::ld_32x32(from + 96, u[1]);
                         tc::wait_ld(u[0]);
                         tc::wait_ld(u[1]);
-                        release();
+                        if (kb + 1 < k1) release();
                         add(u[0], 64, f);
                         add(u[1], 96, f);
                     }
+                    if (ok) {
+                        const uint32_t at = mine + acc.at * kMaxCols + hf * kHalfCols;
+                        keep(at, sum);
+                        finish(at, false);
+                        release();
+                    }
                 } else {
-                    for (int kb = k0; kb < k1; ++kb) {
-                        const float4 *fs = reinterpret_cast<const float4 *>(scales(kb) + n0);
-                        if (!ok || !wait_for(&acc_full[acc.at][0], acc.parity)) break;
+                    constexpr int kNarrow = kFp8Cols / 2 / kStep;  // steps, at most
+                    const int each = blocks_each(false, sg.cols);
+                    float sum[kNarrow][kStep];
+                    clear(sum);
+                    const auto add = [&](float (&t)[kStep], const uint32_t (&v)[kStep], const float *f) {
+#pragma unroll
+                        for (int j = 0; j < kStep / 4; ++j) {
+                            const float4 f4 = reinterpret_cast<const float4 *>(f)[j];
+                            t[4 * j] = __fmaf_rn(__uint_as_float(v[4 * j]), f4.x, t[4 * j]);
+                            t[4 * j + 1] = __fmaf_rn(__uint_as_float(v[4 * j + 1]), f4.y, t[4 * j + 1]);
+                            t[4 * j + 2] = __fmaf_rn(__uint_as_float(v[4 * j + 2]), f4.z, t[4 * j + 2]);
+                            t[4 * j + 3] = __fmaf_rn(__uint_as_float(v[4 * j + 3]), f4.w, t[4 * j + 3]);
+                        }
+                    };
+                    const uint32_t mine_half = mine + hf * kHalfCols;
+                    for (int kb = k0; ok && kb < k1;) {
+                        const int to = min(k1, (kb / each + 1) * each);
+                        if (!wait_for(&acc_full[acc.at][hf], acc.parity)) break;
+                        tc::fence_after_sync();
+                        const uint32_t from = mine_half + acc.at * kMaxCols;
+                        if (steps <= 1) {  // (at most 48 columns: four blocks) all at once
+                            const float *f = scales(kb) - kb % 4 * kFp8Cols + n0;
+                            uint32_t u[4][kStep];
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                tc::ld_32x16(from + r * (kHalfCols / 4), u[r]);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) tc::wait_ld(u[r]);
+                            if (to < k1) release();
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                if (steps > 0 && r >= kb % 4 && r <= (to - 1) % 4)
+                                    add(sum[0], u[r], f + r * kFp8Cols);
+                            scales_read(to - 1);
+                        } else {
+                            for (int b = kb; ok && b < to; ++b) {
+                                const float *f = scales(b) + n0;
+                                const uint32_t at = from + b % each * (kHalfCols / each);
+                                uint32_t u[2][kStep];  // (the loads of the next step are in flight)
+                                tc::ld_32x16(at, u[0]);
+#pragma unroll
+                                for (int i = 0; i < kNarrow; ++i) {
+                                    if (i >= steps) break;
+                                    tc::wait_ld(u[i & 1]);
+                                    // (the last one once more: past it may be no column)
+                                    tc::ld_32x16(at + min(i + 1, steps - 1) * kStep, u[(i + 1) & 1]);
+                                    add(sum[i], u[i & 1], f + i * kStep);
+                                }
+                                scales_read(b);
+                            }
+                            if (to < k1) release();
+                        }
+                        kb = to;
+                    }
+                    if (ok) {  // (kept where the last block was)
+                        const uint32_t at = mine_half + acc.at * kMaxCols +
+                                            (k1 - 1) % each * (kHalfCols / each);
+                        keep(at, sum);
+                        finish(at, false);
+                        release();
+                    }
+                }
+            } else {
+                if (!KRAGGED || k1 - k0 <= kRun) {  // all of k in one accumulator, or nothing
+                    if (k0 < k1) wait_for(&acc_full[acc.at][0], acc.parity);
+                    tc::fence_after_sync();
+                } else {
+                    float sum[kSteps][kStep];
+                    clear(sum);
+                    for (int kb = k0; kb < k1;) {
+                        if (!wait_for(&acc_full[acc.at][0], acc.parity)) break;
                         tc::fence_after_sync();
                         const uint32_t from = mine + acc.at * kMaxCols + n0;
                         uint32_t u[2][kStep];  // (the loads of the next step are in flight)
-                        if (steps > 0) tc::ld_32x16(from, u[0]);
+                        tc::ld_32x16(from, u[0]);
 #pragma unroll
-                        for (int i = 0; i < kFp8Cols / 2 / kStep; ++i) {
+                        for (int i = 0; i < kSteps; ++i) {
                             if (i >= steps) break;
                             tc::wait_ld(u[i & 1]);
-                            if (i + 1 < steps)
+                            if (i + 1 < kSteps)
                                 tc::ld_32x16(from + (i + 1) * kStep, u[(i + 1) & 1]);
-                            float(&t)[kStep] = sum[i];
 #pragma unroll
-                            for (int j = 0; j < kStep / 4; ++j) {
-                                const float4 f4 = fs[i * (kStep / 4) + j];
-                                const uint32_t *v = &u[i & 1][4 * j];
-                                t[4 * j] = __fmaf_rn(__uint_as_float(v[0]), f4.x, t[4 * j]);
-                                t[4 * j + 1] = __fmaf_rn(__uint_as_float(v[1]), f4.y, t[4 * j + 1]);
-                                t[4 * j + 2] = __fmaf_rn(__uint_as_float(v[2]), f4.z, t[4 * j + 2]);
-                                t[4 * j + 3] = __fmaf_rn(__uint_as_float(v[3]), f4.w, t[4 * j + 3]);
-                            }
+                            for (int j = 0; j < kStep; ++j)
+                                sum[i][j] = __fadd_rn(sum[i][j], __uint_as_float(u[i & 1][j]));
                         }
-                        release();
-                        scales_read(kb);
+                        kb = kRun < k1 - kb ? kb + kRun : k1;
+                        if (kb < k1) release();
                     }
+                    if (ok) keep(mine + acc.at * kMaxCols + n0, sum);
                 }
-            } else {
-                for (int kb = k0; kb < k1; kb = kRun < k1 - kb ? kb + kRun : k1) {
-                    if (!wait_for(&acc_full[acc.at][0], acc.parity)) break;
-                    tc::fence_after_sync();
-                    const uint32_t from = mine + acc.at * kMaxCols + n0;
-                    uint32_t u[2][kStep];  // (the loads of the next step are in flight)
-                    if (steps > 0) tc::ld_32x16(from, u[0]);
-#pragma unroll
-                    for (int i = 0; i < kSteps; ++i) {
-                        if (i >= steps) break;
-                        tc::wait_ld(u[i & 1]);
-                        if (i + 1 < steps && i + 1 < kSteps)
-                            tc::ld_32x16(from + (i + 1) * kStep, u[(i + 1) & 1]);
-#pragma unroll
-                        for (int j = 0; j < kStep; ++j)
-                            sum[i][j] = __fadd_rn(sum[i][j], __uint_as_float(u[i & 1][j]));
-                    }
-                    release();
+                if (ok) {
+                    finish(mine + acc.at * kMaxCols + n0, k0 == k1);
+                    if (k0 < k1) release();
                 }
             }
             if (!ok) break;
-
-            // the lane's channel (not turned)
-            const int chan = sg.l * kLanes + rank * kTileRows + row;
-            const bool live = chan < p.lanes;
-            uint16_t *const out16 = static_cast<uint16_t *>(p.out);
-            // values 2 j and 2 j + 1
-            const auto pack_bf16 = [](const float (&v)[kStep], int j) {
-                const __nv_bfloat162 o = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-                return *reinterpret_cast<const uint32_t *>(&o);
-            };
-            // 16 neighbouring values of a row of `left` more, `left` a multiple of 8
-            const bool whole32 = (KRAGGED ? p.cols : p.lanes) % 16 == 0 &&
-                                 reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
-            const auto store_row = [&](uint16_t *o, const float (&v)[kStep], int left) {
-                if (left <= 0) return;
-                uint32_t w[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = pack_bf16(v, j);
-                if (whole32) {
-                    store_256(o, w);
-                } else {
-                    reinterpret_cast<uint4 *>(o)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                    if (left > 8)
-                        reinterpret_cast<uint4 *>(o)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                }
-            };
-            // Where columns n of this lane go (n = 0: the tile's first), and how many are left.
-            const size_t first = KRAGGED ? 0 : (size_t)plan.start[sg.g] + sg.c0;
-            const int turned = OP == kFp8 && sg.turned, at0 = sg.l * kMaxCols;
-            uint16_t *to16 = out16;
-            size_t to = 0;
-            int room = 0;
-            if (turned) {  // a token's row
-                to16 += (first + row) * p.lanes + at0;
-                room = row < sg.cols ? p.lanes - at0 : 0;
-            } else if (KRAGGED) {  // a row of the map's gradient
-                to = ((size_t)sg.g * p.lanes + chan) * p.cols + sg.c0;
-                room = live ? p.cols - sg.c0 : 0;
-            } else {
-                to16 += (first + (lane & 1)) * p.lanes + (chan & ~1);
-                room = sg.cols - (lane & 1);
-            }
-            const bool words = p.lanes % 2 == 0 && reinterpret_cast<uintptr_t>(p.out) % 4 == 0;
-            // Columns n .. n + 15 (of the tile) of this lane.
-            const auto store = [&](int n, const float (&v)[kStep]) {
-                const int left = room - n;
-                if (turned) {
-                    store_row(to16 + n, v, left);
-                } else if constexpr (!KRAGGED) {
-                    // Tokens as columns: two a word; neighbouring lanes exchange, so that the
-                    // even lane stores both lanes' values of the first column and the odd
-                    // lane those of the second.
-                    const uint32_t pick = lane & 1 ? 0x3276u : 0x5410u;
-                    uint16_t *at = to16 + (size_t)n * p.lanes;
-#pragma unroll
-                    for (int j = 0; j < kStep / 2; ++j, at += 2 * (size_t)p.lanes) {
-                        const uint32_t mine2 = pack_bf16(v, j);
-                        const uint32_t both =
-                            __byte_perm(mine2, __shfl_xor_sync(0xffffffffu, mine2, 1), pick);
-                        if (words) {
-                            if (live && 2 * j < left) *reinterpret_cast<uint32_t *>(at) = both;
-                        } else if (2 * j < left) {  // odd extent or address: rows start off a word
-                            if ((chan & ~1) < p.lanes) at[0] = (uint16_t)both;
-                            if ((chan | 1) < p.lanes) at[1] = (uint16_t)(both >> 16);
-                        }
-                    }
-                } else if (!p.f32) {
-                    store_row(out16 + to + n, v, left);
-                } else {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (8 * h >= left) break;
-                        float *o = static_cast<float *>(p.out) + to + n + 8 * h;
-                        float f[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) f[j] = v[8 * h + j];
-                        if (p.accumulate) {
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const float4 old = reinterpret_cast<const float4 *>(o)[j];
-                                f[4 * j] = old.x + f[4 * j];
-                                f[4 * j + 1] = old.y + f[4 * j + 1];
-                                f[4 * j + 2] = old.z + f[4 * j + 2];
-                                f[4 * j + 3] = old.w + f[4 * j + 3];
-                            }
-                        }
-                        if (reinterpret_cast<uintptr_t>(p.out) % 32 == 0) {
-                            uint32_t w[8];
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(f[j]);
-                            store_256(o, w);
-                        } else {
-                            reinterpret_cast<float4 *>(o)[0] = make_float4(f[0], f[1], f[2], f[3]);
-                            reinterpret_cast<float4 *>(o)[1] = make_float4(f[4], f[5], f[6], f[7]);
-                        }
-                    }
-                }
-            };
-            if (sg.parts == 1) {
-                // (adding nothing to what is there: left alone)
-                if (!(KRAGGED && p.accumulate && k0 == k1)) {
-#pragma unroll
-                    for (int i = 0; i < kSteps; ++i) {
-                        if (i >= steps) break;
-                        store(n0 + i * kStep, sum[i]);
-                    }
-                }
-            } else if (steps > 0) {
-                const int pair = blockIdx.x / kCtas;
-                auto part_of = [&](int c) {
-                    return p.part +
-                           (size_t)(2 * (kCtas * c + rank) + sg.slot(c)) * p.nmax * kTileRows + row;
-                };
-                float *part = part_of(pair) + n0 * kTileRows;
-#pragma unroll
-                for (int i = 0; i < kSteps; ++i) {
-                    if (i >= steps) break;
-#pragma unroll
-                    for (int j = 0; j < kStep; ++j)
-                        __stcg(part + (i * kStep + j) * kTileRows, sum[i][j]);
-                }
-                // the warp's parts, then lane 0's fence and count; and the other way round: what
-                // lane 0 finds counted, its fence, then the warp's reads (a shuffle orders no
-                // memory)
-                __syncwarp();
-                __threadfence();
-                int last = 0;
-                if (lane == 0) {
-                    int *m = &p.header->merged[hf][kCtas * sg.p0 + rank][q];
-                    last = atomicAdd(m, 1) == sg.parts - 1;
-                    if (last) *m = 0;  // for the next call
-                    __threadfence();
-                }
-                last = __shfl_sync(0xffffffffu, last, 0);
-                __syncwarp();
-                for (int i = 0; last && i < steps; ++i) {
-                    const int n = n0 + i * kStep;
-                    float v[kStep];
-#pragma unroll
-                    for (int j = 0; j < kStep; ++j) v[j] = 0.0f;
-                    for (int c = sg.p0; c < sg.p0 + sg.parts; ++c) {
-                        const float *f = part_of(c) + (size_t)n * kTileRows;
-#pragma unroll
-                        for (int j = 0; j < kStep; ++j) v[j] += __ldcg(f + j * kTileRows);
-                    }
-                    store(n, v);
-                }
-            }
             __syncwarp();
             if (lane == 0) mbar_arrive(&seg_free[sq.at]);
             sq.next();

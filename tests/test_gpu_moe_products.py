@@ -242,6 +242,28 @@ def test_fp8_groups(api, counts, N, H):
     assert handle.get_error() == (api.MOE_OK, 0)
 
 
+@pytest.mark.parametrize("seed,N,H", [(1, 1024, 256), (2, 1096, 720), (3, 520, 2048), (4, 1003, 640)])
+def test_fp8_many_tiles_of_every_width(api, seed, N, H):
+    """More tiles than SMs, groups of no token up to several tiles, in one call."""
+    rng = np.random.default_rng(seed)
+    G, M = 40, 600
+    counts = np.concatenate([rng.integers(0, 140, 20), rng.integers(0, M + 1, 20)])
+    counts[[3, 20, 39]] = 0
+    rng.shuffle(counts)
+    g = gen(seed)
+    handle = api.MoeGemmFp8(G, M, N, H, DEV)
+    xq, sx, wq, sw = fp8_inputs((G,), G, M, N, H, g)
+    cnt = torch.tensor(counts, dtype=torch.int32, device=DEV)
+    want = torch.full((G, M, N), 7.0, dtype=BF, device=DEV)
+    for e, c in enumerate(counts.tolist()):
+        want[e, :c] = fp8_ref(xq[e, :c], sx[e, :c], wq[e], sw[e])[0].to(BF)
+    for _ in range(3):
+        out = torch.full((G, M, N), 7.0, dtype=BF, device=DEV)
+        handle.gemm(xq, sx, wq, sw, counts=cnt, out=out)
+        assert torch.equal(out, want)
+    assert handle.get_error() == (api.MOE_OK, 0)
+
+
 def test_fp8_takes_what_the_quantiser_gives(api):
     rows, N, H = 70, 300, 1040
     g = gen(9)
@@ -360,6 +382,26 @@ def test_ragged_long(api, counts):
             # 2^-8 (and for fp32 below half of 2^-16) of the norm
             far = (got.double() - ref).norm() / ref.norm()
             assert far <= (2.0 ** -8 if got.dtype is BF else 2.0 ** -17)
+
+
+@pytest.mark.parametrize("seed", [1, 2, 3])
+def test_ragged_many_tiles_of_every_width(api, seed):
+    rng = np.random.default_rng(seed)
+    G, N, H = 37, 776, 520
+    counts = np.concatenate([rng.integers(0, 70, 20), rng.integers(0, 900, 17)])
+    counts[[0, 19, 36]] = 0
+    rng.shuffle(counts)
+    x, dy, w, off = ragged(counts.tolist(), N, H, gen(seed))
+    handle = api.MoeGemmRagged(G, x.shape[0], N, H, DEV)
+    y, dx = handle.forward(x, w, off), handle.input_grad(dy, w, off)
+    dw, dw32 = handle.weight_grad(dy, x, off), handle.weight_grad(dy, x, off, dtype=F32)
+    for e in range(G):
+        a, b = int(off[e]), int(off[e + 1])
+        assert torch.equal(y[a:b], (x[a:b].double() @ w[e].double().T).to(BF))
+        assert torch.equal(dx[a:b], (dy[a:b].double() @ w[e].double()).to(BF))
+        ref = dy[a:b].double().T @ x[a:b].double()
+        assert torch.equal(dw[e], ref.to(BF)) and torch.equal(dw32[e], ref.float())
+    assert handle.get_error() == (api.MOE_OK, 0)
 
 
 def test_ragged_gradients_against_differences(api):
