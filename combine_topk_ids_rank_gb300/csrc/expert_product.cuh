@@ -61,13 +61,14 @@ namespace product {
 
 using namespace stream;
 
-enum Op { kFp8, kForward, kInputGrad, kWeightGrad };
+enum Op { kFp8, kFp8Narrow, kForward, kInputGrad, kWeightGrad };
+constexpr bool is_fp8(Op op) { return op == kFp8 || op == kFp8Narrow; }
 
 constexpr int kEpiWarps = 8, kProducerWarp = 8, kMmaWarp = 9, kHelpWarp = 10, kListWarp = 11;
 constexpr int kThreads = 12 * 32;
-// Registers: 384 threads start with 168 each (64512); the epilogue's 256 go to 224, the
-// other 128 to 56, which is 64512 again.
-constexpr int kStartRegs = 168, kEpiRegs = 224, kOtherRegs = 56;
+// Registers: 384 threads start with 168 each (64512); the epilogue's 256 go to 200, the
+// other 128 to 104, which is 64512 again.
+constexpr int kStartRegs = 168, kEpiRegs = 200, kOtherRegs = 104;
 static_assert(kEpiWarps * 32 * kEpiRegs + (kThreads - kEpiWarps * 32) * kOtherRegs <=
                   kThreads * kStartRegs, "more registers than the block starts with");
 constexpr int kMaxCols = kProductMaxCols;
@@ -86,7 +87,7 @@ constexpr int kGradRun = 8;       // blocks of 64 rows of k that stay in tensor 
 constexpr int kMinPart = 4;       // blocks of k that make a part worth its way through memory
 constexpr int kFp8Cols = 128;     // columns of an 8-bit tile that is not turned, at most
 
-constexpr int ctas_of(Op op) { return op == kFp8 ? 1 : 2; }
+constexpr int ctas_of(Op op) { return is_fp8(op) ? 1 : 2; }
 
 // Columns of the `k` tiles of `cols` columns: evened out, a multiple of 16.
 __device__ __forceinline__ int width_of(int cols, int k) {
@@ -127,6 +128,9 @@ struct Shape {
 // tile, and 256 channels as the columns: a lane then has one scale for a block and
 // 128 columns, in a register, where tokens as columns need one read of shared
 // memory for four products.
+//
+// Where no group has many tokens kFp8Narrow is launched: no turned tiles, and what
+// the others take is fitted to narrow ones.
 //
 // The work of a call, in shared memory.  Tiles: groups in `order`; in a group,
 // blocks of kRowGroup tiles along the channels (l), tile along the tokens (or the
@@ -254,11 +258,16 @@ struct Half {
     }
 };
 
-// 8-bit: blocks of k that half an accumulator holds side by side.  (A meeting of
-// the issuer and the epilogue takes about 1000 cycles, whatever it is about.)
-__device__ __forceinline__ int blocks_each(bool turned, int cols) {
-    return turned ? 1 : (cols <= kMaxCols / 4 ? 4 : 2);
-}
+// kFp8Narrow: blocks of k that half an accumulator holds side by side, 1 << shift of
+// them (kFp8: one).  (A meeting of the issuer and the epilogue takes about 1000 cycles,
+// whatever it is about.)
+struct Sides {
+    int shift;
+    __device__ Sides(bool narrow, int cols) : shift(narrow ? (cols <= kMaxCols / 4 ? 2 : 1) : 0) {}
+    __device__ bool first(int kb) const { return (kb & ((1 << shift) - 1)) == 0; }
+    __device__ int next(int kb) const { return ((kb >> shift) + 1) << shift; }
+    __device__ int col(int kb) const { return (kb & ((1 << shift) - 1)) * (kHalfCols >> shift); }
+};
 
 // Bytes that `cols` columns of a tile take of a CTA's stage.
 template <Op OP>
@@ -283,11 +292,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kCtas = ctas_of(OP), kLanes = kCtas * kTileRows;
     constexpr bool PAIR = kCtas == 2;
     constexpr bool A_MN = OP == kInputGrad || OP == kWeightGrad, B_MN = OP == kWeightGrad;
-    constexpr bool HELP = OP == kFp8 || KRAGGED;
-    constexpr int kBlock = OP == kFp8 ? kAtom : kAtom / 2;  // extent of k in a stage
-    constexpr int kScaleFloats = OP == kFp8 ? kScaleSlots * kScaleRun * kFp8Cols : 4;
+    constexpr bool HELP = is_fp8(OP) || KRAGGED;
+    constexpr int kBlock = is_fp8(OP) ? kAtom : kAtom / 2;  // extent of k in a stage
+    constexpr int kScaleFloats = is_fp8(OP) ? kScaleSlots * kScaleRun * kFp8Cols : 4;
     // blocks of k whose products one accumulator takes
-    constexpr int kRun = OP == kFp8 ? 1 : (OP == kWeightGrad ? kGradRun : INT32_MAX);
+    constexpr int kRun = is_fp8(OP) ? 1 : (OP == kWeightGrad ? kGradRun : INT32_MAX);
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(16) float s_scale[kScaleFloats];
     // (pairs.  full, acc_free: CTA 0's, both CTAs arrive; empty, acc_full: either's own)
@@ -309,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (tid < kMaxStages) {
         ptx::mbar_init(&full[tid], KRAGGED ? kCtas : 1);
-        ptx::mbar_init(&empty[tid], OP == kFp8 ? 2 : 1);
+        ptx::mbar_init(&empty[tid], is_fp8(OP) ? 2 : 1);
         ptx::mbar_init(&tail[tid], 1);
         if (tid < kScaleSlots) {
             ptx::mbar_init(&sc_full[tid], 1);
@@ -322,11 +331,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tid < kAccs) {
             for (int h = 0; h < 2; ++h) {
                 ptx::mbar_init(&acc_full[tid][h], 1);
-                ptx::mbar_init(&acc_free[tid][h], OP == kFp8 ? kEpiWarps / 2 : kCtas * kEpiWarps);
+                ptx::mbar_init(&acc_free[tid][h], is_fp8(OP) ? kEpiWarps / 2 : kCtas * kEpiWarps);
             }
         }
         if (tid == 0) {
-            ptx::mbar_init(&drained, OP == kFp8 ? 2 : 1);
+            ptx::mbar_init(&drained, is_fp8(OP) ? 2 : 1);
             s_failed = 0;
             plan.most_tokens = 0;
             for (int i = 0; i < 4; ++i) plan.sums[i] = 0;
@@ -346,8 +355,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     shape.turn_from = OP == kFp8 && p.lanes % 8 == 0 &&
                               reinterpret_cast<uintptr_t>(p.out) % 16 == 0
                           ? kProductTurnFrom : INT32_MAX;
-    constexpr int kShift = OP == kFp8 ? 7 : 8;
-    static_assert(1 << kShift == (OP == kFp8 ? kFp8Cols : kMaxCols), "columns of a tile");
+    constexpr int kShift = is_fp8(OP) ? 7 : 8;
+    static_assert(1 << kShift == (is_fp8(OP) ? kFp8Cols : kMaxCols), "columns of a tile");
     shape.shift = kShift;
     __syncthreads();
     ptx::grid_dependency_wait();  // nothing of the caller's memory is touched before
@@ -523,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp >= kEpiWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         Turn sq(kSegs);
-        if (OP != kFp8 && warp == kListWarp) {
+        if (!is_fp8(OP) && warp == kListWarp) {
             if (ptx::elect_one()) {
                 Work<OP> work(plan);
                 for (bool more = true; more && !s_failed; sq.next()) {
@@ -543,25 +552,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t issued = 0, tails = 0, tail_parity = 0;
                 Work<OP> work(plan);
                 for (;;) {
-                    Seg sg;
-                    if (OP == kFp8) {  // lists the tiles itself
-                        sg.g = -1;
-                        const bool more = !s_failed && work.next(p, sg);
+                    const Seg *sp;
+                    if (is_fp8(OP)) {  // lists the tiles itself (and alone writes the list)
+                        Seg next;
+                        next.g = -1;
+                        const bool more = !s_failed && work.next(p, next);
                         if (!ptx::mbar_park(&seg_free[sq.at], sq.parity ^ 1u, kWaitNs)) {
                             s_failed = 1;
                             break;
                         }
-                        segs[sq.at] = sg;
+                        segs[sq.at] = next;
                         mbar_arrive(&seg_full[sq.at]);
+                        sp = more ? &segs[sq.at] : nullptr;
                         sq.next();
-                        if (!more) break;
                     } else {
-                        const Seg *sp = s_failed ? nullptr : listed(sq);
-                        if (sp == nullptr) break;
-                        sg = *sp;
-                        mbar_arrive(&seg_free[sq.at]);
-                        sq.next();
+                        sp = s_failed ? nullptr : listed(sq);
                     }
+                    if (sp == nullptr) break;
+                    const Seg &sg = *sp;
                     // columns of this CTA; its first lane and column; the group's first row
                     const int half = (sg.cols + 15) / 16 * (16 / kCtas);
                     const int a0 = sg.l * (OP == kFp8 && sg.turned ? kMaxCols : kLanes) +
@@ -610,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             load_3d(b + kLaneBytes, &map_a, k, a0 + kTileRows);
                             continue;
                         }
-                        if constexpr (OP == kFp8 || OP == kForward) {
+                        if constexpr (is_fp8(OP) || OP == kForward) {
                             load_3d(a, &map_a, k, a0);
                         } else if constexpr (OP == kInputGrad) {
                             load_3d(a, &map_a, a0, k);
@@ -630,6 +638,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 load_2d(b + c * kAtom, &map_b8, k, at + b0 + c);
                         }
                     }
+                    if (!is_fp8(OP)) {
+                        mbar_arrive(&seg_free[sq.at]);
+                        sq.next();
+                    }
                 }
                 // copies still in flight land before shared memory goes away (CTA 1's
                 // complete on CTA 0's barriers, and the pair ends together)
@@ -639,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (tails >> s & 1u) ptx::mbar_park(&tail[s], tail_parity >> s & 1u, kWaitNs);
                 }
             }
-        } else if (warp == kMmaWarp || (OP == kFp8 && warp == kListWarp)) {
+        } else if (warp == kMmaWarp || (is_fp8(OP) && warp == kListWarp)) {
             if (rank == 0 && ptx::elect_one()) {
                 const int h = warp == kMmaWarp ? 0 : 1;
                 Turn st(stages), acc(kAccs);
@@ -663,63 +675,65 @@ __global__ void __launch_bounds__(kThreads, 1)
                     else tc::commit(bar);
                 };
                 while (const Seg *sp = s_failed ? nullptr : listed(sq)) {
-                    const Seg sg = *sp;
-                    mbar_arrive(&seg_free[sq.at]);
-                    sq.next();
-                    // 8-bit: an accumulator's halves are filled and given back by themselves,
-                    // this issuer's from column b0 of the tile on
-                    const int each = blocks_each(sg.turned, sg.cols);
-                    int n = (sg.cols + 15) / 16 * 16, b0 = 0;
-                    if (OP == kFp8) {
-                        const Half half(sg.turned, sg.cols, h);
-                        n = half.steps * kStep;
-                        b0 = half.first * kStep;
-                    }
-                    const uint32_t idesc = (OP == kFp8 ? tc::idesc_e4m3_f32(kLanes, n)
-                                                       : tc::idesc_bf16_f32(kLanes, n)) |
-                                           kMajor;
-                    for (int kb = sg.k0; kb < sg.k1 && !s_failed;) {
-                        const int from = kb, to = kRun < sg.k1 - kb ? kb + kRun : sg.k1;
-                        const uint32_t d = taddr + acc.at * kMaxCols;
-                        if (!wait_for(&full[st.at], st.parity)) break;
-                        if (OP == kFp8) {
+                    const Seg &sg = *sp;
+                    const int k0 = sg.k0, k1 = sg.k1;
+                    if constexpr (is_fp8(OP)) {
+                        // An accumulator's halves are filled and given back by themselves;
+                        // this issuer's has the tile's columns from 16 half.first on.
+                        const Sides sides(OP == kFp8Narrow, sg.cols);
+                        const Half half(OP == kFp8 && sg.turned, sg.cols, h);
+                        const uint32_t idesc = tc::idesc_e4m3_f32(kLanes, half.steps * kStep);
+                        const uint64_t bdh = bd0 + half.first * (kStep * kAtom / 16);
+                        const bool some = half.steps > 0;
+                        for (int kb = k0; kb < k1;) {
+                            if (!wait_for(&full[st.at], st.parity)) break;
                             const uint32_t at = st.at * (uint32_t)(stage_bytes / 16);
-                            if ((kb == sg.k0 || kb % each == 0) &&
+                            if ((kb == k0 || sides.first(kb)) &&
                                 !wait_for(&acc_free[acc.at][h], acc.parity ^ 1u))
                                 break;
-                            if (n > 0) {
-                                const uint32_t col = h * kHalfCols + kb % each * (kHalfCols / each);
+                            if (some) {
+                                const uint32_t d = taddr + acc.at * kMaxCols + h * kHalfCols +
+                                                   (OP == kFp8Narrow ? sides.col(kb) : 0);
 #pragma unroll
                                 for (int kk = 0; kk < 4; ++kk)
-                                    tc::mma_f8(d + col, ad0 + at + kk * kStepA,
-                                               bd0 + at + b0 * (kAtom / 16) + kk * kStepB, idesc,
-                                               kk != 0);
+                                    tc::mma_f8(d, ad0 + at + kk * kStepA, bdh + at + kk * kStepB,
+                                               idesc, kk != 0);
                             }
-                            commit(&empty[st.at]);
                             ++kb;
-                            st.next();
-                            if (kb == sg.k1 || kb % each == 0) {
+                            if (kb == k1 || sides.first(kb)) {
                                 commit(&acc_full[acc.at][h]);
                                 acc.next();
                             }
-                            continue;
-                        }
-                        if (!wait_for(&acc_free[acc.at][0], acc.parity ^ 1u)) break;
-                        for (; kb < to; ++kb, st.next()) {
-                            if (kb != from && !wait_for(&full[st.at], st.parity)) break;
-                            const uint32_t at = st.at * (uint32_t)(stage_bytes / 16);
-                            const int steps = (rows_of(sg.g, kb) + 15) / 16;
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) {
-                                if (KRAGGED && kk >= steps) break;
-                                tc::mma_bf16_pair(d, ad0 + at + kk * kStepA, bd0 + at + kk * kStepB,
-                                                  idesc, kb != from || kk != 0);
-                            }
                             commit(&empty[st.at]);
+                            st.next();
                         }
-                        commit(&acc_full[acc.at][0]);
-                        acc.next();
+                    } else {
+                        const int n = (sg.cols + 15) / 16 * 16;
+                        const uint32_t idesc = tc::idesc_bf16_f32(kLanes, n) | kMajor;
+                        for (int kb = k0; kb < k1 && !s_failed;) {
+                            const int from = kb, to = kRun < k1 - kb ? kb + kRun : k1;
+                            const uint32_t d = taddr + acc.at * kMaxCols;
+                            if (!wait_for(&full[st.at], st.parity)) break;
+                            if (!wait_for(&acc_free[acc.at][0], acc.parity ^ 1u)) break;
+                            for (; kb < to; ++kb, st.next()) {
+                                if (kb != from && !wait_for(&full[st.at], st.parity)) break;
+                                const uint32_t at = st.at * (uint32_t)(stage_bytes / 16);
+                                const int steps = (rows_of(sg.g, kb) + 15) / 16;
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk) {
+                                    if (KRAGGED && kk >= steps) break;
+                                    tc::mma_bf16_pair(d, ad0 + at + kk * kStepA,
+                                                      bd0 + at + kk * kStepB, idesc,
+                                                      kb != from || kk != 0);
+                                }
+                                commit(&empty[st.at]);
+                            }
+                            commit(&acc_full[acc.at][0]);
+                            acc.next();
+                        }
                     }
+                    mbar_arrive(&seg_free[sq.at]);
+                    sq.next();
                 }
                 commit(&drained);  // before tensor memory is freed
                 ptx::mbar_park(&drained, 0, kWaitNs);
@@ -736,10 +750,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&seg_free[sq.at]);
                 sq.next();
-                if constexpr (OP == kFp8) {
+                if constexpr (is_fp8(OP)) {
                     // Products of the tokens' scales and the channels' of tiles that are not
                     // turned, four blocks of k (a run) at a time, for each column.
-                    if (sg.turned) continue;
+                    if (OP == kFp8 && sg.turned) continue;
                     const int KB = blocks, NB = (p.lanes + kScaleBlock - 1) / kScaleBlock;
                     const bool vec = KB % 4 == 0 && reinterpret_cast<uintptr_t>(p.x_scale) % 16 == 0;
                     const float *sw = p.w_scale + ((size_t)sg.g * NB + sg.l) * KB;
@@ -832,16 +846,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Seg *const sp = listed(sq);
             if (__any_sync(0xffffffffu, sp == nullptr)) break;
             const Seg &sg = *sp;  // (stays there until the tile is stored)
-            const Half half(OP == kFp8 && sg.turned, sg.cols, hf);
-            int steps = half.steps;
-            if (OP == kFp8 && sg.turned) {  // channels that exist, if a token of the warp does
-                const int chans = p.lanes - sg.l * kMaxCols - half.first * kStep;
-                steps = q * 32 < sg.cols ? min(max((chans + kStep - 1) / kStep, 0), kSteps) : 0;
-            }
-            const int n0 = half.first * kStep, k0 = sg.k0, k1 = sg.k1;
+            // this warp's steps of kStep columns of the tile, and the first one
+            const auto steps_of = [&] {
+                const int n = Half(OP == kFp8 && sg.turned, sg.cols, hf).steps;
+                if (OP != kFp8 || !sg.turned) return n;
+                // channels that exist, if a token of the warp does
+                const int chans = p.lanes - sg.l * kMaxCols - hf * kHalfCols;
+                return q * 32 < sg.cols ? min(max((chans + kStep - 1) / kStep, 0), kSteps) : 0;
+            };
+            const auto first_of = [&] {
+                return Half(OP == kFp8 && sg.turned, sg.cols, hf).first * kStep;
+            };
             // Sums to the columns from `to` on (16 a step).
             const auto keep = [&](uint32_t to, const auto &sum) {
                 constexpr int S = sizeof sum / sizeof sum[0];
+                const int steps = steps_of();
 #pragma unroll
                 for (int i = 0; i < S; ++i) {
                     uint32_t v[kStep];
@@ -860,6 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // What the sums (columns n0 + 16 i .. of this lane), kept in tensor memory, come
             // to.  (Held in registers here they do not leave enough for the rest.)
             const auto finish = [&](uint32_t from, bool none) {
+                const int steps = steps_of(), n0 = first_of();
                 const auto get = [&](int i, float (&v)[2][kStep]) {  // steps i and i + 1
                     uint32_t u[2][kStep];
 #pragma unroll
@@ -1040,23 +1060,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             };
-            if constexpr (OP == kFp8) {
+            if constexpr (is_fp8(OP)) {
                 const auto scales = [&](int kb) {  // of block kb; (a new run's: once they are there)
-                    if (kb % kScaleRun == 0 || kb == k0) wait_for(&sc_full[sc.at], sc.parity);
+                    if (kb % kScaleRun == 0 || kb == sg.k0) wait_for(&sc_full[sc.at], sc.parity);
                     return s_scale + (sc.at * kScaleRun + kb % kScaleRun) * kFp8Cols;
                 };
                 const auto scales_read = [&](int kb) {
-                    if (kb % kScaleRun == kScaleRun - 1 || kb + 1 == k1) {
+                    if (kb % kScaleRun == kScaleRun - 1 || kb + 1 == sg.k1) {
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&sc_free[sc.at]);
                         sc.next();
                     }
                 };
-                if (sg.turned) {
-                    // Four loads of 32 columns a block; the last two are added when the
-                    // accumulator's half has been given back.
+                if (OP == kFp8 && sg.turned) {
+                    // Four reads of 32 columns a block, the last of which is added when the
+                    // accumulator's half has been given back.  (Reads in flight beside the
+                    // additions take registers that are not there: 193 to 294 us for 8192 x
+                    // 4096 x 7168, by what the compiler made of it; so 211 us.)
                     constexpr int kHeld = 32;
-                    uint32_t u[2][kHeld];
+                    uint32_t u[kHeld];
                     float sum[kSteps][kStep];
                     clear(sum);
                     const auto add = [&](const uint32_t (&v)[kHeld], int at, float f) {
@@ -1069,6 +1091,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             x2::unpack(o, t[0], t[1]);
                         }
                     };
+                    const int k0 = sg.k0, k1 = sg.k1;
                     // Scales of this lane's token, four blocks (a run) at a time, a run ahead.
                     const int KB = plan.blocks, NB = (p.lanes + kScaleBlock - 1) / kScaleBlock;
                     const bool there = row < sg.cols;
@@ -1103,19 +1126,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!wait_for(&acc_full[acc.at][hf], acc.parity)) break;
                         tc::fence_after_sync();
                         const uint32_t from = mine + acc.at * kMaxCols + hf * kHalfCols;
-                        tc::ld_32x32(from, u[0]);
-                        tc::ld_32x32(from + 32, u[1]);
-                        tc::wait_ld(u[0]);
-                        tc::wait_ld(u[1]);
-                        add(u[0], 0, f);
-                        tc::ld_32x32(from + 64, u[0]);
-                        add(u[1], 32, f);
-                        tc::ld_32x32(from + 96, u[1]);
-                        tc::wait_ld(u[0]);
-                        tc::wait_ld(u[1]);
-                        if (kb + 1 < k1) release();
-                        add(u[0], 64, f);
-                        add(u[1], 96, f);
+#pragma unroll
+                        for (int i = 0; i < kHalfCols; i += kHeld) {
+                            tc::ld_wait_32x32(from + i, u);
+                            if (i + kHeld == kHalfCols && kb + 1 < k1) release();
+                            add(u, i, f);
+                        }
                     }
                     if (ok) {
                         const uint32_t at = mine + acc.at * kMaxCols + hf * kHalfCols;
@@ -1125,7 +1141,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 } else {
                     constexpr int kNarrow = kFp8Cols / 2 / kStep;  // steps, at most
-                    const int each = blocks_each(false, sg.cols);
+                    const Sides sides(OP == kFp8Narrow, sg.cols);
+                    const int steps = steps_of();
+                    const int n0 = first_of(), k0 = sg.k0, k1 = sg.k1;
                     float sum[kNarrow][kStep];
                     clear(sum);
                     const auto add = [&](float (&t)[kStep], const uint32_t (&v)[kStep], const float *f) {
@@ -1140,11 +1158,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     };
                     const uint32_t mine_half = mine + hf * kHalfCols;
                     for (int kb = k0; ok && kb < k1;) {
-                        const int to = min(k1, (kb / each + 1) * each);
+                        const int to = min(k1, sides.next(kb));
                         if (!wait_for(&acc_full[acc.at][hf], acc.parity)) break;
                         tc::fence_after_sync();
                         const uint32_t from = mine_half + acc.at * kMaxCols;
-                        if (steps <= 1) {  // (at most 48 columns: four blocks) all at once
+                        if (OP == kFp8Narrow && steps <= 1) {  // (four blocks) all at once
                             const float *f = scales(kb) - kb % 4 * kFp8Cols + n0;
                             uint32_t u[4][kStep];
 #pragma unroll
@@ -1161,7 +1179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else {
                             for (int b = kb; ok && b < to; ++b) {
                                 const float *f = scales(b) + n0;
-                                const uint32_t at = from + b % each * (kHalfCols / each);
+                                const uint32_t at = from + sides.col(b);
                                 uint32_t u[2][kStep];  // (the loads of the next step are in flight)
                                 tc::ld_32x16(at, u[0]);
 #pragma unroll
@@ -1179,14 +1197,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         kb = to;
                     }
                     if (ok) {  // (kept where the last block was)
-                        const uint32_t at = mine_half + acc.at * kMaxCols +
-                                            (k1 - 1) % each * (kHalfCols / each);
+                        const uint32_t at = mine_half + acc.at * kMaxCols + sides.col(k1 - 1);
                         keep(at, sum);
                         finish(at, false);
                         release();
                     }
                 }
             } else {
+                const int steps = steps_of(), n0 = first_of(), k0 = sg.k0, k1 = sg.k1;
                 if (!KRAGGED || k1 - k0 <= kRun) {  // all of k in one accumulator, or nothing
                     if (k0 < k1) wait_for(&acc_full[acc.at][0], acc.parity);
                     tc::fence_after_sync();
