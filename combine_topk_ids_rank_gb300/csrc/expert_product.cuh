@@ -82,6 +82,7 @@ constexpr int kBigBox = 64, kSmallBox = 8;                // rows of the token b
 constexpr int kScaleSlots = 4, kScaleRun = 4;             // runs of 4 blocks' scales
 constexpr int kSegs = 4;                                  // listed tiles
 constexpr int kDynamic = 193 * 1024;                      // 227 KB less the static tables
+constexpr int kBoxRows = 32, kBoxBytes = kBoxRows * kAtom;  // an output box of an epilogue warp
 constexpr int kClasses = 64;
 constexpr int kGradRun = 8;       // blocks of 64 rows of k that stay in tensor memory
 constexpr int kMinPart = 4;       // blocks of k that make a part worth its way through memory
@@ -109,6 +110,7 @@ struct Shape {
     static constexpr int kLanes = ctas_of(OP) * kTileRows;
     int turn_from;  // tokens that make a group's tiles turned
     int shift;      // columns of a tile that is not, at most: 1 << shift
+    int even;       // tiles of a group are evened out (else: full ones and what is left)
 
     __device__ bool turned(int c) const { return OP == kFp8 && c >= turn_from; }
     // Tiles along the channels, and along `c` tokens (or the maps' columns).
@@ -119,7 +121,9 @@ struct Shape {
         return turned(c) ? (c + kTileRows - 1) / kTileRows : (c + (1 << shift) - 1) >> shift;
     }
     // Columns of a tile, and the tokens (or columns) from one tile to the next.
-    __device__ int width(int c) const { return turned(c) ? kMaxCols : width_of(c, mtiles(c)); }
+    __device__ int width(int c) const {
+        return turned(c) ? kMaxCols : (even ? width_of(c, mtiles(c)) : min(c, 1 << shift));
+    }
     __device__ int stride(int c) const { return turned(c) ? kTileRows : width(c); }
     __device__ int tiles(int c, int lanes) const { return mtiles(c) * ltiles(c, lanes); }
 };
@@ -358,6 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kShift = is_fp8(OP) ? 7 : 8;
     static_assert(1 << kShift == (is_fp8(OP) ? kFp8Cols : kMaxCols), "columns of a tile");
     shape.shift = kShift;
+    shape.even = !(KRAGGED && p.boxes);
     __syncthreads();
     ptx::grid_dependency_wait();  // nothing of the caller's memory is touched before
     int sums[4] = {0, 0, 0, 0}, most = 0;
@@ -505,7 +510,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const uint32_t taddr = s_taddr;
     const int stage_bytes = kLaneBytes + col_bytes<OP>(widest);
-    const int stages = min(kMaxStages, (kDynamic - 1024) / stage_bytes);
+    const int boxes = KRAGGED && p.boxes ? kEpiWarps * kBoxBytes : 0;  // (at the end)
+    const int stages = min(kMaxStages, (kDynamic - 1024 - boxes) / stage_bytes);
     auto a_of = [&](uint32_t s) { return smem + s * stage_bytes; };
     auto b_of = [&](uint32_t s) { return smem + s * stage_bytes + kLaneBytes; };
     __syncthreads();
@@ -994,7 +1000,53 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 };
-                if (sg.whole) {
+                if (KRAGGED && p.boxes && sg.whole) {
+                    // Boxes of 32 rows by 128 bytes, through shared memory (128-byte swizzle),
+                    // clipped at the map's last row by the tensor map.
+                    uint8_t *box = smem + (kDynamic - 1024 - boxes) + (warp) * kBoxBytes;
+                    const int y = sg.l * kLanes + rank * kTileRows + q * 32;
+                    const int each = p.f32 ? 2 : 4;  // steps of a box
+                    if (y < p.lanes)
+#pragma unroll 1
+                        for (int i = 0; i < steps; i += each) {
+                            if (lane == 0) ptx::bulk_wait_read<0>();  // (the box before)
+                            __syncwarp();
+#pragma unroll 1
+                            for (int k = 0; k < each; k += 2) {
+                                float v[2][kStep];
+                                get(i + k, v);
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                    for (int c = 0; c < 4; ++c) {
+                                        uint4 w;
+                                        int at = 4 * h + c;  // 16-byte chunk of the row
+                                        if (p.f32) {
+                                            w = make_uint4(__float_as_uint(v[h][4 * c]),
+                                                           __float_as_uint(v[h][4 * c + 1]),
+                                                           __float_as_uint(v[h][4 * c + 2]),
+                                                           __float_as_uint(v[h][4 * c + 3]));
+                                        } else {
+                                            if (c >= 2) continue;
+                                            at = 2 * (k + h) + c;
+                                            w = make_uint4(pack_bf16(v[h], 4 * c),
+                                                           pack_bf16(v[h], 4 * c + 1),
+                                                           pack_bf16(v[h], 4 * c + 2),
+                                                           pack_bf16(v[h], 4 * c + 3));
+                                        }
+                                        *reinterpret_cast<uint4 *>(box + lane * kAtom +
+                                                                   ((at ^ (lane & 7)) << 4)) = w;
+                                    }
+                            }
+                            ptx::fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                const int x = sg.c0 + n0 + i * kStep;
+                                tc::tma_store_3d(&map_b8, p.f32 ? 2 * x : x, y, sg.g, box);
+                                ptx::bulk_commit();
+                            }
+                        }
+                } else if (sg.whole) {
                     // (adding nothing to what is there: left alone)
                     if (KRAGGED && p.accumulate && none) return;
 #pragma unroll 1
@@ -1244,6 +1296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
 
+    if (KRAGGED && lane == 0) ptx::bulk_wait_all();  // output boxes on their way
     __syncwarp();
     if (warp == kMmaWarp && rank != 0)  // CTA 0's products read this CTA's memory too
         ptx::mbar_park(&drained, 0, kWaitNs);

@@ -355,6 +355,17 @@ __device__ __forceinline__ void tma_load_5d(void *smem_dst, const void *tmap, in
         : "memory");
 }
 
+// 3-D tiled TMA store of the box at (x, y, z), in the thread's bulk group; what lies
+// past the tensor's extents is left out.
+__device__ __forceinline__ void tma_store_3d(const void *tmap, int x, int y, int z,
+                                             const void *smem_src) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+            reinterpret_cast<uint64_t>(tmap)),
+        "r"(x), "r"(y), "r"(z), "r"(ptx::smem_u32(smem_src))
+        : "memory");
+}
+
 // Fetch a tensor map ahead of its first use.
 __device__ __forceinline__ void prefetch_map(const void *tmap) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");

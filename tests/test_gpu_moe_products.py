@@ -310,7 +310,8 @@ def ragged(counts, N, H, g, first=2, behind=5):
 
 
 @pytest.mark.parametrize("counts", COUNTS, ids=lambda c: "%dx%d" % (len(c), max(c)))
-@pytest.mark.parametrize("N,H", [(8, 8), (72, 136), (264, 520), (128, 64), (520, 264)])
+@pytest.mark.parametrize("N,H", [(8, 8), (72, 136), (264, 520), (128, 64), (520, 264), (72, 128),
+                                 (264, 384), (40, 1152)])
 def test_ragged(api, counts, N, H):
     G = len(counts)
     x, dy, w, off = ragged(counts, N, H, gen(sum(counts) + N + H))
@@ -384,10 +385,10 @@ def test_ragged_long(api, counts):
             assert far <= (2.0 ** -8 if got.dtype is BF else 2.0 ** -17)
 
 
-@pytest.mark.parametrize("seed", [1, 2, 3])
-def test_ragged_many_tiles_of_every_width(api, seed):
+@pytest.mark.parametrize("seed,N,H", [(1, 776, 520), (2, 520, 640), (3, 1032, 384)])
+def test_ragged_many_tiles_of_every_width(api, seed, N, H):
     rng = np.random.default_rng(seed)
-    G, N, H = 37, 776, 520
+    G = 37
     counts = np.concatenate([rng.integers(0, 70, 20), rng.integers(0, 900, 17)])
     counts[[0, 19, 36]] = 0
     rng.shuffle(counts)
