@@ -556,6 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ptx::elect_one()) {
                 Turn st(stages);
                 uint32_t issued = 0, tails = 0, tail_parity = 0;
+                const uint32_t full0 = PAIR ? ptx::cluster_smem(full, 0) : 0;
                 Work<OP> work(plan);
                 for (;;) {
                     const Seg *sp;
@@ -575,27 +576,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                         sp = s_failed ? nullptr : listed(sq);
                     }
                     if (sp == nullptr) break;
-                    const Seg &sg = *sp;
+                    const Seg sg = *sp;
+                    if (!is_fp8(OP)) {
+                        mbar_arrive(&seg_free[sq.at]);
+                        sq.next();
+                    }
                     // columns of this CTA; its first lane and column; the group's first row
                     const int half = (sg.cols + 15) / 16 * (16 / kCtas);
                     const int a0 = sg.l * (OP == kFp8 && sg.turned ? kMaxCols : kLanes) +
                                    rank * kTileRows;
-                    const int b0 = sg.c0 + rank * half, at = plan.start[sg.g];
+                    const int at = plan.start[sg.g];
+                    const int b0 = (KRAGGED ? 0 : at) + sg.c0 + rank * half;
+                    int left = KRAGGED ? plan.count[sg.g] - sg.k0 * 64 : 64;  // rows of k
                     uint32_t bytes = kLaneBytes + col_bytes<OP>(kCtas * half);
                     if (OP == kFp8 && sg.turned)  // boxes of 64 tokens, 256 channels
                         bytes = (sg.cols + 63) / 64 * kPanelBytes + 2 * kLaneBytes;
                     for (int kb = sg.k0; kb < sg.k1; ++kb, st.next()) {
-                        const int s = (int)st.at;
+                        const int s = (int)st.at, k = kb * kBlock;
                         if (!ptx::mbar_park(&empty[s], st.parity ^ 1u, kWaitNs)) {
                             s_failed = 1;
                             break;
                         }
                         // A last block with rows of the next group lands on a barrier of this
                         // CTA; the helper clears those rows and arrives in the producer's place.
-                        const bool last = KRAGGED && rows_of(sg.g, kb) < 64;
                         uint64_t *bar = &full[s];
-                        uint32_t bar0 = PAIR ? ptx::cluster_smem(bar, 0) : 0;
-                        if (last) {
+                        uint32_t bar0 = full0 + 8 * s;
+                        if (KRAGGED && left < 64) {
                             bar = &tail[s];
                             ptx::mbar_arrive_expect_tx(bar, bytes);
                             if (tails >> s & 1u) tail_parity ^= 1u << s;
@@ -607,6 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else if (KRAGGED) {
                             ptx::mbar_arrive_pair(bar0);
                         }
+                        if (KRAGGED) left -= 64;
                         const auto load_2d = [&](uint8_t *to, const CUtensorMap *m, int x, int y) {
                             if (PAIR) tc::tma_load_2d_pair(to, m, x, y, bar0);
                             else tc::tma_load_2d(to, m, x, y, bar);
@@ -616,10 +623,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             else tc::tma_load_3d(to, m, x, y, sg.g, bar);
                         };
                         uint8_t *a = a_of(s), *b = b_of(s);
-                        const int k = kb * kBlock;
                         if (OP == kFp8 && sg.turned) {
                             for (int c = 0; c < sg.cols; c += kBigBox)
-                                load_2d(a + c * kAtom, &map_b, k, at + sg.c0 + c);
+                                load_2d(a + c * kAtom, &map_b, k, b0 + c);
                             load_3d(b, &map_a, k, a0);
                             load_3d(b + kLaneBytes, &map_a, k, a0 + kTileRows);
                             continue;
@@ -634,19 +640,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                             load_2d(a + kPanelBytes, &map_a, a0 + 64, at + k);
                         }
                         if constexpr (B_MN) {
-                            for (int c = 0; c < half; c += 64)
-                                load_2d(b + c / 64 * kPanelBytes, &map_b, b0 + c, at + k);
+                            load_2d(b, &map_b, b0, at + k);
+                            if (half > 64) load_2d(b + kPanelBytes, &map_b, b0 + 64, at + k);
                         } else {
                             int c = 0;
                             for (; c + kBigBox <= half; c += kBigBox)
-                                load_2d(b + c * kAtom, &map_b, k, at + b0 + c);
+                                load_2d(b + c * kAtom, &map_b, k, b0 + c);
                             for (; c < half; c += kSmallBox)
-                                load_2d(b + c * kAtom, &map_b8, k, at + b0 + c);
+                                load_2d(b + c * kAtom, &map_b8, k, b0 + c);
                         }
-                    }
-                    if (!is_fp8(OP)) {
-                        mbar_arrive(&seg_free[sq.at]);
-                        sq.next();
                     }
                 }
                 // copies still in flight land before shared memory goes away (CTA 1's
@@ -716,6 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else {
                         const int n = (sg.cols + 15) / 16 * 16;
                         const uint32_t idesc = tc::idesc_bf16_f32(kLanes, n) | kMajor;
+                        int left = KRAGGED ? plan.count[sg.g] - k0 * 64 : 64;  // rows of k
                         for (int kb = k0; kb < k1 && !s_failed;) {
                             const int from = kb, to = kRun < k1 - kb ? kb + kRun : k1;
                             const uint32_t d = taddr + acc.at * kMaxCols;
@@ -724,14 +727,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (; kb < to; ++kb, st.next()) {
                                 if (kb != from && !wait_for(&full[st.at], st.parity)) break;
                                 const uint32_t at = st.at * (uint32_t)(stage_bytes / 16);
-                                const int steps = (rows_of(sg.g, kb) + 15) / 16;
 #pragma unroll
                                 for (int kk = 0; kk < 4; ++kk) {
-                                    if (KRAGGED && kk >= steps) break;
+                                    if (KRAGGED && kk != 0 && left <= 16 * kk) break;
                                     tc::mma_bf16_pair(d, ad0 + at + kk * kStepA,
                                                       bd0 + at + kk * kStepB, idesc,
                                                       kb != from || kk != 0);
                                 }
+                                if (KRAGGED) left -= 64;
                                 commit(&empty[st.at]);
                             }
                             commit(&acc_full[acc.at][0]);
