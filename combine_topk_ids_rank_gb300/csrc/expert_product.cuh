@@ -111,11 +111,13 @@ struct Shape {
     int turn_from;  // tokens that make a group's tiles turned
     int shift;      // columns of a tile that is not, at most: 1 << shift
     int even;       // tiles of a group are evened out (else: full ones and what is left)
+    int thin;       // kFp8Narrow: a tile has 64 lanes only, so that none is cut
 
     __device__ bool turned(int c) const { return OP == kFp8 && c >= turn_from; }
     // Tiles along the channels, and along `c` tokens (or the maps' columns).
     __device__ int ltiles(int c, int lanes) const {
-        return turned(c) ? (lanes + kMaxCols - 1) / kMaxCols : (lanes + kLanes - 1) / kLanes;
+        const int l = turned(c) ? kMaxCols : (OP == kFp8Narrow && thin ? 64 : kLanes);
+        return (lanes + l - 1) / l;
     }
     __device__ int mtiles(int c) const {
         return turned(c) ? (c + kTileRows - 1) / kTileRows : (c + (1 << shift) - 1) >> shift;
@@ -280,6 +282,14 @@ __device__ __forceinline__ int col_bytes(int cols) {
     return OP == kWeightGrad ? (mine + 63) / 64 * kPanelBytes : mine * kAtom;
 }
 
+// One more on a counter in memory: what this thread has seen written is released, and
+// what others released there acquired.
+__device__ __forceinline__ int count_up(int *p) {
+    int old;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(p) : "memory");
+    return old;
+}
+
 // 32 bytes of 16 neighbouring bf16 values or 8 fp32 values, 32-byte aligned.
 __device__ __forceinline__ void store_256(void *p, const uint32_t (&v)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
@@ -363,6 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     static_assert(1 << kShift == (is_fp8(OP) ? kFp8Cols : kMaxCols), "columns of a tile");
     shape.shift = kShift;
     shape.even = !(KRAGGED && p.boxes);
+    shape.thin = 0;
     __syncthreads();
     ptx::grid_dependency_wait();  // nothing of the caller's memory is touched before
     int sums[4] = {0, 0, 0, 0}, most = 0;
@@ -406,6 +417,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 shape.shift = 8 - i;
                 tiles = plan.sums[i] * l;
             }
+    }
+    // 8-bit, fewer tiles than half the SMs: of 64 lanes instead of cut ones (one SM can
+    // take more than its share of the memory's rate, and no part goes through memory)
+    if (OP == kFp8Narrow && tiles * 2 <= pairs) {
+        shape.thin = 1;
+        tiles = plan.sums[8 - shape.shift] * ((p.lanes + 63) / 64);
     }
     // the widest tile decides how many stages the ring has
     const int blocks = KRAGGED ? 0 : (p.depth + kBlock - 1) / kBlock;
@@ -583,12 +600,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     // columns of this CTA; its first lane and column; the group's first row
                     const int half = (sg.cols + 15) / 16 * (16 / kCtas);
-                    const int a0 = sg.l * (OP == kFp8 && sg.turned ? kMaxCols : kLanes) +
+                    const bool thin = OP == kFp8Narrow && plan.shape.thin;
+                    const int a0 = sg.l * (OP == kFp8 && sg.turned ? kMaxCols : (thin ? 64 : kLanes)) +
                                    rank * kTileRows;
                     const int at = plan.start[sg.g];
                     const int b0 = (KRAGGED ? 0 : at) + sg.c0 + rank * half;
                     int left = KRAGGED ? plan.count[sg.g] - sg.k0 * 64 : 64;  // rows of k
-                    uint32_t bytes = kLaneBytes + col_bytes<OP>(kCtas * half);
+                    uint32_t bytes = kLaneBytes / (thin ? 2 : 1) + col_bytes<OP>(kCtas * half);
                     if (OP == kFp8 && sg.turned)  // boxes of 64 tokens, 256 channels
                         bytes = (sg.cols + 63) / 64 * kPanelBytes + 2 * kLaneBytes;
                     for (int kb = sg.k0; kb < sg.k1; ++kb, st.next()) {
@@ -630,7 +648,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             load_3d(b + kLaneBytes, &map_a, k, a0 + kTileRows);
                             continue;
                         }
-                        if constexpr (is_fp8(OP) || OP == kForward) {
+                        if constexpr (OP == kFp8Narrow) {
+                            load_3d(a, &map_a, k, a0);
+                            if (!thin) load_3d(a + kPanelBytes, &map_a, k, a0 + 64);
+                        } else if constexpr (OP == kFp8 || OP == kForward) {
                             load_3d(a, &map_a, k, a0);
                         } else if constexpr (OP == kInputGrad) {
                             load_3d(a, &map_a, a0, k);
@@ -765,7 +786,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (OP == kFp8 && sg.turned) continue;
                     const int KB = blocks, NB = (p.lanes + kScaleBlock - 1) / kScaleBlock;
                     const bool vec = KB % 4 == 0 && reinterpret_cast<uintptr_t>(p.x_scale) % 16 == 0;
-                    const float *sw = p.w_scale + ((size_t)sg.g * NB + sg.l) * KB;
+                    const int nb = OP == kFp8Narrow && plan.shape.thin ? sg.l / 2 : sg.l;
+                    const float *sw = p.w_scale + ((size_t)sg.g * NB + nb) * KB;
                     const float *sx = p.x_scale + ((size_t)plan.start[sg.g] + sg.c0 + lane) * KB;
                     const int left = sg.cols - lane;  // tokens from this lane's first one on
                     for (int kb = sg.k0 & ~3; kb < sg.k1; kb += kScaleRun, sc.next()) {
@@ -858,6 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // this warp's steps of kStep columns of the tile, and the first one
             const auto steps_of = [&] {
                 const int n = Half(OP == kFp8 && sg.turned, sg.cols, hf).steps;
+                if (OP == kFp8Narrow && plan.shape.thin && q >= 2) return 0;  // no lane
                 if (OP != kFp8 || !sg.turned) return n;
                 // channels that exist, if a token of the warp does
                 const int chans = p.lanes - sg.l * kMaxCols - hf * kHalfCols;
@@ -907,7 +930,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int j = 0; j < kStep; ++j) v[h][j] = __uint_as_float(u[h][j]);
                 };
                 // the lane's channel (not turned)
-                const int chan = sg.l * kLanes + rank * kTileRows + row;
+                const int chan = sg.l * (OP == kFp8Narrow && plan.shape.thin ? 64 : kLanes) +
+                                 rank * kTileRows + row;
                 const bool live = chan < p.lanes;
                 uint16_t *const out16 = static_cast<uint16_t *>(p.out);
                 // values 2 j and 2 j + 1
@@ -1087,17 +1111,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 for (int j = 0; j < kStep; ++j)
                                     __stcg(part + ((i + h) * kStep + j) * kTileRows, v[h][j]);
                     }
-                    // the warp's parts, then lane 0's fence and count; and the other way round: what
-                    // lane 0 finds counted, its fence, then the warp's reads (a shuffle orders no
-                    // memory)
+                    // the warp's parts, then lane 0's count, which releases them; and the other
+                    // way round: what lane 0 finds counted (acquired), then the warp's reads
                     __syncwarp();
-                    __threadfence();
                     int last = 0;
                     if (lane == 0) {
                         int *m = &p.header->merged[hf][kCtas * p0 + rank][q];
-                        last = atomicAdd(m, 1) == parts - 1;
+                        last = count_up(m) == parts - 1;
                         if (last) *m = 0;  // for the next call
-                        __threadfence();
                     }
                     last = __shfl_sync(0xffffffffu, last, 0);
                     __syncwarp();

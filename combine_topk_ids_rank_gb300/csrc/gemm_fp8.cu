@@ -15,21 +15,21 @@ namespace moe {
 cudaError_t launch_gemm_fp8(ProductParams p, const void *xq, const void *wq, int num_sms,
                             cudaStream_t st) {
     using namespace product;
-    CUtensorMap a, b, b8;
-    const long long rows = p.offsets != nullptr ? p.M : (long long)p.G * p.M;
-    if (!map_3d(&a, wq, p.G, p.lanes, p.depth, kAtom, kTileRows, true) ||
-        !map_2d(&b, xq, rows, p.depth, kAtom, kBigBox, true) ||
-        !map_2d(&b8, xq, rows, p.depth, kAtom, kSmallBox, true))
-        return cudaErrorInvalidValue;
     // Few tokens in every group, or (as far as the host knows) in most of them, or so few
     // tiles that narrower ones keep more SMs at work: none is turned.
     const long long tiles = ((long long)p.M + kTileRows - 1) / kTileRows *
-                            ((p.lanes + kMaxCols - 1) / kMaxCols);
+                            ((p.lanes + kProductMaxCols - 1) / kProductMaxCols);
     const bool one = p.G == 1 && p.counts == nullptr && p.offsets == nullptr;
-    if (p.M < kProductTurnFrom || (p.offsets != nullptr && p.M / p.G < 32) ||
-        (one && tiles * 2 <= num_sms))
-        return launch<kFp8Narrow>(p, a, b, b8, num_sms, st);
-    return launch<kFp8>(p, a, b, b8, num_sms, st);
+    const bool narrow = p.M < kProductTurnFrom || (p.offsets != nullptr && p.M / p.G < 32) ||
+                        (one && tiles * 2 <= num_sms);
+    CUtensorMap a, b, b8;
+    const long long rows = p.offsets != nullptr ? p.M : (long long)p.G * p.M;
+    if (!map_3d(&a, wq, p.G, p.lanes, p.depth, kAtom, narrow ? 64 : kTileRows, true) ||
+        !map_2d(&b, xq, rows, p.depth, kAtom, kBigBox, true) ||
+        !map_2d(&b8, xq, rows, p.depth, kAtom, kSmallBox, true))
+        return cudaErrorInvalidValue;
+    return narrow ? launch<kFp8Narrow>(p, a, b, b8, num_sms, st)
+                  : launch<kFp8>(p, a, b, b8, num_sms, st);
 }
 
 }  // namespace moe
