@@ -676,18 +676,17 @@ def quantize_blocks_fp8(x, block_rows: int = 1, counts=None, out=None, scale=Non
     [..., ceil(rows / 128), ceil(H / 128)]).  With counts (int32 [G] on the
     device, block_rows = 1) x is [G, rows, H] and rows past a plane's count are
     left alone.  2-D x may have any row stride that is a multiple of 16 bytes."""
-    dtype, device = x.dtype, x.device
+    dtype, device, shape = x.dtype, x.device, x.shape
     bf16 = dtype is _torch.bfloat16
     tiles = block_rows != 1
-    if not x.is_cuda or not (bf16 or dtype is _torch.float32) or x.dim() < 1 + tiles:
+    if not x.is_cuda or not (bf16 or dtype is _torch.float32) or len(shape) < 1 + tiles:
         raise ValueError("x must be a float32 or bfloat16 CUDA tensor [..., H]")
-    if block_rows not in (1, MOE_SCALE_BLOCK):
+    if tiles and block_rows != MOE_SCALE_BLOCK:
         raise ValueError("block_rows must be 1 or %d" % MOE_SCALE_BLOCK)
-    shape = x.shape
     *lead, H = shape
     row_stride = H
     if not x.is_contiguous():
-        if x.dim() != 2 or x.stride(1) != 1 or x.stride(0) < H:
+        if len(shape) != 2 or x.stride(1) != 1 or x.stride(0) < H:
             raise ValueError("x must be contiguous, or 2-D with dense rows")
         row_stride = x.stride(0)
     n = x.numel()
@@ -695,9 +694,9 @@ def quantize_blocks_fp8(x, block_rows: int = 1, counts=None, out=None, scale=Non
     if tiles:
         rows = lead[-1]
         groups = n // (rows * H) if n else 0
-        lead = (*lead[:-1], _blocks(rows))
+        lead[-1] = _blocks(rows)
     if counts is not None:
-        if x.dim() != 3 or tiles:
+        if len(shape) != 3 or tiles:
             raise ValueError("with counts x must be [groups, rows, hidden], block_rows 1")
         groups, rows = lead
         _expect(counts, _torch.int32, (groups,), device, "counts")
@@ -708,11 +707,11 @@ def quantize_blocks_fp8(x, block_rows: int = 1, counts=None, out=None, scale=Non
         out = _empty(shape, _torch.float8_e4m3fn, device, stream, raw)
     else:
         _expect(out, _e4m3(out, "out"), shape, device, "out")
-    scales = (*lead, _blocks(H))
+    lead.append((H + MOE_SCALE_BLOCK - 1) // MOE_SCALE_BLOCK)
     if scale is None:
-        scale = _empty(scales, _torch.float32, device, stream, raw)
+        scale = _empty(lead, _torch.float32, device, stream, raw)
     else:
-        _expect(scale, _torch.float32, scales, device, "scale")
+        _expect(scale, _torch.float32, tuple(lead), device, "scale")
     st = _lib.moe_quantize_blocks_fp8(x.data_ptr(), bf16, groups, rows, H, row_stride, block_rows,
                                       0 if counts is None else counts.data_ptr(), out.data_ptr(),
                                       scale.data_ptr(), raw)
