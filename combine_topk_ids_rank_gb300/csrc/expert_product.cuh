@@ -5,6 +5,7 @@
 //
 //   op          lanes              columns        k
 //   kFp8        output channels    tokens         hidden size, 8-bit codes with block scales
+//   kFp8Narrow  the same, for groups of few tokens
 //   kForward    output channels    tokens         hidden size
 //   kInputGrad  hidden size        tokens         output channels
 //   kWeightGrad output channels    hidden size    tokens
@@ -16,19 +17,20 @@
 // bf16: pairs of CTAs (cta_group::2), 256 lanes by up to 256 columns a tile.
 // 8-bit: one CTA a tile, 128 lanes by up to 256 columns: its accumulators are
 // read after every block of k, and two CTAs' meeting takes longer than that.  An
-// accumulator's two halves of 128 columns are filled by an issuing warp each and
-// given back by themselves.
+// accumulator's two halves of 128 columns are filled by an issuing warp each, read
+// by four warps each and given back by themselves, so that no warp waits on a
+// barrier whose phases it does not see one by one.
 //
 // Both operands come by TMA with the 128-byte swizzle, 128 bytes of k (or 64
 // rows of k where k is not the innermost extent: MN-major tiles) a stage.
 // Warps of a CTA:
 //   0-7  epilogue: tensor-memory lanes 32 (w mod 4), half of the tile's columns;
-//   8    producer; kFp8: lists the CTA's tiles for the others as it goes;
-//   9    (of CTA 0 of a pair) issues the products; kFp8: of columns 0 to 127;
-//   10   kFp8: fetches the scales of tiles that are not turned; kWeightGrad:
+//   8    producer; 8-bit: lists the CTA's tiles for the others as it goes;
+//   9    (of CTA 0 of a pair) issues the products; 8-bit: of the first half;
+//   10   8-bit: fetches the scales of tiles that are not turned; kWeightGrad:
 //        clears what a last block of k holds of the next group's rows;
 //   11   lists the pair's tiles, a few ahead (finding the next tile takes 1500 to
-//        2000 cycles); kFp8: issues the products of columns 128 to 255.
+//        2000 cycles); 8-bit: issues the products of the second half.
 // Sums.  The tensor cores add in fp32 with truncation (measured on bf16 normal
 // values against 64 bits: 4.7e-7 of the result's norm after 512 products, 2.1e-6
 // after 2048, 9.1e-6 after 8192), so what is kept in 32 bits (kWeightGrad) leaves
@@ -41,6 +43,24 @@
 // (tokens as columns), or each tile into equal parts (kWeightGrad).  The parts
 // go through memory; the CTA that finishes last adds them in ascending k, so the
 // order of the additions does not depend on timing.
+//
+// Bounds (device time of calls in a row, at 2.07 GHz or the power cap).
+//   kFp8, 8192 x 4096 x 7168: 210 us, 2290 TFLOP/s.  The products alone take 154 us,
+//     with the epilogue's reads and meetings 182: the rest is its 256 additions a block
+//     and SM sub-partition, which wait for reads and barriers in between (1000 cycles a
+//     block, 810 the products).  Pairs of CTAs: 337 us; additions held in
+//     64-bit pairs throughout: 294; one issuing warp: 220.
+//   kFp8, 32 planes of up to 1024 rows, 4096 x 2048: 120 to 138 us by the counts (57 at the
+//     memory's rate): 16 blocks a tile, then 3400 cycles to store it.
+//   kFp8Narrow, 16 x 7168 x 4096: 13.0 us (4.4): 2 us to the first load, DRAM latency, the
+//     last reads.  333 x 1000 x 1040: 9.6 us; with turned tiles 13.
+//   kForward, 16384 rows of 32 groups, 4096 x 2048: one group 150 us (1840 TFLOP/s, the
+//     power cap), even groups 162, uneven ones 186 (1480 TFLOP/s; 570 cycles a block where
+//     the products need 420 on average: about 50 bytes a cycle and SM come from L2).
+//     kInputGrad: 145, 171 and 183.  Prefetching weights into L2: 197.
+//   kForward, 8 rows of 128 groups, 1536 x 2048: 12 us (7.4).
+//   kWeightGrad, the same 16384 rows: 162, 204 and 222 us (537 MB of output), fp32 283: tiles
+//     of eight blocks, between which the issuer waits 1500 cycles for the next operands.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -111,7 +131,7 @@ struct Shape {
     int turn_from;  // tokens that make a group's tiles turned
     int shift;      // columns of a tile that is not, at most: 1 << shift
     int even;       // tiles of a group are evened out (else: full ones and what is left)
-    int thin;       // kFp8Narrow: a tile has 64 lanes only, so that none is cut
+    int thin;       // kFp8Narrow: a tile has 64 lanes only, so that few are cut
 
     __device__ bool turned(int c) const { return OP == kFp8 && c >= turn_from; }
     // Tiles along the channels, and along `c` tokens (or the maps' columns).
@@ -315,7 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ __align__(16) float s_scale[kScaleFloats];
     // (pairs.  full, acc_free: CTA 0's, both CTAs arrive; empty, acc_full: either's own)
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tail[kMaxStages];
-    __shared__ uint64_t acc_full[kAccs][2], acc_free[kAccs][2], sc_full[kScaleSlots], sc_free[kScaleSlots];
+    __shared__ uint64_t acc_full[kAccs][2], acc_free[kAccs][2];
+    __shared__ uint64_t sc_full[kScaleSlots], sc_free[kScaleSlots];
     __shared__ uint64_t seg_full[kSegs], seg_free[kSegs], drained;
     __shared__ Seg segs[kSegs];
     __shared__ Plan<OP> plan;
@@ -406,9 +427,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     // the pair's barriers are set up before either arrives on the other's
     if (PAIR) ptx::cluster_arrive();
+    // Offsets that descend may repeat rows, and so count more tiles than 32 bits hold: then
+    // there is no work at all.  (Others stay below the host's limit.)
+    int tiles = plan.sums[0];
+    if (!KRAGGED && p.offsets != nullptr &&
+        (long long)p.G * shape.tiles(p.M, p.lanes) >= 1 << 29) {
+        bool down = false;
+        for (int g = tid; g < p.G; g += kThreads)
+            down = down || __ldg(p.offsets + g + 1) < __ldg(p.offsets + g);
+        if (__syncthreads_or(down)) tiles = 0;
+    }
     // Few tiles: narrower ones while each still finds an idle pair (333 x 1000 x 1040 in
     // 8 bits: 12 turned tiles of nine blocks, or 56 of 48 columns).
-    int tiles = plan.sums[0];
     if (!KRAGGED && tiles * 2 <= pairs) {
         const int l = (p.lanes + kLanes - 1) / kLanes;
         for (int i = 1; i < 4; ++i)
@@ -419,7 +449,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
     }
     // 8-bit, fewer tiles than half the SMs: of 64 lanes instead of cut ones (one SM can
-    // take more than its share of the memory's rate, and no part goes through memory)
+    // take more than its share of the memory's rate, and no part goes through memory;
+    // 16 x 7168 x 4096: 13.0 us, 14.3 with 128 lanes)
     if (OP == kFp8Narrow && tiles * 2 <= pairs) {
         shape.thin = 1;
         tiles = plan.sums[8 - shape.shift] * ((p.lanes + 63) / 64);
@@ -601,8 +632,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // columns of this CTA; its first lane and column; the group's first row
                     const int half = (sg.cols + 15) / 16 * (16 / kCtas);
                     const bool thin = OP == kFp8Narrow && plan.shape.thin;
-                    const int a0 = sg.l * (OP == kFp8 && sg.turned ? kMaxCols : (thin ? 64 : kLanes)) +
-                                   rank * kTileRows;
+                    const int tall = OP == kFp8 && sg.turned ? kMaxCols : (thin ? 64 : kLanes);
+                    const int a0 = sg.l * tall + rank * kTileRows;
                     const int at = plan.start[sg.g];
                     const int b0 = (KRAGGED ? 0 : at) + sg.c0 + rank * half;
                     int left = KRAGGED ? plan.count[sg.g] - sg.k0 * 64 : 64;  // rows of k
@@ -785,7 +816,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // turned, four blocks of k (a run) at a time, for each column.
                     if (OP == kFp8 && sg.turned) continue;
                     const int KB = blocks, NB = (p.lanes + kScaleBlock - 1) / kScaleBlock;
-                    const bool vec = KB % 4 == 0 && reinterpret_cast<uintptr_t>(p.x_scale) % 16 == 0;
+                    const bool vec =
+                        KB % 4 == 0 && reinterpret_cast<uintptr_t>(p.x_scale) % 16 == 0;
                     const int nb = OP == kFp8Narrow && plan.shape.thin ? sg.l / 2 : sg.l;
                     const float *sw = p.w_scale + ((size_t)sg.g * NB + nb) * KB;
                     const float *sx = p.x_scale + ((size_t)plan.start[sg.g] + sg.c0 + lane) * KB;
@@ -841,8 +873,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int chunks = ((rows + 15) / 16 * 16 - rows) * (kAtom / 16);
                         for (int i = lane; i < panels * chunks; i += 32) {
                             const int panel = i / chunks, c = i - panel * chunks;
-                            *reinterpret_cast<uint4 *>(a_of(st.at) + panel * kPanelBytes +
-                                                       rows * kAtom + c * 16) = make_uint4(0, 0, 0, 0);
+                            uint8_t *at = a_of(st.at) + panel * kPanelBytes + rows * kAtom;
+                            reinterpret_cast<uint4 *>(at)[c] = make_uint4(0, 0, 0, 0);
                         }
                         ptx::fence_proxy_async_smem();  // read next by the tensor cores
                         __syncwarp();
@@ -990,7 +1022,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 __byte_perm(mine2, __shfl_xor_sync(0xffffffffu, mine2, 1), pick);
                             if (words) {
                                 if (live && 2 * j < left) *reinterpret_cast<uint32_t *>(at) = both;
-                            } else if (2 * j < left) {  // odd extent or address: rows start off a word
+                            } else if (2 * j < left) {  // rows may start off a word
                                 if ((chan & ~1) < p.lanes) at[0] = (uint16_t)both;
                                 if ((chan | 1) < p.lanes) at[1] = (uint16_t)(both >> 16);
                             }
@@ -1021,8 +1053,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(f[j]);
                                 store_256(o, w);
                             } else {
-                                reinterpret_cast<float4 *>(o)[0] = make_float4(f[0], f[1], f[2], f[3]);
-                                reinterpret_cast<float4 *>(o)[1] = make_float4(f[4], f[5], f[6], f[7]);
+                                float4 *o4 = reinterpret_cast<float4 *>(o);
+                                o4[0] = make_float4(f[0], f[1], f[2], f[3]);
+                                o4[1] = make_float4(f[4], f[5], f[6], f[7]);
                             }
                         }
                     }
@@ -1030,7 +1063,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (KRAGGED && p.boxes && sg.whole) {
                     // Boxes of 32 rows by 128 bytes, through shared memory (128-byte swizzle),
                     // clipped at the map's last row by the tensor map.
-                    uint8_t *box = smem + (kDynamic - 1024 - boxes) + (warp) * kBoxBytes;
+                    uint8_t *box = smem + (kDynamic - 1024 - boxes) + warp * kBoxBytes;
                     const int y = sg.l * kLanes + rank * kTileRows + q * 32;
                     const int each = p.f32 ? 2 : 4;  // steps of a box
                     if (y < p.lanes)
@@ -1096,8 +1129,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     auto part_of = [&](int c) {
                         const int slot = c == p0 ? slot0 : 0;
-                        return p.part + (size_t)(2 * (kCtas * c + rank) + slot) * p.nmax * kTileRows +
-                               row;
+                        const size_t at = 2 * (kCtas * c + rank) + slot;
+                        return p.part + at * p.nmax * kTileRows + row;
                     };
                     float *part = part_of(pair) + n0 * kTileRows;
 #pragma unroll 1
@@ -1137,7 +1170,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             };
             if constexpr (is_fp8(OP)) {
-                const auto scales = [&](int kb) {  // of block kb; (a new run's: once they are there)
+                const auto scales = [&](int kb) {  // of block kb; a new run's once they are there
                     if (kb % kScaleRun == 0 || kb == sg.k0) wait_for(&sc_full[sc.at], sc.parity);
                     return s_scale + (sc.at * kScaleRun + kb % kScaleRun) * kFp8Cols;
                 };
@@ -1152,7 +1185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // Four reads of 32 columns a block, the last of which is added when the
                     // accumulator's half has been given back.  (Reads in flight beside the
                     // additions take registers that are not there: 193 to 294 us for 8192 x
-                    // 4096 x 7168, by what the compiler made of it; so 211 us.)
+                    // 4096 x 7168, by what the compiler made of it; so 210 us.)
                     constexpr int kHeld = 32;
                     uint32_t u[kHeld];
                     float sum[kSteps][kStep];
@@ -1171,7 +1204,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // Scales of this lane's token, four blocks (a run) at a time, a run ahead.
                     const int KB = plan.blocks, NB = (p.lanes + kScaleBlock - 1) / kScaleBlock;
                     const bool there = row < sg.cols;
-                    const bool vec = KB % 4 == 0 && reinterpret_cast<uintptr_t>(p.x_scale) % 16 == 0;
+                    const bool vec =
+                        KB % 4 == 0 && reinterpret_cast<uintptr_t>(p.x_scale) % 16 == 0;
                     const float *sx = p.x_scale + ((size_t)plan.start[sg.g] + sg.c0 + row) * KB;
                     const float *sw =
                         p.w_scale + ((size_t)sg.g * NB + min(2 * sg.l + hf, NB - 1)) * KB;
@@ -1222,14 +1256,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int n0 = first_of(), k0 = sg.k0, k1 = sg.k1;
                     float sum[kNarrow][kStep];
                     clear(sum);
-                    const auto add = [&](float (&t)[kStep], const uint32_t (&v)[kStep], const float *f) {
+                    const auto add = [&](float (&t)[kStep], const uint32_t (&v)[kStep],
+                                         const float *f) {
 #pragma unroll
-                        for (int j = 0; j < kStep / 4; ++j) {
-                            const float4 f4 = reinterpret_cast<const float4 *>(f)[j];
-                            t[4 * j] = __fmaf_rn(__uint_as_float(v[4 * j]), f4.x, t[4 * j]);
-                            t[4 * j + 1] = __fmaf_rn(__uint_as_float(v[4 * j + 1]), f4.y, t[4 * j + 1]);
-                            t[4 * j + 2] = __fmaf_rn(__uint_as_float(v[4 * j + 2]), f4.z, t[4 * j + 2]);
-                            t[4 * j + 3] = __fmaf_rn(__uint_as_float(v[4 * j + 3]), f4.w, t[4 * j + 3]);
+                        for (int j = 0; j < kStep; j += 4) {
+                            const float4 f4 = *reinterpret_cast<const float4 *>(f + j);
+                            t[j] = __fmaf_rn(__uint_as_float(v[j]), f4.x, t[j]);
+                            t[j + 1] = __fmaf_rn(__uint_as_float(v[j + 1]), f4.y, t[j + 1]);
+                            t[j + 2] = __fmaf_rn(__uint_as_float(v[j + 2]), f4.z, t[j + 2]);
+                            t[j + 3] = __fmaf_rn(__uint_as_float(v[j + 3]), f4.w, t[j + 3]);
                         }
                     };
                     const uint32_t mine_half = mine + hf * kHalfCols;
@@ -1263,9 +1298,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     if (i >= steps) break;
                                     tc::wait_ld(u[i & 1]);
                                     // (the last one once more: past it may be no column)
-                                    tc::ld_32x16(at + min(i + 1, steps - 1) * kStep, u[(i + 1) & 1]);
+                                    const int next = min(i + 1, steps - 1);
+                                    tc::ld_32x16(at + next * kStep, u[(i + 1) & 1]);
                                     add(sum[i], u[i & 1], f + i * kStep);
                                 }
+                                tc::wait_ld();  // the one that was not used
                                 scales_read(b);
                             }
                             if (to < k1) release();
@@ -1303,6 +1340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int j = 0; j < kStep; ++j)
                                 sum[i][j] = __fadd_rn(sum[i][j], __uint_as_float(u[i & 1][j]));
                         }
+                        tc::wait_ld();  // the one that was not used
                         kb = kRun < k1 - kb ? kb + kRun : k1;
                         if (kb < k1) release();
                     }

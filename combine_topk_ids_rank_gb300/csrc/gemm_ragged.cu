@@ -39,8 +39,9 @@ cudaError_t launch_gemm_ragged_weight_grad(ProductParams p, const void *dy, cons
     if (!map_2d(&a, dy, p.M, p.lanes, 64, 64, false) ||
         !map_2d(&b, x, p.M, p.cols, 64, 64, false))
         return cudaErrorInvalidValue;
-    // Boxes of 128 bytes by 32 rows where tiles end with a box (fp32 as pairs of words); 16
-    // rows of every kind of type a store otherwise (32 x 512 rows, 4096 x 2048: 214 us).
+    // Whole tiles are stored as boxes of 128 bytes by 32 rows where every tile ends with a box
+    // (fp32 as pairs of 16-bit words), else row by row from the lanes.  (32 groups of 512 rows,
+    // 4096 x 2048: bf16 203 and 214 us, fp32 287 and 340.)
     p.boxes = p.cols % 128 == 0 && !p.accumulate;
     if (!p.boxes) out = b;
     else if (!map_3d(&out, p.out, p.G, p.lanes, (long long)p.cols * (p.f32 ? 2 : 1), 64, kBoxRows,

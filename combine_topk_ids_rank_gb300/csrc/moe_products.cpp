@@ -9,15 +9,15 @@ namespace {
 
 using namespace moe;
 
-// Extents that every product takes: 32-bit coordinates and tile numbers.  `wide`:
-// columns of all groups together.
+// Extents that every product takes: 32-bit coordinates, and twice the number of tiles.
+// `wide`: columns of all groups together.
 bool extents_ok(int64_t groups, int64_t rows, int64_t lanes, int64_t wide, int64_t depth) {
     if (rows > kProductMaxExtent || lanes > kProductMaxExtent || wide > kProductMaxExtent ||
-        depth > kProductMaxExtent || groups * lanes > kProductMaxExtent ||
+        depth > kProductMaxDepth || groups * lanes > kProductMaxExtent ||
         groups * depth > kProductMaxExtent)
         return false;
-    // (a group may end with a tile that is not full)
-    return (lanes + 255) / 256 * (wide / 128 + groups) <= INT32_MAX / 2;
+    // (the smallest tiles of a call with many; a group may end with one that is not full)
+    return (lanes + 127) / 128 * (wide / 128 + groups) <= INT32_MAX / 2;
 }
 
 ProductParams params(const int32_t *counts, const int32_t *offsets, void *out, void *scratch,
@@ -62,7 +62,8 @@ int moe_quantize_blocks_fp8(const void *d_x, int32_t bf16, int32_t groups, int32
                             const int32_t *d_counts, void *d_q, float *d_scale, void *stream) {
     const int vec = bf16 ? 8 : 4;  // elements of a 16-byte load
     if (groups < 0 || rows < 0 || hidden < 16 || hidden % 16 != 0 ||
-        hidden > kProductMaxExtent || row_stride < hidden || row_stride % vec != 0 ||
+        hidden > kProductMaxExtent || rows > kProductMaxExtent || row_stride < hidden ||
+        row_stride % vec != 0 ||
         (block_rows != 1 && block_rows != kScaleBlock) ||
         (d_counts != nullptr && block_rows != 1))
         return MOE_ERR_INVALID_ARG;
@@ -83,7 +84,9 @@ int moe_quantize_blocks_fp8(const void *d_x, int32_t bf16, int32_t groups, int32
     p.H = hidden;
     p.block_rows = block_rows;
     p.bf16 = bf16 != 0;
-    return launched([&] { return launch_quantize_blocks(p, sms, static_cast<cudaStream_t>(stream)); });
+    return launched([&] {
+        return launch_quantize_blocks(p, sms, static_cast<cudaStream_t>(stream));
+    });
 }
 
 size_t moe_gemm_fp8_scratch_bytes(int32_t rows) {

@@ -34,6 +34,10 @@ cudaError_t launch_quantize_blocks(const QuantBlocksParams &p, int num_sms, cuda
 constexpr int kProductMaxGroups = 1024;
 // 32-bit coordinates, with room for rounding up to whole tiles
 constexpr int kProductMaxExtent = INT32_MAX - (1 << 24);
+// of k, where tiles are cut along it: the blocks of all cut tiles are numbered with 32 bits
+constexpr int kProductMaxDepth = 1 << 28;
+static_assert((long long)kStreamMaxCtas * 5 / 4 * 2 * (kProductMaxDepth / 64) <= INT32_MAX,
+              "numbers of blocks (twice that in between)");
 constexpr int kProductMaxCols = 256;  // columns of a tile, at most
 
 struct ProductParams {
@@ -51,13 +55,13 @@ struct ProductParams {
     int boxes;               // its whole tiles are stored as boxes (set by the launcher)
 };
 
-// Columns a part needs for M rows of tokens (an 8-bit group of kProductTurnFrom
-// tokens or more may have tiles of 128 channels).
+// Columns a part of the 8-bit product needs for M rows of tokens (a group of
+// kProductTurnFrom tokens or more may have tiles of kProductMaxCols channels).
 constexpr int kProductTurnFrom = 81;
-static_assert(kProductTurnFrom > 64, "parts of 128 columns");
 inline int product_nmax(int M) {
+    if (M >= kProductTurnFrom) return kProductMaxCols;
     int n = 16;
-    while (n < M && n < kProductMaxCols) n *= 2;
+    while (n < M) n *= 2;
     return n;
 }
 

@@ -602,12 +602,14 @@ int moe_quantize_blocks_fp8(const void *d_x, int32_t bf16, int32_t groups, int32
  * clamped to 0..rows); or one group after another, d_offsets int32
  * [groups + 1], ascending: group g has rows d_offsets[g] <= m < d_offsets[g+1]
  * of `rows`, and rows of no group are not written (offsets are clamped to
- * 0..rows; those of a group that would begin past its end are none).  Not both.
+ * 0..rows; a group that would begin past its end has none; rows that descending
+ * offsets give to several groups are undefined).  Not both.
  *   d_xq e4m3 [..rows][hidden], d_x_scale fp32 [..rows][ceil(hidden / 128)]
  *   d_wq e4m3 [groups][N][hidden],
  *   d_w_scale fp32 [groups][ceil(N / 128)][ceil(hidden / 128)]
- *   hidden  a multiple of 16; N and rows any; groups <= 1024; hidden, all rows,
- *           groups * N, groups * hidden < 2^31 - 2^24
+ *   hidden  a multiple of 16, at most 2^28; N and rows any; groups <= 1024; all rows,
+ *           groups * N, groups * hidden at most 2^31 - 2^24 - 1, tiles of 128 x 128
+ *           outputs fewer than 2^30
  *   d_out   bf16 [..rows][N]
  *   d_scratch at least moe_gemm_fp8_scratch_bytes(rows) bytes, as for
  *           moe_gemm_int8
@@ -631,8 +633,9 @@ int moe_gemm_fp8(const void *d_xq, const float *d_x_scale, const void *d_wq,
  * bf16 operands, fp32 sums.  Rows of no expert are not written (and take no
  * part in dW); the dW of an expert without rows is zero.
  *   hidden  a multiple of 8; N any, a multiple of 8 for the gradients;
- *           groups <= 1024; limits as for moe_gemm_fp8 (weight gradient:
- *           groups * hidden and the tiles of 256 x 256 of all maps < 2^30)
+ *           groups <= 1024; limits as for moe_gemm_fp8 (the input gradient sums over
+ *           N: N at most 2^28; the weight gradient over rows: hidden has no such
+ *           limit, and the tiles are those of all maps)
  *   d_x bf16 [rows][hidden], d_dy bf16 [rows][N], d_w bf16 [groups][N][hidden]:
  *           16-byte aligned; d_out, d_dx bf16; d_dw 16-byte aligned.  Outputs
  *           overlap no input.
