@@ -1243,7 +1243,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                             add(u, i, f);
                         }
                     }
-                    if (ok) {
+                    if (ok && sg.whole && p.lanes % 16 == 0 &&
+                        reinterpret_cast<uintptr_t>(p.out) % 32 == 0) {
+                        release();
+                        // Four lanes exchange 32-byte chunks, so that together they store 128
+                        // bytes of one row after another.
+                        const int t = lane & 3, c0 = sg.l * kMaxCols + hf * kHalfCols + t * kStep;
+                        uint16_t *const o =
+                            static_cast<uint16_t *>(p.out) +
+                            ((size_t)plan.start[sg.g] + sg.c0 + (row & ~3)) * p.lanes + c0;
+#pragma unroll
+                        for (int i = 0; i < kSteps; i += 4) {
+                            uint32_t w[4][8];
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    const __nv_bfloat162 two = __floats2bfloat162_rn(
+                                        sum[i + c][2 * j], sum[i + c][2 * j + 1]);
+                                    w[c][j] = *reinterpret_cast<const uint32_t *>(&two);
+                                }
+#pragma unroll
+                            for (int b = 1; b < 4; b *= 2)
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) {
+                                    if (c & b) continue;
+#pragma unroll
+                                    for (int j = 0; j < 8; ++j) {
+                                        const uint32_t give = t & b ? w[c][j] : w[c | b][j];
+                                        const uint32_t got = __shfl_xor_sync(0xffffffffu, give, b);
+                                        if (t & b) w[c][j] = got;
+                                        else w[c | b][j] = got;
+                                    }
+                                }
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                if (c0 + i * kStep < p.lanes && (row & ~3) + c < sg.cols)
+                                    store_256(o + (size_t)c * p.lanes + i * kStep, w[c]);
+                        }
+                    } else if (ok) {
                         const uint32_t at = mine + acc.at * kMaxCols + hf * kHalfCols;
                         keep(at, sum);
                         finish(at, false);
