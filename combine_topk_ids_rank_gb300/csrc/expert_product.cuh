@@ -45,13 +45,12 @@
 // order of the additions does not depend on timing.
 //
 // Bounds (device time of calls in a row, at 2.07 GHz or the power cap).
-//   kFp8, 8192 x 4096 x 7168: 210 us, 2290 TFLOP/s.  The products alone take 154 us,
+//   kFp8, 8192 x 4096 x 7168: 195 us, 2460 TFLOP/s.  The products alone take 154 us,
 //     with the epilogue's reads and meetings 182: the rest is its 256 additions a block
-//     and SM sub-partition, which wait for reads and barriers in between (1000 cycles a
-//     block, 810 the products).  Pairs of CTAs: 337 us; additions held in
-//     64-bit pairs throughout: 294; one issuing warp: 220.
-//   kFp8, 32 planes of up to 1024 rows, 4096 x 2048: 120 to 138 us by the counts (57 at the
-//     memory's rate): 16 blocks a tile, then 3400 cycles to store it.
+//     and SM sub-partition, which wait for reads and barriers in between.  Pairs of CTAs:
+//     337 us; reads in flight beside the additions: 197; each lane storing its own row: 210.
+//   kFp8, 32 planes of up to 1024 rows (12388 in all), 4096 x 2048: 125 us (57 at the memory's
+//     rate): tiles of 16 blocks, 15% of their rows empty; lanes storing their own rows: 139.
 //   kFp8Narrow, 16 x 7168 x 4096: 13.0 us (4.4): 2 us to the first load, DRAM latency, the
 //     last reads.  333 x 1000 x 1040: 9.6 us; with turned tiles 13.
 //   kForward, 16384 rows of 32 groups, 4096 x 2048: one group 150 us (1840 TFLOP/s, the
@@ -59,8 +58,9 @@
 //     the products need 420 on average: about 50 bytes a cycle and SM come from L2).
 //     kInputGrad: 145, 171 and 183.  Prefetching weights into L2: 197.
 //   kForward, 8 rows of 128 groups, 1536 x 2048: 12 us (7.4).
-//   kWeightGrad, the same 16384 rows: 162, 204 and 222 us (537 MB of output), fp32 283: tiles
-//     of eight blocks, between which the issuer waits 1500 cycles for the next operands.
+//   kWeightGrad, the same 16384 rows: 162, 187 and 215 us (537 MB of output), fp32 278:
+//     even tiles have eight blocks at 0.87 of the dense rate; tiles of less than six wait
+//     for the memory that takes their outputs.  Groups large and small in turn: 214 to 219.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -106,6 +106,11 @@ constexpr int kBoxRows = 32, kBoxBytes = kBoxRows * kAtom;  // an output box of 
 constexpr int kClasses = 64;
 constexpr int kGradRun = 8;       // blocks of 64 rows of k that stay in tensor memory
 constexpr int kMinPart = 4;       // blocks of k that make a part worth its way through memory
+// kWeightGrad: a group's rows of up to this many bytes are fetched into L2 when its first
+// tile is listed: all pairs come to a group at the same time, and then wait for memory.
+// (32 groups of 512 rows, 6 MB each: 187 us, 196 without; uneven groups up to 18 MB: 215 us,
+// 216 without, 218 with those above 8 MB too.)
+constexpr long long kAheadBytes = 8 << 20;
 constexpr int kFp8Cols = 128;     // columns of an 8-bit tile that is not turned, at most
 
 constexpr int ctas_of(Op op) { return is_fp8(op) ? 1 : 2; }
@@ -315,6 +320,15 @@ __device__ __forceinline__ void store_256(void *p, const uint32_t (&v)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
                  "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
+}
+
+// This CTA's share of `bytes` bytes (a multiple of 16) from `p` on, into L2.
+__device__ __forceinline__ void prefetch_share(const void *p, long long bytes) {
+    const long long each = (bytes / gridDim.x + 127) / 128 * 128, at = each * blockIdx.x;
+    if (at >= bytes) return;
+    const uint32_t n = (uint32_t)(bytes - at < each ? bytes - at : each);
+    const char *from = static_cast<const char *>(p) + at;
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(n) : "memory");
 }
 
 template <Op OP>
@@ -589,9 +603,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!is_fp8(OP) && warp == kListWarp) {
             if (ptx::elect_one()) {
                 Work<OP> work(plan);
+                int seen = -1;
                 for (bool more = true; more && !s_failed; sq.next()) {
                     Seg s;
                     more = work.next(p, s);
+                    if (KRAGGED && more && s.g != seen) {
+                        seen = s.g;
+                        const long long at = plan.start[s.g], n = plan.count[s.g];
+                        const long long a = (long long)p.lanes * 2, b = (long long)p.cols * 2;
+                        if (n * (a + b) <= kAheadBytes) {
+                            prefetch_share(static_cast<const char *>(p.a) + at * a, n * a);
+                            prefetch_share(static_cast<const char *>(p.b) + at * b, n * b);
+                        }
+                    }
                     if (!ptx::mbar_park(&seg_free[sq.at], sq.parity ^ 1u, kWaitNs)) {
                         s_failed = 1;
                         break;
@@ -1184,8 +1208,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (OP == kFp8 && sg.turned) {
                     // Four reads of 32 columns a block, the last of which is added when the
                     // accumulator's half has been given back.  (Reads in flight beside the
-                    // additions take registers that are not there: 193 to 294 us for 8192 x
-                    // 4096 x 7168, by what the compiler made of it; so 210 us.)
+                    // additions gain nothing, or take registers that are not there: 197 to
+                    // 294 us for 8192 x 4096 x 7168, by how; so 195 us.)
                     constexpr int kHeld = 32;
                     uint32_t u[kHeld];
                     float sum[kSteps][kStep];

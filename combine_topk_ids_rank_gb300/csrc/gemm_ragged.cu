@@ -42,6 +42,8 @@ cudaError_t launch_gemm_ragged_weight_grad(ProductParams p, const void *dy, cons
     // Whole tiles are stored as boxes of 128 bytes by 32 rows where every tile ends with a box
     // (fp32 as pairs of 16-bit words), else row by row from the lanes.  (32 groups of 512 rows,
     // 4096 x 2048: bf16 203 and 214 us, fp32 287 and 340.)
+    p.a = dy;
+    p.b = x;
     p.boxes = p.cols % 128 == 0 && !p.accumulate;
     if (!p.boxes) out = b;
     else if (!map_3d(&out, p.out, p.G, p.lanes, (long long)p.cols * (p.f32 ? 2 : 1), 64, kBoxRows,

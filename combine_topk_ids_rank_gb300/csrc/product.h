@@ -44,6 +44,7 @@ struct ProductParams {
     const int32_t *counts;   // [G] rows in use of each plane, or null
     const int32_t *offsets;  // [G + 1] first row of each group, or null (planes)
     const float *x_scale, *w_scale;  // 8-bit product
+    const void *a, *b;       // gradient of the maps: dy and x
     void *out;
     StreamHeader *header;
     float *part;             // [CTAs][2][nmax][128]
