@@ -1,5 +1,5 @@
 // pair.cuh -- inline PTX of the persistent products (layer_small.cu,
-// gemm_int8.cu) beside ptx.cuh: the electing branch, clusters, parked waits.
+// gemm_int8.cu, expert_product.cuh) beside ptx.cuh: the electing branch, clusters, parked waits.
 #pragma once
 
 #include "ptx.cuh"

@@ -57,8 +57,10 @@ struct ProductParams {
 };
 
 // Columns a part of the 8-bit product needs for M rows of tokens (a group of
-// kProductTurnFrom tokens or more may have tiles of kProductMaxCols channels).
-constexpr int kProductTurnFrom = 81;
+// kProductTurnFrom tokens or more may have tiles of kProductMaxCols channels; for fewer
+// tokens as columns are faster: 32 groups of 4096 x 2048, 32 tokens each 49 and 54 us, 33
+// tokens 55 and 54, 64 tokens 60 and 55, 128 tokens 77 and 59).
+constexpr int kProductTurnFrom = 33;
 inline int product_nmax(int M) {
     if (M >= kProductTurnFrom) return kProductMaxCols;
     int n = 16;

@@ -1,5 +1,6 @@
 // stream.cuh -- what the two persistent products that stream weights through
-// the tensor cores share (layer_small.cu, gemm_int8.cu): the even split of
+// the tensor cores share (layer_small.cu, gemm_int8.cu; the split and the merge
+// also expert_product.cuh): the even split of
 // the k-blocks of all output tiles over the CTAs, the widening of 8-bit
 // weight rows into tensor memory, and waits on counters in global memory.
 //

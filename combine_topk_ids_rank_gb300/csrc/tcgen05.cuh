@@ -1,7 +1,7 @@
 // tcgen05.cuh -- inline-PTX wrappers for the sm_100-family tensor cores
 // (tcgen05: MMA from shared-memory descriptors or tensor memory into tensor
-// memory) and the tiled TMA load, as used by expert_gemm.cu, layer_small.cu
-// and gemm_int8.cu.
+// memory) and the tiled TMA load, as used by expert_gemm.cu, layer_small.cu,
+// gemm_int8.cu and expert_product.cuh.
 //
 // Encodings (PTX ISA, "Tensor Memory" and "tcgen05.mma" sections):
 //  * shared-memory matrix descriptor (64 bits): start address >> 4 in

@@ -163,8 +163,8 @@ def test_eight_bit_experts_behind_a_dispatch(api):
         assert torch.equal(out.double(), bf(want))
 
 
-@pytest.mark.parametrize("M", [81, 100, 128])
-def test_cut_tiles_of_planes_of_about_a_hundred_rows(api, M):
+@pytest.mark.parametrize("M", [33, 64, 65, 81, 100, 128])
+def test_cut_tiles_of_planes_of_up_to_a_tile_of_rows(api, M):
     """Tiles of 256 channels, cut along a long hidden size."""
     G, N, H = 10, 2560, 8192
     g = gen(M)

@@ -86,6 +86,6 @@ def test_sizes_past_the_limits_are_refused(abi):
 
 
 def test_a_part_has_room_for_the_widest_tile(abi):
-    """Scratch of the 8-bit product: tiles of 256 channels from 81 rows on."""
+    """Scratch of the 8-bit product: tiles of 256 channels from 33 rows on."""
     size = abi.moe_gemm_fp8_scratch_bytes
-    assert size(16) < size(17) < size(64) == size(33) < size(80) < size(81) == size(1 << 20)
+    assert size(16) < size(17) == size(32) < size(33) == size(1 << 20)
