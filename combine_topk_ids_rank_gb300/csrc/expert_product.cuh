@@ -58,7 +58,8 @@
 //     the products need 420 on average: about 50 bytes a cycle and SM come from L2).
 //     kInputGrad: 145, 171 and 183.  Prefetching weights into L2: 197.
 //   kForward, 8 rows of 128 groups, 1536 x 2048: 12 us (7.4).
-//   kWeightGrad, the same 16384 rows: 162, 187 and 215 us (537 MB of output), fp32 278:
+//   kWeightGrad, the same 16384 rows: 162, 187 and 215 us (537 MB of output), fp32 278, added to
+//     fp32 448 (2.15 GB, 317 at the copy's rate; each lane adding to its own row: 700):
 //     even tiles have eight blocks at 0.87 of the dense rate; tiles of less than six wait
 //     for the memory that takes their outputs.  Groups large and small in turn: 214 to 219.
 #pragma once
@@ -1054,22 +1055,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else if (!p.f32) {
                         store_row(out16 + to + n, v, left);
                     } else {
+                        float *const o16 = static_cast<float *>(p.out) + to + n;
+                        float4 old[kStep / 4];
+#pragma unroll
+                        for (int j = 0; j < kStep / 4; ++j)
+                            old[j] = p.accumulate && 4 * j < left
+                                         ? reinterpret_cast<const float4 *>(o16)[j]
+                                         : make_float4(-0.0f, -0.0f, -0.0f, -0.0f);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             if (8 * h >= left) break;
-                            float *o = static_cast<float *>(p.out) + to + n + 8 * h;
+                            float *o = o16 + 8 * h;
                             float f[8];
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) f[j] = v[8 * h + j];
-                            if (p.accumulate) {
-#pragma unroll
-                                for (int j = 0; j < 2; ++j) {
-                                    const float4 old = reinterpret_cast<const float4 *>(o)[j];
-                                    f[4 * j] = old.x + f[4 * j];
-                                    f[4 * j + 1] = old.y + f[4 * j + 1];
-                                    f[4 * j + 2] = old.z + f[4 * j + 2];
-                                    f[4 * j + 3] = old.w + f[4 * j + 3];
-                                }
+                            for (int j = 0; j < 2; ++j) {
+                                f[4 * j] = old[2 * h + j].x + v[8 * h + 4 * j];
+                                f[4 * j + 1] = old[2 * h + j].y + v[8 * h + 4 * j + 1];
+                                f[4 * j + 2] = old[2 * h + j].z + v[8 * h + 4 * j + 2];
+                                f[4 * j + 3] = old[2 * h + j].w + v[8 * h + 4 * j + 3];
                             }
                             if (reinterpret_cast<uintptr_t>(p.out) % 32 == 0) {
                                 uint32_t w[8];
@@ -1084,9 +1087,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 };
+                // (adding nothing to what is there: left alone)
+                if (KRAGGED && p.accumulate && none) return;
                 if (KRAGGED && p.boxes && sg.whole) {
                     // Boxes of 32 rows by 128 bytes, through shared memory (128-byte swizzle),
-                    // clipped at the map's last row by the tensor map.
+                    // clipped at the map's last row by the tensor map.  (Added: in L2, once for
+                    // every value, so the order of the CTAs changes nothing.)
                     uint8_t *box = smem + (kDynamic - 1024 - boxes) + warp * kBoxBytes;
                     const int y = sg.l * kLanes + rank * kTileRows + q * 32;
                     const int each = p.f32 ? 2 : 4;  // steps of a box
@@ -1126,13 +1132,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                             __syncwarp();
                             if (lane == 0) {
                                 const int x = sg.c0 + n0 + i * kStep;
-                                tc::tma_store_3d(&map_b8, p.f32 ? 2 * x : x, y, sg.g, box);
+                                if (p.accumulate) tc::tma_add_3d(&map_b8, x, y, sg.g, box);
+                                else tc::tma_store_3d(&map_b8, x, y, sg.g, box);
                                 ptx::bulk_commit();
                             }
                         }
                 } else if (sg.whole) {
-                    // (adding nothing to what is there: left alone)
-                    if (KRAGGED && p.accumulate && none) return;
 #pragma unroll 1
                     for (int i = 0; i < steps; i += 2) {
                         float v[2][kStep];
@@ -1449,10 +1454,10 @@ inline bool map_2d(CUtensorMap *m, const void *base, long long rows, long long c
 
 // `groups` matrices one after another.
 inline bool map_3d(CUtensorMap *m, const void *base, long long groups, long long rows,
-                   long long cols, int box_cols, int box_rows, bool bytes) {
+                   long long cols, int box_cols, int box_rows, bool bytes, bool f32 = false) {
     const long long ext[3] = {cols, rows, groups}, str[3] = {1, cols, rows * cols};
     const int box[3] = {box_cols, box_rows, 1};
-    return make_map_nd(m, base, 3, ext, str, box, bytes);
+    return make_map_nd(m, base, 3, ext, str, box, bytes, f32);
 }
 
 template <Op OP>

@@ -366,6 +366,17 @@ __device__ __forceinline__ void tma_store_3d(const void *tmap, int x, int y, int
         : "memory");
 }
 
+// tma_store_3d that adds to what is there (the tensor map's type is fp32; one addition,
+// rounded to nearest, subnormal values kept: compared with torch's).
+__device__ __forceinline__ void tma_add_3d(const void *tmap, int x, int y, int z,
+                                           const void *smem_src) {
+    asm volatile(
+        "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], "
+        "[%4];" ::"l"(reinterpret_cast<uint64_t>(tmap)),
+        "r"(x), "r"(y), "r"(z), "r"(ptx::smem_u32(smem_src))
+        : "memory");
+}
+
 // Fetch a tensor map ahead of its first use.
 __device__ __forceinline__ void prefetch_map(const void *tmap) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");

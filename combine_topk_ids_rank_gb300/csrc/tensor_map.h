@@ -48,12 +48,13 @@ inline bool make_map(CUtensorMap *m, const void *base, long long rows, int cols,
 }
 
 // The same for `n` > 2 extents (innermost first) with the strides of all but
-// the first in elements.
+// the first in elements; of fp32 values (f32), too.
 inline bool make_map_nd(CUtensorMap *m, const void *base, int n, const long long *extent,
-                        const long long *stride, const int *box_extent, bool bytes) {
+                        const long long *stride, const int *box_extent, bool bytes,
+                        bool f32 = false) {
     EncodeTiled enc = tensor_map_encoder();
     if (enc == nullptr || n > 5) return false;
-    const int esize = bytes ? 1 : 2;
+    const int esize = bytes ? 1 : (f32 ? 4 : 2);
     cuuint64_t dims[5], strides[4];
     cuuint32_t box[5], estr[5];
     for (int i = 0; i < n; ++i) {
@@ -62,8 +63,10 @@ inline bool make_map_nd(CUtensorMap *m, const void *base, int n, const long long
         estr[i] = 1;
         if (i > 0) strides[i - 1] = (cuuint64_t)stride[i] * esize;
     }
-    return enc(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, n,
-               const_cast<void *>(base), dims, strides, box, estr,
+    const CUtensorMapDataType type = bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                           : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    return enc(m, type, n, const_cast<void *>(base), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

@@ -232,3 +232,34 @@ def test_descending_offsets_that_count_too_many_tiles(api):
     handle.forward(x, w, off, out=out)
     assert (out == 8).all()
     assert handle.get_error() == (api.MOE_OK, 0)
+
+
+@pytest.mark.parametrize("counts", [[512] * 6, [0, 1, 700, 64, 0, 1300], [40] * 80])
+@pytest.mark.parametrize("N,H", [(264, 384), (1000, 1024), (520, 200)])
+def test_weight_grad_added_to_what_is_there(api, counts, N, H):
+    """Whole and cut tiles, with and without boxes; an expert without rows keeps every bit."""
+    G, rows = len(counts), sum(counts)
+    g = gen(N)
+    x, dy = ints((rows, H), 2, g), ints((rows, N), 2, g)
+    off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=I32, device=DEV)
+    handle = api.MoeGemmRagged(G, rows, N, H, DEV)
+    start = torch.randint(-1000, 1000, (G, N, H), generator=g, device=DEV).float()
+    start[torch.tensor(counts, device=DEV) == 0] = float("nan")
+    dw = start.clone()
+    for _ in range(3):
+        handle.weight_grad(dy, x, off, out=dw, accumulate=True)
+    o = off.tolist()
+    for e in range(G):
+        if counts[e] == 0:
+            assert torch.equal(dw[e].view(I32), start[e].view(I32))
+            continue
+        one = dy[o[e]:o[e + 1]].double().T @ x[o[e]:o[e + 1]].double()
+        assert torch.equal(dw[e].double(), start[e].double() + 3 * one)
+    # normal values: one more rounding, of the sum, to the nearest
+    real = torch.randn((rows, H), generator=g, device=DEV).to(BF)
+    fresh = handle.weight_grad(dy, real, off, dtype=F32)
+    base = torch.randn((G, N, H), generator=g, device=DEV)
+    dw = base.clone()
+    handle.weight_grad(dy, real, off, out=dw, accumulate=True)
+    assert torch.equal(dw, base + fresh)
+    assert handle.get_error() == (api.MOE_OK, 0)
