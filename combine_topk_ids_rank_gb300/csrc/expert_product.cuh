@@ -283,8 +283,15 @@ struct Work {
 constexpr int kHalfCols = kMaxCols / 2;
 struct Half {
     int first, steps;
-    __device__ Half(bool turned, int cols, int h) {
+    // (grain: the first half has a multiple of so many steps, if there are as many)
+    __device__ Half(bool turned, int cols, int h, int grain = 1) {
         const int all = (cols + kStep - 1) / kStep;
+        if (grain > 1) {
+            const int n = min(all, ((all + 1) / 2 + grain - 1) / grain * grain);
+            first = h ? n : 0;
+            steps = h ? all - n : n;
+            return;
+        }
         first = turned ? h * kSteps : (h ? (all + 1) / 2 : 0);
         steps = turned ? kSteps : (h ? all / 2 : (all + 1) / 2);
     }
@@ -408,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kShift = is_fp8(OP) ? 7 : 8;
     static_assert(1 << kShift == (is_fp8(OP) ? kFp8Cols : kMaxCols), "columns of a tile");
     shape.shift = kShift;
-    shape.even = !(KRAGGED && p.boxes);
+    shape.even = !(KRAGGED && p.cols % 128 == 0);  // (every tile ends with a box)
     shape.thin = 0;
     __syncthreads();
     ptx::grid_dependency_wait();  // nothing of the caller's memory is touched before
@@ -573,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const uint32_t taddr = s_taddr;
     const int stage_bytes = kLaneBytes + col_bytes<OP>(widest);
-    const int boxes = KRAGGED && p.boxes ? kEpiWarps * kBoxBytes : 0;  // (at the end)
+    constexpr int boxes = KRAGGED ? kEpiWarps * kBoxBytes : 0;  // (at the end)
     const int stages = min(kMaxStages, (kDynamic - 1024 - boxes) / stage_bytes);
     auto a_of = [&](uint32_t s) { return smem + s * stage_bytes; };
     auto b_of = [&](uint32_t s) { return smem + s * stage_bytes + kLaneBytes; };
@@ -911,6 +918,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
         // Each warp finishes 32 lanes by half of the tile's columns by itself.
+        constexpr int kGrain = KRAGGED ? 4 : 1;  // (boxes of 64 columns)
         const int q = warp & 3, hf = warp >> 2, row = q * 32 + lane;
         Turn sq(kSegs), acc(kAccs), sc(kScaleSlots);
         const uint32_t mine = taddr + ((uint32_t)(q * 32) << 16);
@@ -936,7 +944,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Seg &sg = *sp;  // (stays there until the tile is stored)
             // this warp's steps of kStep columns of the tile, and the first one
             const auto steps_of = [&] {
-                const int n = Half(OP == kFp8 && sg.turned, sg.cols, hf).steps;
+                const int n = Half(OP == kFp8 && sg.turned, sg.cols, hf, kGrain).steps;
                 if (OP == kFp8Narrow && plan.shape.thin && q >= 2) return 0;  // no lane
                 if (OP != kFp8 || !sg.turned) return n;
                 // channels that exist, if a token of the warp does
@@ -944,7 +952,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return q * 32 < sg.cols ? min(max((chans + kStep - 1) / kStep, 0), kSteps) : 0;
             };
             const auto first_of = [&] {
-                return Half(OP == kFp8 && sg.turned, sg.cols, hf).first * kStep;
+                return Half(OP == kFp8 && sg.turned, sg.cols, hf, kGrain).first * kStep;
             };
             // Sums to the columns from `to` on (16 a step).
             const auto keep = [&](uint32_t to, const auto &sum) {
@@ -1089,16 +1097,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 // (adding nothing to what is there: left alone)
                 if (KRAGGED && p.accumulate && none) return;
-                if (KRAGGED && p.boxes && sg.whole) {
+                int done = 0;  // steps
+                if (KRAGGED && sg.whole) {
                     // Boxes of 32 rows by 128 bytes, through shared memory (128-byte swizzle),
-                    // clipped at the map's last row by the tensor map.  (Added: in L2, once for
-                    // every value, so the order of the CTAs changes nothing.)
+                    // clipped at the map's last row by the tensor map; what is no whole box goes
+                    // row by row.  (Added: in L2, once for every value, so the order of the CTAs
+                    // changes nothing.  32 groups of 512 rows, 4096 x 2048, boxes and rows: bf16
+                    // 203 and 214 us, fp32 287 and 340, added 442 and 649.)
                     uint8_t *box = smem + (kDynamic - 1024 - boxes) + warp * kBoxBytes;
                     const int y = sg.l * kLanes + rank * kTileRows + q * 32;
                     const int each = p.f32 ? 2 : 4;  // steps of a box
+                    done = steps / each * each;
                     if (y < p.lanes)
 #pragma unroll 1
-                        for (int i = 0; i < steps; i += each) {
+                        for (int i = 0; i < done; i += each) {
                             if (lane == 0) ptx::bulk_wait_read<0>();  // (the box before)
                             __syncwarp();
 #pragma unroll 1
@@ -1137,9 +1149,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 ptx::bulk_commit();
                             }
                         }
-                } else if (sg.whole) {
+                }
+                if (sg.whole) {
 #pragma unroll 1
-                    for (int i = 0; i < steps; i += 2) {
+                    for (int i = done; i < steps; i += 2) {
                         float v[2][kStep];
                         get(i, v);
                         store(n0 + i * kStep, v[0]);

@@ -39,16 +39,9 @@ cudaError_t launch_gemm_ragged_weight_grad(ProductParams p, const void *dy, cons
     if (!map_2d(&a, dy, p.M, p.lanes, 64, 64, false) ||
         !map_2d(&b, x, p.M, p.cols, 64, 64, false))
         return cudaErrorInvalidValue;
-    // Whole tiles are stored (or added) as boxes of 128 bytes by 32 rows where every tile ends
-    // with a box, else row by row from the lanes.  (32 groups of 512 rows, 4096 x 2048: bf16 203
-    // and 214 us, fp32 287 and 340, added 442 and
-    // 649.)
     p.a = dy;
     p.b = x;
-    p.boxes = p.cols % 128 == 0;
-    if (!p.boxes) out = b;
-    else if (!map_3d(&out, p.out, p.G, p.lanes, p.cols, p.f32 ? 32 : 64, kBoxRows, false,
-                     p.f32 != 0))
+    if (!map_3d(&out, p.out, p.G, p.lanes, p.cols, p.f32 ? 32 : 64, kBoxRows, false, p.f32 != 0))
         return cudaErrorInvalidValue;
     return launch<kWeightGrad>(p, a, b, out, num_sms, st);
 }

@@ -53,7 +53,6 @@ struct ProductParams {
     int lanes, cols, depth;  // extents: lanes; maps' columns (gradient of the maps); k
     int nmax;                // columns that a part has room for
     int f32, accumulate;     // gradient of the maps: type, added to what is there
-    int boxes;               // its whole tiles are stored as boxes (set by the launcher)
 };
 
 // Columns a part of the 8-bit product needs for M rows of tokens (a group of
