@@ -263,3 +263,18 @@ def test_weight_grad_added_to_what_is_there(api, counts, N, H):
     handle.weight_grad(dy, real, off, out=dw, accumulate=True)
     assert torch.equal(dw, base + fresh)
     assert handle.get_error() == (api.MOE_OK, 0)
+
+
+@pytest.mark.parametrize("H", [128, 136])
+def test_sums_below_the_smallest_normal_number_are_added(api, H):
+    """2^-140 as a product, added to 2^-140 and to nothing."""
+    off = torch.tensor([0, 64], dtype=I32, device=DEV)
+    x = torch.zeros((64, H), dtype=BF, device=DEV)
+    dy = torch.zeros((64, 256), dtype=BF, device=DEV)
+    x[0, :2] = dy[0, 0] = 2.0 ** -70
+    dw = torch.zeros((1, 256, H), device=DEV)
+    dw[0, 0, 1:3] = 2.0 ** -140
+    api.MoeGemmRagged(1, 64, 256, H, DEV).weight_grad(dy, x, off, out=dw, accumulate=True)
+    want = torch.zeros((1, 256, H), dtype=torch.float64)
+    want[0, 0, :3] = torch.tensor([1.0, 2.0, 1.0], dtype=torch.float64) * 2.0 ** -140
+    assert torch.equal(dw.double().cpu(), want)
