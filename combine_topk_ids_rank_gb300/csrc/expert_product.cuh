@@ -74,6 +74,7 @@
 #include "stream.cuh"
 #include "tcgen05.cuh"
 #include "tensor_map.h"
+#include "tiling.h"
 
 #include "moe_a2a.h"
 
@@ -81,9 +82,6 @@ namespace moe {
 namespace product {
 
 using namespace stream;
-
-enum Op { kFp8, kFp8Narrow, kForward, kInputGrad, kWeightGrad };
-constexpr bool is_fp8(Op op) { return op == kFp8 || op == kFp8Narrow; }
 
 constexpr int kEpiWarps = 8, kProducerWarp = 8, kMmaWarp = 9, kHelpWarp = 10, kListWarp = 11;
 constexpr int kThreads = 12 * 32;
@@ -93,6 +91,7 @@ constexpr int kStartRegs = 168, kEpiRegs = 200, kOtherRegs = 104;
 static_assert(kEpiWarps * 32 * kEpiRegs + (kThreads - kEpiWarps * 32) * kOtherRegs <=
                   kThreads * kStartRegs, "more registers than the block starts with");
 constexpr int kMaxCols = kProductMaxCols;
+static_assert(kTileLanes == kTileRows && kTileCols == kMaxCols, "a tile's extents");
 constexpr int kAccs = 2;                                  // accumulators of kMaxCols columns
 constexpr int kStep = 16, kSteps = kMaxCols / 2 / kStep;  // columns an epilogue warp stores at once
 constexpr int kLaneBytes = kTileRows * kAtom;             // A of a stage
@@ -114,13 +113,6 @@ constexpr int kMinPart = 4;       // blocks of k that make a part worth its way 
 constexpr long long kAheadBytes = 8 << 20;
 constexpr int kFp8Cols = 128;     // columns of an 8-bit tile that is not turned, at most
 
-constexpr int ctas_of(Op op) { return is_fp8(op) ? 1 : 2; }
-
-// Columns of the `k` tiles of `cols` columns: evened out, a multiple of 16.
-__device__ __forceinline__ int width_of(int cols, int k) {
-    return k <= 1 ? (cols + 15) / 16 * 16 : ((cols + k - 1) / k + 15) / 16 * 16;
-}
-
 // Blocks [k0, k1) of k of a tile of a pair's (a CTA's) work: channel tile l, tokens
 // (or the maps' columns) from c0 on.
 struct Seg {
@@ -128,32 +120,6 @@ struct Seg {
     int turned;                   // tokens are the lanes
     int whole, t;                 // the sum is whole; else t: the tile among the cut ones
     int p0, parts;                // (kWeightGrad)
-};
-
-// How groups are divided into tiles.
-template <Op OP>
-struct Shape {
-    static constexpr int kLanes = ctas_of(OP) * kTileRows;
-    int turn_from;  // tokens that make a group's tiles turned
-    int shift;      // columns of a tile that is not, at most: 1 << shift
-    int even;       // tiles of a group are evened out (else: full ones and what is left)
-    int thin;       // kFp8Narrow: a tile has 64 lanes only, so that few are cut
-
-    __device__ bool turned(int c) const { return OP == kFp8 && c >= turn_from; }
-    // Tiles along the channels, and along `c` tokens (or the maps' columns).
-    __device__ int ltiles(int c, int lanes) const {
-        const int l = turned(c) ? kMaxCols : (OP == kFp8Narrow && thin ? 64 : kLanes);
-        return (lanes + l - 1) / l;
-    }
-    __device__ int mtiles(int c) const {
-        return turned(c) ? (c + kTileRows - 1) / kTileRows : (c + (1 << shift) - 1) >> shift;
-    }
-    // Columns of a tile, and the tokens (or columns) from one tile to the next.
-    __device__ int width(int c) const {
-        return turned(c) ? kMaxCols : (even ? width_of(c, mtiles(c)) : min(c, 1 << shift));
-    }
-    __device__ int stride(int c) const { return turned(c) ? kTileRows : width(c); }
-    __device__ int tiles(int c, int lanes) const { return mtiles(c) * ltiles(c, lanes); }
 };
 
 // Turned tiles (kFp8).  A group with many tokens has them as the lanes, 128 a
@@ -433,8 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         plan.count[g] = c;
         plan.order[g] = (uint16_t)g;
         most = max(most, c);
-        sums[0] += shape.tiles(KRAGGED ? p.cols : c, p.lanes);
-        for (int i = 1; i < 4; ++i) sums[i] += (c + (128 >> (i - 1)) - 1) >> (8 - i);
+        add_tiles(sums, shape, c, KRAGGED ? p.cols : c, p.lanes);
     }
     // (groups that this warp has none of leave the sums as they are)
     if (warp * 32 < p.G) {
@@ -449,34 +414,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     // the pair's barriers are set up before either arrives on the other's
     if (PAIR) ptx::cluster_arrive();
-    // Offsets that descend may repeat rows, and so count more tiles than 32 bits hold: then
-    // there is no work at all.  (Others stay below the host's limit.)
-    int tiles = plan.sums[0];
-    if (!KRAGGED && p.offsets != nullptr &&
-        (long long)p.G * shape.tiles(p.M, p.lanes) >= 1 << 29) {
-        bool down = false;
+    bool repeats = false;
+    if (p.offsets != nullptr && could_repeat_too_many(shape, p.G, p.M, p.lanes)) {
         for (int g = tid; g < p.G; g += kThreads)
-            down = down || __ldg(p.offsets + g + 1) < __ldg(p.offsets + g);
-        if (__syncthreads_or(down)) tiles = 0;
+            repeats = repeats || __ldg(p.offsets + g + 1) < __ldg(p.offsets + g);
+        repeats = __syncthreads_or(repeats);
     }
-    // Few tiles: narrower ones while each still finds an idle pair (333 x 1000 x 1040 in
-    // 8 bits: 12 turned tiles of nine blocks, or 56 of 48 columns).
-    if (!KRAGGED && tiles * 2 <= pairs) {
-        const int l = (p.lanes + kLanes - 1) / kLanes;
-        for (int i = 1; i < 4; ++i)
-            if (plan.sums[i] * l <= pairs) {
-                shape.turn_from = INT32_MAX;
-                shape.shift = 8 - i;
-                tiles = plan.sums[i] * l;
-            }
-    }
-    // 8-bit, fewer tiles than half the SMs: of 64 lanes instead of cut ones (one SM can
-    // take more than its share of the memory's rate, and no part goes through memory;
-    // 16 x 7168 x 4096: 13.0 us, 14.3 with 128 lanes)
-    if (OP == kFp8Narrow && tiles * 2 <= pairs) {
-        shape.thin = 1;
-        tiles = plan.sums[8 - shape.shift] * ((p.lanes + 63) / 64);
-    }
+    const int tiles = settle(shape, plan.sums, repeats, pairs, p.lanes);
     // the widest tile decides how many stages the ring has
     const int blocks = KRAGGED ? 0 : (p.depth + kBlock - 1) / kBlock;
     int widest = max(16, KRAGGED ? shape.width(p.cols)

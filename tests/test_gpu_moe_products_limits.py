@@ -1,0 +1,71 @@
+"""The experts' products at the ends of what their entry points take: offsets that
+descend, very long sums."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+DEV = "cuda:0"
+BF, F8, F32, I32 = torch.bfloat16, torch.float8_e4m3fn, torch.float32, torch.int32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from combine_topk_ids_rank_gb300 import build_lib
+    build_lib.build()
+
+
+@pytest.fixture(scope="module")
+def api():
+    from combine_topk_ids_rank_gb300 import moe_a2a
+    return moe_a2a
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def offsets(values):
+    return torch.tensor(values, dtype=I32, device=DEV)
+
+
+def untouched(t, value):
+    return all((part == value).all() for part in t.split(1 << 20))
+
+
+# (tests/test_moe_tiling.py goes through the counts of these offsets)
+def test_descending_offsets_whose_tiles_wrap_to_a_few(api):
+    G, M, N, H = 1024, (1 << 28) + 1, 8, 8
+    off = offsets([0] + [1 << 28, 0] * 500 + [M, 0] * 12)
+    x = torch.ones((M, H), dtype=BF, device=DEV)
+    out = torch.full((M, N), 7.0, dtype=BF, device=DEV)
+    w = torch.ones((G, N, H), dtype=BF, device=DEV)
+    handle = api.MoeGemmRagged(G, M, N, H, DEV)
+    handle.forward(x, w, off, out=out)
+    assert untouched(out, 7)
+    handle.input_grad(x, w, off, out=out)
+    assert untouched(out, 7)
+    handle.forward(x, w, off.sort()[0], out=out)         # the call after it works
+    assert untouched(out, 8)
+    assert handle.get_error() == (api.MOE_OK, 0)
+
+
+def test_descending_offsets_of_the_narrow_eight_bit_product(api):
+    G, M, N, H = 1024, 48000, 180000, 16
+    off = offsets([M if g % 2 else 0 for g in range(G + 1)])
+    xq = torch.ones((M, H), device=DEV).to(F8)
+    sx = torch.ones((M, 1), device=DEV)
+    wq = torch.ones((1, 1, 1), device=DEV).to(F8).view(torch.uint8).expand(G, N, H).contiguous()
+    sw = torch.ones((G, (N + 127) // 128, 1), device=DEV)
+    out = torch.full((M, N), 7.0, dtype=BF, device=DEV)
+    handle = api.MoeGemmFp8(G, M, N, H, DEV)
+    handle.gemm(xq, sx, wq, sw, offsets=off, out=out)
+    assert all((part == 7).all() for part in out.split(4000))
+    few = torch.zeros_like(off)
+    few[1:] = 40                                         # ascending ones
+    handle.gemm(xq, sx, wq, sw, offsets=few, out=out)
+    assert (out[:40] == 16).all() and (out[40:4000] == 7).all()
+    assert handle.get_error() == (api.MOE_OK, 0)
