@@ -105,6 +105,9 @@ constexpr int kDynamic = 193 * 1024;                      // 227 KB less the sta
 constexpr int kBoxRows = 32, kBoxBytes = kBoxRows * kAtom;  // an output box of an epilogue warp
 constexpr int kClasses = 64;
 constexpr int kGradRun = 8;       // blocks of 64 rows of k that stay in tensor memory
+// Blocks of k of the longest tile for which a wait for whole tiles has one limit of kWaitNs
+// (kSegs + 1 tiles at 4 us a block; a block takes 0.2 to 0.7 us).
+constexpr int kWaitBlocks = 25000;
 constexpr int kMinPart = 4;       // blocks of k that make a part worth its way through memory
 // kWeightGrad: a group's rows of up to this many bytes are fetched into L2 when its first
 // tile is listed: all pairs come to a group at the same time, and then wait for memory.
@@ -533,9 +536,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_after_sync();
     // rows of k of a block (kWeightGrad: fewer than 64 in a group's last one)
     auto rows_of = [&](int g, int kb) { return KRAGGED ? min(64, plan.count[g] - kb * 64) : 64; };
-    // the listed tiles in turn: waits for the next one, null behind the last (or on failure)
-    const auto listed = [&](const Turn &sq) -> const Seg * {
-        if (!ptx::mbar_park(&seg_full[sq.at], sq.parity, kWaitNs)) {
+    // A wait for as long as tiles take: for a free place in the list and for a tile that
+    // comes to stand there, and the help warp's for a last block, since it passes over the
+    // others.  As many limits as their length asks for.  (The other products' tiles of all
+    // of k end within the limit: k of all groups together has 32 bits, and fewer tiles than
+    // pairs are cut.)
+    const auto park_tiles = [&](uint64_t *bar, uint32_t parity) {
+        for (int i = KRAGGED ? plan.most_tokens / (64 * kWaitBlocks) : 0; i >= 0; --i) {
+            if (ptx::mbar_park(bar, parity, kWaitNs)) return true;
+            if (s_failed) break;
+        }
+        return false;
+    };
+    // the listed tiles in turn: waits for the next one, null behind the last (or on failure).
+    // `far`: by a warp that may be ahead of the epilogue.
+    const auto listed = [&](const Turn &sq, bool far) -> const Seg * {
+        uint64_t *bar = &seg_full[sq.at];
+        if (!(far ? park_tiles(bar, sq.parity) : ptx::mbar_park(bar, sq.parity, kWaitNs))) {
             s_failed = 1;
             return nullptr;
         }
@@ -568,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             prefetch_share(static_cast<const char *>(p.b) + at * b, n * b);
                         }
                     }
-                    if (!ptx::mbar_park(&seg_free[sq.at], sq.parity ^ 1u, kWaitNs)) {
+                    if (!park_tiles(&seg_free[sq.at], sq.parity ^ 1u)) {
                         s_failed = 1;
                         break;
                     }
@@ -588,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         Seg next;
                         next.g = -1;
                         const bool more = !s_failed && work.next(p, next);
-                        if (!ptx::mbar_park(&seg_free[sq.at], sq.parity ^ 1u, kWaitNs)) {
+                        if (!park_tiles(&seg_free[sq.at], sq.parity ^ 1u)) {
                             s_failed = 1;
                             break;
                         }
@@ -597,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         sp = more ? &segs[sq.at] : nullptr;
                         sq.next();
                     } else {
-                        sp = s_failed ? nullptr : listed(sq);
+                        sp = s_failed ? nullptr : listed(sq, true);
                     }
                     if (sp == nullptr) break;
                     const Seg sg = *sp;
@@ -710,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (PAIR) tc::commit_pair(bar);
                     else tc::commit(bar);
                 };
-                while (const Seg *sp = s_failed ? nullptr : listed(sq)) {
+                while (const Seg *sp = s_failed ? nullptr : listed(sq, true)) {
                     const Seg &sg = *sp;
                     const int k0 = sg.k0, k1 = sg.k1;
                     if constexpr (is_fp8(OP)) {
@@ -781,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t parity = 0;
             Turn sc(kScaleSlots);     // (kFp8)
             while (ok) {
-                const Seg *sp = listed(sq);
+                const Seg *sp = listed(sq, true);
                 if (__any_sync(0xffffffffu, sp == nullptr)) break;
                 const Seg sg = *sp;
                 __syncwarp();
@@ -838,8 +855,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int kb = sg.k0; kb < sg.k1; ++kb, st.next()) {
                         const int rows = rows_of(sg.g, kb);
                         if (rows == 64) continue;
-                        ok = __all_sync(0xffffffffu, ptx::mbar_park(&tail[st.at],
-                                                                    parity >> st.at & 1u, kWaitNs));
+                        ok = __all_sync(0xffffffffu,
+                                        park_tiles(&tail[st.at], parity >> st.at & 1u));
                         if (!ok) {
                             s_failed = 1;
                             break;
@@ -883,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             acc.next();
         };
         for (;;) {
-            const Seg *const sp = listed(sq);
+            const Seg *const sp = listed(sq, false);
             if (__any_sync(0xffffffffu, sp == nullptr)) break;
             const Seg &sg = *sp;  // (stays there until the tile is stored)
             // this warp's steps of kStep columns of the tile, and the first one

@@ -69,3 +69,32 @@ def test_descending_offsets_of_the_narrow_eight_bit_product(api):
     handle.gemm(xq, sx, wq, sw, offsets=few, out=out)
     assert (out[:40] == 16).all() and (out[40:4000] == 7).all()
     assert handle.get_error() == (api.MOE_OK, 0)
+
+
+@pytest.mark.parametrize("G,big,each", [(40, (1 << 29) + 17, 3), (400, (1 << 29) + 17, 3),
+                                        (400, 1 << 29, 64)])
+def test_weight_grad_of_a_tile_that_takes_seconds(api, G, big, each):
+    """All rows but a few in one group, whose tile is not cut (40 tiles), or has others
+    behind it (400), with and without a last block that is not full: the waits for it go
+    past their usual limit."""
+    N, H = 8, 8
+    counts = [each] * G
+    counts[3] = big
+    off = [0]
+    for c in counts:
+        off.append(off[-1] + c)
+    M = off[-1]
+    g = gen(G)
+    # most rows hold zeros, so the sums are exact
+    x, dy = torch.zeros((M, H), dtype=BF, device=DEV), torch.zeros((M, N), dtype=BF, device=DEV)
+    at = torch.randint(M, (2000,), generator=g, device=DEV)
+    at = torch.cat([at, torch.arange(3 * G, device=DEV), M - 1 - torch.arange(3 * G, device=DEV)])
+    for t in (x, dy):
+        t[at] = torch.randint(-2, 3, (len(at), 8), generator=g, device=DEV).to(BF)
+    handle = api.MoeGemmRagged(G, M, N, H, DEV)
+    dw = handle.weight_grad(dy, x, offsets(off), dtype=F32)
+    assert handle.get_error() == (api.MOE_OK, 0)
+    live = at.unique()
+    for e in range(G):
+        rows = live[(live >= off[e]) & (live < off[e + 1])]
+        assert torch.equal(dw[e].double(), dy[rows].double().T @ x[rows].double())
