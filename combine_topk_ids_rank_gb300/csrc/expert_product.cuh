@@ -33,9 +33,11 @@
 //        2000 cycles); 8-bit: issues the products of the second half.
 // Sums.  The tensor cores add in fp32 with truncation (measured on bf16 normal
 // values against 64 bits: 4.7e-7 of the result's norm after 512 products, 2.1e-6
-// after 2048, 9.1e-6 after 8192), so what is kept in 32 bits (kWeightGrad) leaves
-// tensor memory every 512 rows of k and is summed to nearest in registers.  The
-// 8-bit product leaves it every 128 codes, where its scales change.  Two
+// after 2048, 9.1e-6 after 8192; products of one sign lose 3.5e-5 after 8192 and 7.9e-4
+// after 131072), so what is kept in 32 bits (kWeightGrad) leaves tensor memory every 512
+// rows of k and is summed to nearest in registers, and what is rounded to bf16 at the
+// end (kForward, kInputGrad) every 8192, where the loss is a hundredth of that rounding.
+// The 8-bit product leaves it every 128 codes, where its scales change.  Two
 // accumulators of 256 columns take turns meanwhile.
 //
 // Split.  Whole waves of tiles go round robin, those with the most work first.
@@ -105,6 +107,7 @@ constexpr int kDynamic = 193 * 1024;                      // 227 KB less the sta
 constexpr int kBoxRows = 32, kBoxBytes = kBoxRows * kAtom;  // an output box of an epilogue warp
 constexpr int kClasses = 64;
 constexpr int kGradRun = 8;       // blocks of 64 rows of k that stay in tensor memory
+constexpr int kRowRun = 128;      // (kForward, kInputGrad) blocks of 64 of k that do
 // Blocks of k of the longest tile for which a wait for whole tiles has one limit of kWaitNs
 // (kSegs + 1 tiles at 4 us a block; a block takes 0.2 to 0.7 us).
 constexpr int kWaitBlocks = 25000;
@@ -321,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kBlock = is_fp8(OP) ? kAtom : kAtom / 2;  // extent of k in a stage
     constexpr int kScaleFloats = is_fp8(OP) ? kScaleSlots * kScaleRun * kFp8Cols : 4;
     // blocks of k whose products one accumulator takes
-    constexpr int kRun = is_fp8(OP) ? 1 : (OP == kWeightGrad ? kGradRun : INT32_MAX);
+    constexpr int kRun = is_fp8(OP) ? 1 : (OP == kWeightGrad ? kGradRun : kRowRun);
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(16) float s_scale[kScaleFloats];
     // (pairs.  full, acc_free: CTA 0's, both CTAs arrive; empty, acc_full: either's own)
@@ -1359,7 +1362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             } else {
                 const int steps = steps_of(), n0 = first_of(), k0 = sg.k0, k1 = sg.k1;
-                if (!KRAGGED || k1 - k0 <= kRun) {  // all of k in one accumulator, or nothing
+                if (k1 - k0 <= kRun) {  // all of k in one accumulator, or nothing
                     if (k0 < k1) wait_for(&acc_full[acc.at][0], acc.parity);
                     tc::fence_after_sync();
                 } else {

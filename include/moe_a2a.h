@@ -630,7 +630,8 @@ int moe_gemm_fp8(const void *d_xq, const float *d_x_scale, const void *d_wq,
  *   moe_gemm_ragged_weight_grad: dW_e[n][h] = sum_m dy[m][n] * x[m][h],
  *                                bf16 (fp32 = 0) or fp32, or (accumulate, fp32
  *                                only) added to what d_dw holds
- * bf16 operands, fp32 sums.  Rows of no expert are not written (and take no
+ * bf16 operands, fp32 sums: as the tensor cores add (by truncation) over up to 8192 terms,
+ * 512 for the weight gradient, and to nearest from there.  Rows of no expert are not written (and take no
  * part in dW); the dW of an expert without rows is zero.
  *   hidden  a multiple of 8; N any, a multiple of 8 for the gradients;
  *           groups <= 1024; limits as for moe_gemm_fp8 (the input gradient sums over

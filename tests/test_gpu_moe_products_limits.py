@@ -98,3 +98,55 @@ def test_weight_grad_of_a_tile_that_takes_seconds(api, G, big, each):
     for e in range(G):
         rows = live[(live >= off[e]) & (live < off[e + 1])]
         assert torch.equal(dw[e].double(), dy[rows].double().T @ x[rows].double())
+
+
+def one_sided(shape, g):
+    return torch.rand(shape, generator=g, device=DEV) + 0.5
+
+
+@pytest.mark.parametrize("way", ["forward", "input_grad"])
+def test_long_sums_of_one_sign_are_not_biased(api, way):
+    """As many tiles as pairs of 256 x 256 tiles' CTAs, so that none is cut along k.
+
+    Truncating additions lose at most 2^-23 of the sum so far each: over 8192 terms that
+    grow it evenly, 8192 * 2^-23 / 2 = 4.9e-4 of it.  (Without an end, 2^18 terms lost
+    1.6e-3.)  The sums of those to nearest are 32 roundings of 2^-24.  The rounding to bf16,
+    of outputs spread over a factor of four, is up or down by 2^-8 at most; the mean of n
+    such is below 6 * 2^-8 / sqrt(3 n)."""
+    k, lanes, M = (1 << 18) + 8, 76 * 256, 16
+    g = gen(k)
+    x = one_sided((M, k), g).to(BF)
+    scale = 1 + torch.rand(lanes, generator=g, device=DEV)
+    shape = (1, lanes, k) if way == "forward" else (1, k, lanes)
+    w = torch.empty(shape, dtype=BF, device=DEV)
+    maps = w[0] if way == "forward" else w[0].T          # [lanes, k]
+    want = torch.empty((M, lanes), dtype=torch.float64, device=DEV)
+    for i in range(0, lanes, 256):
+        part = (one_sided((256, k), g) * scale[i:i + 256, None]).to(BF)
+        maps[i:i + 256] = part
+        want[:, i:i + 256] = x.double() @ part.double().T
+    handle = api.MoeGemmRagged(1, M, lanes if way == "forward" else k,
+                               k if way == "forward" else lanes, DEV)
+    got = getattr(handle, way)(x, w, offsets([0, M])).double()
+    assert handle.get_error() == (api.MOE_OK, 0)
+    off = (got - want) / want
+    lost = 8192 * 2.0 ** -23 / 2 + 32 * 2.0 ** -24
+    assert off.abs().max() <= lost + 2.0 ** -8
+    assert abs(off.mean()) <= lost + 6 * 2.0 ** -8 / (3 * off.numel()) ** 0.5
+
+
+@pytest.mark.parametrize("lanes", [40, 256, 1000])
+@pytest.mark.parametrize("k", [8192, 8200, 16384, 1 << 20])
+def test_long_sums_of_integers(api, k, lanes):
+    """Exact in fp32 (below 2^24), with parts that leave tensor memory once and more often."""
+    off = offsets([0, 5, 5, 305])
+    g = gen(k + lanes)
+    three = lambda *s: torch.randint(-1, 2, s, generator=g, device=DEV, dtype=torch.int8).to(BF)
+    x, w = three(305, k), three(3, lanes, k)
+    up, down = (api.MoeGemmRagged(3, 305, n, h, DEV) for n, h in ((lanes, k), (k, lanes)))
+    turned = w.transpose(1, 2).contiguous()              # [3, k, lanes]
+    y, dx = up.forward(x, w, off), down.input_grad(x, turned, off)
+    for e, (a, b) in enumerate(((0, 5), (5, 5), (5, 305))):
+        want = (x[a:b].double() @ w[e].double().T).to(BF)
+        assert torch.equal(y[a:b], want) and torch.equal(dx[a:b], want)
+    assert up.get_error() == down.get_error() == (api.MOE_OK, 0)
