@@ -108,9 +108,9 @@ constexpr int kBoxRows = 32, kBoxBytes = kBoxRows * kAtom;  // an output box of 
 constexpr int kClasses = 64;
 constexpr int kGradRun = 8;       // blocks of 64 rows of k that stay in tensor memory
 constexpr int kRowRun = 128;      // (kForward, kInputGrad) blocks of 64 of k that do
-// Blocks of k of the longest tile for which a wait for whole tiles has one limit of kWaitNs
-// (kSegs + 1 tiles at 4 us a block; a block takes 0.2 to 0.7 us).
-constexpr int kWaitBlocks = 25000;
+// What a block of k takes at most, with much to spare (0.2 to 0.7 us): the limit of waits
+// for whole tiles.
+constexpr uint64_t kBlockNs = 4000;
 constexpr int kMinPart = 4;       // blocks of k that make a part worth its way through memory
 // kWeightGrad: a group's rows of up to this many bytes are fetched into L2 when its first
 // tile is listed: all pairs come to a group at the same time, and then wait for memory.
@@ -541,15 +541,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto rows_of = [&](int g, int kb) { return KRAGGED ? min(64, plan.count[g] - kb * 64) : 64; };
     // A wait for as long as tiles take: for a free place in the list and for a tile that
     // comes to stand there, and the help warp's for a last block, since it passes over the
-    // others.  As many limits as their length asks for.  (The other products' tiles of all
-    // of k end within the limit: k of all groups together has 32 bits, and fewer tiles than
-    // pairs are cut.)
+    // others.  (The other products' tiles of all of k end within kWaitNs: k of all groups
+    // together has 32 bits, and fewer tiles than pairs are cut.)
+    const uint64_t tiles_ns =
+        kWaitNs + (KRAGGED ? (uint64_t)plan.most_tokens / 64 * kBlockNs * (kSegs + 1) : 0);
     const auto park_tiles = [&](uint64_t *bar, uint32_t parity) {
-        for (int i = KRAGGED ? plan.most_tokens / (64 * kWaitBlocks) : 0; i >= 0; --i) {
-            if (ptx::mbar_park(bar, parity, kWaitNs)) return true;
-            if (s_failed) break;
-        }
-        return false;
+        return ptx::mbar_park(bar, parity, tiles_ns, &s_failed);
     };
     // the listed tiles in turn: waits for the next one, null behind the last (or on failure).
     // `far`: by a warp that may be ahead of the epilogue.

@@ -71,9 +71,11 @@ __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
 
 // mbar_wait_timed whose probes suspend the warp in hardware for up to kParkNs
 // (it wakes when the phase completes) instead of coming back at once: probes
-// go through the queue that the working warps' loads, stores and shuffles use.
+// go through the queue that the working warps' loads, stores and shuffles use.  Gives up
+// early where *failed is set.
 constexpr uint32_t kParkNs = 20000;
-__device__ __forceinline__ bool mbar_park(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
+__device__ __forceinline__ bool mbar_park(uint64_t *bar, uint32_t parity, uint64_t limit_ns,
+                                          const volatile int *failed = nullptr) {
     auto probe = [&] {
         uint32_t done;
         asm volatile(
@@ -90,7 +92,7 @@ __device__ __forceinline__ bool mbar_park(uint64_t *bar, uint32_t parity, uint64
     for (;;) {
         for (int i = 0; i < 4; ++i)
             if (probe()) return true;
-        if (globaltimer_ns() - t0 > limit_ns) return false;
+        if (globaltimer_ns() - t0 > limit_ns || (failed != nullptr && *failed)) return false;
     }
 }
 
