@@ -777,7 +777,9 @@ class MoeGemmRagged(_Scratch):
     expert after another, and its gradients, with the scratch memory they need.
     offsets: int32 [G + 1] on the device, expert e has rows offsets[e] to
     offsets[e + 1]; rows of no expert are left alone (undefined in a new
-    tensor).  One call at a time: calls in stream order."""
+    tensor).  One call at a time: calls in stream order.  Autograd does not
+    follow these calls: the gradients are called for, and forward refuses
+    tensors that expect a history."""
 
     def __init__(self, groups: int, max_rows: int, N: int, hidden: int, device=None):
         self.groups, self.max_rows, self.N, self.hidden = groups, max_rows, N, hidden
@@ -807,7 +809,13 @@ class MoeGemmRagged(_Scratch):
         return out
 
     def forward(self, x, w, offsets, out=None, stream=None):
-        """x bf16 [rows, H], w bf16 [G, N, H] -> out bf16 [rows, N]."""
+        """x bf16 [rows, H], w bf16 [G, N, H] -> out bf16 [rows, N].  Under
+        torch.no_grad(), or in a torch.autograd.Function, x and w may require
+        gradients; elsewhere that is an error."""
+        if (getattr(x, "requires_grad", False) or getattr(w, "requires_grad", False)) and \
+                _torch.is_grad_enabled():
+            raise ValueError("forward returns no history: call it under torch.no_grad(), and "
+                             "input_grad and weight_grad for the gradients")
         G, N, H = self.groups, self.N, self.hidden
         rows = self._rows(x, H, "x", offsets, "moe_gemm_ragged")
         _expect(w, _torch.bfloat16, (G, N, H), self.device, "w")

@@ -1,5 +1,5 @@
 """The experts' products at the ends of what their entry points take: offsets that
-descend, very long sums."""
+descend, very long sums, tensors that require gradients."""
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -150,3 +150,40 @@ def test_long_sums_of_integers(api, k, lanes):
         want = (x[a:b].double() @ w[e].double().T).to(BF)
         assert torch.equal(y[a:b], want) and torch.equal(dx[a:b], want)
     assert up.get_error() == down.get_error() == (api.MOE_OK, 0)
+
+
+def test_tensors_that_require_gradients(api):
+    """forward refuses them where autograd expects a history, and works in a function of
+    its own, whose gradients are the class's."""
+    N, H = 24, 40
+    off = offsets([0, 9, 9, 79])
+    g = gen(2)
+    ints = lambda *s: torch.randint(-2, 3, s, generator=g, device=DEV).to(BF)
+    x, w, dy = ints(79, H).requires_grad_(), ints(3, N, H).requires_grad_(), ints(79, N)
+    handle = api.MoeGemmRagged(3, 79, N, H, DEV)
+
+    class Map(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, w):
+            ctx.save_for_backward(x, w)
+            return handle.forward(x, w, off)
+
+        @staticmethod
+        def backward(ctx, dy):
+            x, w = ctx.saved_tensors
+            return handle.input_grad(dy, w, off), handle.weight_grad(dy, x, off)
+
+    for tensors in ((x, w.detach()), (x.detach(), w)):
+        with pytest.raises(ValueError, match="no history"):
+            handle.forward(*tensors, off)
+    with torch.no_grad():
+        y = handle.forward(x, w, off)
+    z = Map.apply(x, w)
+    z.backward(dy)
+    assert torch.equal(y, z) and z.requires_grad and not y.requires_grad
+    a, b, d = x.detach().double(), w.detach().double(), dy.double()
+    for e, (i, j) in enumerate(((0, 9), (9, 9), (9, 79))):
+        assert torch.equal(y[i:j], (a[i:j] @ b[e].T).to(BF))
+        assert torch.equal(x.grad[i:j], (d[i:j] @ b[e]).to(BF))
+        assert torch.equal(w.grad[e], (d[i:j].T @ a[i:j]).to(BF))
+    assert handle.get_error() == (api.MOE_OK, 0)
