@@ -187,3 +187,22 @@ def test_tensors_that_require_gradients(api):
         assert torch.equal(x.grad[i:j], (d[i:j] @ b[e]).to(BF))
         assert torch.equal(w.grad[e], (d[i:j].T @ a[i:j]).to(BF))
     assert handle.get_error() == (api.MOE_OK, 0)
+
+
+def test_fp32_weight_gradient_of_many_rows(api):
+    """40 tiles, none of them cut, over 32768 rows of normal values.
+
+    A run of 512 rows is 32 additions of the tensor cores, each of which loses at most
+    2^-23 of what is there, which has grown with the root of their number: 2/3 * 32 * 2^-23
+    = 2.6e-6 of the run's norm.  The 64 runs are added to nearest, at most 2^-24 each time:
+    2/3 * 64 * 2^-24 = 2.6e-6.  Both are below 2^-17 = 7.6e-6; sums that stay in the tensor
+    cores for all rows lose 1.1e-9 a row, 3.6e-5."""
+    rows, N, H = 32768, 2048, 1280
+    g = gen(5)
+    x = torch.randn((rows, H), generator=g, device=DEV).to(BF)
+    dy = torch.randn((rows, N), generator=g, device=DEV).to(BF)
+    handle = api.MoeGemmRagged(1, rows, N, H, DEV)
+    dw = handle.weight_grad(dy, x, offsets([0, rows]), dtype=F32)[0].double()
+    want = dy.double().T @ x.double()
+    assert (dw - want).norm() <= 2.0 ** -17 * want.norm()
+    assert handle.get_error() == (api.MOE_OK, 0)
