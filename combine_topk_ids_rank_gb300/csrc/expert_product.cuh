@@ -46,22 +46,27 @@
 // go through memory; the CTA that finishes last adds them in ascending k, so the
 // order of the additions does not depend on timing.
 //
-// Bounds (device time of calls in a row, at 2.07 GHz or the power cap).
-//   kFp8, 8192 x 4096 x 7168: 195 us, 2460 TFLOP/s.  The products alone take 154 us,
-//     with the epilogue's reads and meetings 182: the rest is its 256 additions a block
-//     and SM sub-partition, which wait for reads and barriers in between.  Pairs of CTAs:
-//     337 us; reads in flight beside the additions: 197; each lane storing its own row: 210.
+// Bounds (device time of ten calls in a row; "stream": of thousands, which come to the power
+// cap; operands of the calls of less than 20 us stand in L2, "cold": weights that do not).
+//   kFp8, 8192 x 4096 x 7168: 195 us, 2460 TFLOP/s; stream 210.  The products alone take 154 us
+//     (126 at the rate), with the epilogue's reads and meetings 182; its 256 additions a block
+//     and SM sub-partition are the rest.  What holds the products themselves is not measured.
+//     Pairs of CTAs: 337 us; reads in flight beside the additions: 197; each lane storing its
+//     own row: 210.
 //   kFp8, 32 planes of up to 1024 rows (12388 in all), 4096 x 2048: 125 us (57 at the memory's
 //     rate): tiles of 16 blocks, 15% of their rows empty; lanes storing their own rows: 139.
-//   kFp8Narrow, 16 x 7168 x 4096: 13.0 us (4.4): 2 us to the first load, DRAM latency, the
-//     last reads.  333 x 1000 x 1040: 9.6 us; with turned tiles 13.
+//     (104, stream 107, with 9559 rows in all.)
+//   kFp8Narrow, 16 x 7168 x 4096: 13.0 us, cold 13.8 (4.4): 2 us to the first load, the
+//     chain along k, the last reads.  333 x 1000 x 1040: 9.6 us; with turned tiles 13.
 //   kForward, 16384 rows of 32 groups, 4096 x 2048: one group 150 us (1840 TFLOP/s, the
 //     power cap), even groups 162, uneven ones 186 (1480 TFLOP/s; 570 cycles a block where
 //     the products need 420 on average: about 50 bytes a cycle and SM come from L2).
 //     kInputGrad: 145, 171 and 183.  Prefetching weights into L2: 197.
-//   kForward, 8 rows of 128 groups, 1536 x 2048: 12 us (7.4).
-//   kWeightGrad, the same 16384 rows: 162, 187 and 215 us (537 MB of output), fp32 278, added to
-//     fp32 448 (2.15 GB, 317 at the copy's rate; each lane adding to its own row: 700):
+//     Uneven ones in a stream: 202 and 203.
+//   kForward, 8 rows of 128 groups, 1536 x 2048: 11.5 to 12 us, cold 14.0 (7.4).
+//   kWeightGrad, the same 16384 rows: 162, 187 and 215 to 220 us, stream 226 to 235
+//     (537 MB of output), fp32 278, added to fp32 448 (2.15 GB, 317 at the copy's
+//     rate; each lane adding to its own row: 700):
 //     even tiles have eight blocks at 0.87 of the dense rate; tiles of less than six wait
 //     for the memory that takes their outputs.  Groups large and small in turn: 214 to 219.
 #pragma once
@@ -114,6 +119,8 @@ constexpr uint64_t kBlockNs = 4000;
 constexpr int kMinPart = 4;       // blocks of k that make a part worth its way through memory
 // kWeightGrad: a group's rows of up to this many bytes are fetched into L2 when its first
 // tile is listed: all pairs come to a group at the same time, and then wait for memory.
+// (Each CTA fetches its share of the grid, if it has a tile of the group: of a group with
+// fewer tiles than pairs a part only.)
 // (32 groups of 512 rows, 6 MB each: 187 us, 196 without; uneven groups up to 18 MB: 215 us,
 // 216 without, 218 with those above 8 MB too.)
 constexpr long long kAheadBytes = 8 << 20;

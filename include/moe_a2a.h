@@ -640,8 +640,8 @@ int moe_gemm_fp8(const void *d_xq, const float *d_x_scale, const void *d_wq,
  *   d_x bf16 [rows][hidden], d_dy bf16 [rows][N], d_w bf16 [groups][N][hidden]:
  *           16-byte aligned; d_out, d_dx bf16; d_dw 16-byte aligned.  Outputs
  *           overlap no input.
- *   d_scratch at least moe_gemm_ragged_scratch_bytes() bytes, as for
- *           moe_gemm_int8
+ *   d_scratch at least moe_gemm_ragged_scratch_bytes() bytes (50 MB, whatever the sizes:
+ *           one buffer may serve any calls that do not overlap), as for moe_gemm_int8
  * Each queues one kernel on `stream` (the weight gradient of no rows a memset). */
 size_t moe_gemm_ragged_scratch_bytes(void);
 
